@@ -13,6 +13,7 @@ Typical use (all tensors on one CUDA device, bf16 [B, H, N, d]):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -26,6 +27,8 @@ __all__ = [
     "permute", "sparse_attn", "sparse_attention", "check_device_errors", "workspace_sizes",
     "SvooError", "CLUSTER_WARM", "CLUSTER_IDENTITY", "PSA_INF", "psa_config", "psa_params",
     "psa_mask", "psa_attention", "snr_top_p", "cluster_outputs",
+    "BlockConfig", "BlockShape", "block_pool", "block_select", "block_attn", "block_attn_backward",
+    "block_attention", "cache_attn", "cache_evict",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +45,11 @@ class Shape(ctypes.Structure):
                 ("n_text", ctypes.c_int)]
 
 
+class BlockShape(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("B", "H", "Hkv", "Nq", "Nk", "cap", "d", "block", "n_sel",
+                                            "sink", "local", "causal", "q_start")]
+
+
 _PLAN_FIELDS = ["kmask", "q_label", "q_sizes", "stats", "q_perm", "q_off", "k_perm", "k_off",
                 "tiles", "tile_count", "units", "unit_count"]
 
@@ -56,6 +64,7 @@ _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _SP = ctypes.POINTER(Shape)
 _PP = ctypes.POINTER(_CPlan)
+_BP = ctypes.POINTER(BlockShape)
 
 _SIGS = {
     "svoo_status_string": (ctypes.c_char_p, [_I]),
@@ -73,6 +82,15 @@ _SIGS = {
     "svoo_psa_block_count": (_I, [_I, _I, _I, _I, _I, _I]),
     "svoo_psa_mask": (_I, [_SP, _I, _I, _I, _I, _I, _I, _P, _I, _PP, _P, _P, _P]),
     "svoo_snr_top_p": (_I, [_I, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P]),
+    "svoo_block_pool": (_I, [_BP, _P, _P, _I, _P, _P]),
+    "svoo_block_select": (_I, [_BP, _P, _P, _P, _P, _P]),
+    "svoo_block_attn": (_I, [_BP, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P]),
+    "svoo_block_attn_backward_workspace_size": (_SZ, [_BP]),
+    "svoo_block_attn_backward": (_I, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _SZ, _P, _P]),
+    "svoo_cache_attn_workspace_size": (_SZ, [_BP, _I, _I]),
+    "svoo_cache_attn": (_I, [_BP, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _SZ, _P, _P]),
+    "svoo_cache_evict_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "svoo_cache_evict": (_I, [_I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -446,3 +464,254 @@ def snr_top_p(steps: int, warmup: int = 0, p_min: float = 0.7, tau: float = 0.99
     _check(load().svoo_snr_top_p(int(steps), int(warmup), float(p_min), float(tau), float(shift),
                                  p.ctypes.data_as(ctypes.c_void_p)), "svoo_snr_top_p")
     return p
+
+
+# --------------------------------------------------------------------------- block-selected attention
+
+
+@dataclasses.dataclass
+class BlockConfig:
+    """How every query selects its key blocks (see svoo_block_shape in include/svoo.h)."""
+    block: int = 64                # keys per block: a multiple of 64 up to 1024
+    n_sel: int = 16                # blocks per query, forced ones included
+    sink: int = 1                  # the first blocks, kept by every query
+    local: int = 1                 # causal: the query's own block and the local - 1 before it
+    causal: bool = True            # when False, local must be 0
+    scale: Optional[float] = None  # default 1/sqrt(d)
+
+
+def _on_device(t: torch.Tensor):
+    """The call's device made current for the launch (nothing when it already is)."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _need(what: str, dtype, device, shape, t: Optional[torch.Tensor]):
+    """A dense tensor of that type, device and shape, or None."""
+    if t is None:
+        return
+    if not t.is_cuda:
+        raise SvooError(f"{what} must live on a CUDA device")
+    if t.dtype != dtype or t.device != device:
+        raise SvooError(f"{what} must be {dtype} on {device}, not {t.dtype} on {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise SvooError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise SvooError(f"{what} must be contiguous")
+
+
+def _key_rows(what: str, t: torch.Tensor, device) -> int:
+    """Rows from one head to the next of a bf16 [B, Hkv, Nk, d] tensor: contiguous, or the first Nk
+    rows of every head of a longer contiguous buffer."""
+    if t.dim() != 4 or not t.is_cuda or t.dtype != torch.bfloat16 or t.device != device:
+        raise SvooError(f"{what} must be a bf16 [B, Hkv, N, d] tensor on {device}")
+    B, Hkv, Nk, d = t.shape
+    if t.is_contiguous():
+        return Nk
+    cap = t.stride(1) // d if Hkv > 1 else t.stride(0) // d
+    if t.stride(3) != 1 or t.stride(2) != d or cap < Nk or (Hkv > 1 and t.stride(1) != cap * d) or \
+            (B > 1 and t.stride(0) != Hkv * cap * d):
+        raise SvooError(f"{what} must be contiguous or the first rows of every head of a contiguous buffer")
+    return cap
+
+
+def _block_shape(q, k, v, cfg: BlockConfig, lengths, q_start) -> BlockShape:
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda:
+        raise SvooError("q must be a bf16 [B, H, N, d] tensor on a CUDA device")
+    if not q.is_contiguous():
+        raise SvooError("q must be contiguous")
+    B, H, Nq, d = q.shape
+    cap = _key_rows("k", k, q.device)
+    if v is not None and (v.shape != k.shape or _key_rows("v", v, q.device) != cap):
+        raise SvooError("k and v must have the same shape and strides")
+    if k.shape[0] != B or k.shape[3] != d:
+        raise SvooError("q, k and v must agree in batch and head dimension")
+    _need("lengths", torch.int32, q.device, (B,), lengths)
+    Nk = k.shape[2]
+    return BlockShape(B, H, k.shape[1], Nq, Nk, cap, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local,
+                      1 if cfg.causal else 0, Nk - Nq if q_start is None else q_start)
+
+
+def _block_scale(cfg: Optional[BlockConfig], d: int) -> float:
+    return cfg.scale if cfg is not None and cfg.scale is not None else 1.0 / math.sqrt(d)
+
+
+def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stream=None) -> torch.Tensor:
+    """Mean of the valid keys of every block of cfg.block keys: fp32 [B, Hkv, blocks, d].
+
+    `pool` is written in place instead of a new tensor; with last > 0 only the last `last` blocks that
+    hold keys of each sequence are renewed (after a token was appended, last=1)."""
+    if k.dim() != 4 or not k.is_cuda:
+        raise SvooError("k must be a bf16 [B, Hkv, N, d] tensor on a CUDA device")
+    cap = _key_rows("k", k, k.device)
+    B, Hkv, Nk, d = k.shape
+    nb = -(-Nk // cfg.block) if cfg.block > 0 else 0
+    _need("lengths", torch.int32, k.device, (B,), lengths)
+    _need("pool", torch.float32, k.device, (B, Hkv, nb, d), pool)
+    if pool is None:
+        if last:
+            raise SvooError("last renews blocks of an existing pool: pass it")
+        pool = torch.empty(B, Hkv, nb, d, dtype=torch.float32, device=k.device)
+    sh = BlockShape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0)
+    with _on_device(k):
+        _check(load().svoo_block_pool(ctypes.byref(sh), _ptr(k), _ptr(lengths), last, _ptr(pool),
+                                      _stream(stream)), "svoo_block_pool")
+    return pool
+
+
+def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: Optional[int] = None,
+                 idx=None, stream=None) -> torch.Tensor:
+    """The blocks that every query selects: int32 [B, Hkv, Nq, n_sel], ascending, -1 behind them.
+
+    n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
+    queries are the last Nq of n_keys; -1: the last Nq of each sequence's lengths."""
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
+        raise SvooError("q must be a contiguous bf16 [B, H, N, d] tensor on a CUDA device")
+    B, H, Nq, d = q.shape
+    nb = -(-n_keys // cfg.block) if cfg.block > 0 else 0
+    Hkv = pool.shape[1] if pool.dim() == 4 else 0
+    _need("pool", torch.float32, q.device, (B, Hkv, nb, d), pool)
+    _need("lengths", torch.int32, q.device, (B,), lengths)
+    _need("idx", torch.int32, q.device, (B, Hkv, Nq, cfg.n_sel), idx)
+    if idx is None:
+        idx = torch.empty(B, Hkv, Nq, max(cfg.n_sel, 0), dtype=torch.int32, device=q.device)
+    sh = BlockShape(B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local,
+                    1 if cfg.causal else 0, n_keys - Nq if q_start is None else q_start)
+    with _on_device(q):
+        _check(load().svoo_block_select(ctypes.byref(sh), _ptr(q), _ptr(pool), _ptr(lengths), _ptr(idx),
+                                        _stream(stream)), "svoo_block_select")
+    return idx
+
+
+def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[int] = None, out=None,
+               dev_err=None, stream=None):
+    """Attention of every query over the blocks in idx; returns (o, lse). No gradient is recorded
+    (block_attention records one)."""
+    sh = _block_shape(q, k, v, cfg, lengths, q_start)
+    _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, sh.Nq, cfg.n_sel), idx)
+    _need("out", torch.bfloat16, q.device, q.shape, out)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(sh.B, sh.H, sh.Nq, dtype=torch.float32, device=q.device)
+    with _on_device(q):
+        _check(load().svoo_block_attn(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), _ptr(lengths),
+                                      _block_scale(cfg, sh.d), _ptr(out), _ptr(lse), _ptr(dev_err),
+                                      _stream(stream)), "svoo_block_attn")
+    return out, lse
+
+
+def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=None,
+                        q_start: Optional[int] = None, workspace=None, dev_err=None, stream=None):
+    """Gradient of block_attn: (dq, dk, dv), with idx, o and lse as block_attn had or gave them."""
+    sh = _block_shape(q, k, v, cfg, lengths, q_start)
+    _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, sh.Nq, cfg.n_sel), idx)
+    _need("o", torch.bfloat16, q.device, q.shape, o)
+    _need("grad_o", torch.bfloat16, q.device, q.shape, grad_o)
+    _need("lse", torch.float32, q.device, (sh.B, sh.H, sh.Nq), lse)
+    L = load()
+    if workspace is None:
+        workspace = torch.empty(L.svoo_block_attn_backward_workspace_size(ctypes.byref(sh)),
+                                dtype=torch.uint8, device=q.device)
+    dq = torch.empty_like(q)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    with _on_device(q):
+        _check(L.svoo_block_attn_backward(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                          _ptr(grad_o), _ptr(idx), _ptr(lengths), _block_scale(cfg, sh.d),
+                                          _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+                                          _ptr(dev_err), _stream(stream)), "svoo_block_attn_backward")
+    return dq, dk, dv
+
+
+class _BlockAttn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, idx, cfg, lengths, q_start, dev_err):
+        o, lse = block_attn(q, k, v, idx, cfg, lengths, q_start, dev_err=dev_err)
+        ctx.save_for_backward(q, k, v, idx, lengths, o, lse, dev_err)
+        ctx.args = (cfg, q_start)
+        ctx.mark_non_differentiable(lse)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_o, _):
+        q, k, v, idx, lengths, o, lse, dev_err = ctx.saved_tensors
+        cfg, q_start = ctx.args
+        dq, dk, dv = block_attn_backward(q, k, v, o, lse, grad_o.contiguous(), idx, cfg, lengths, q_start,
+                                         dev_err=dev_err)
+        return dq, dk, dv, None, None, None, None, None
+
+
+def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[int] = None, dev_err=None):
+    """The whole path on the current stream: block means -> selection -> attention over the selected
+    blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
+    right-padded batch. Differentiable in q, k and v (the selection is a constant of the gradient; the
+    gradient's gradient is not offered). Returns (o, dict(idx, lse, pool, dev_err))."""
+    with torch.no_grad():
+        err = _err_buf(dev_err, q.device)
+        pool = block_pool(k, cfg, lengths)
+        idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start)
+    o, lse = _BlockAttn.apply(q, k, v, idx, cfg, lengths, q_start, err)
+    return o, dict(idx=idx, lse=lse, pool=pool, dev_err=err)
+
+
+# --------------------------------------------------------------------------- single tokens over a cache
+
+
+def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = None, weight=None, out=None,
+               workspace=None, dev_err=None, stream=None):
+    """Attention of one token per sequence, q bf16 [B, H, 1, d], over the first lengths[b] slots of a
+    cache, k and v bf16 [B, Hkv, cap, d]; returns (o, lse).
+
+    idx (from block_select, with its cfg): only the slots of the selected blocks. weight (fp32
+    [B, Hkv, cap]): every valid slot's softmax weight, summed over the group's heads, is added to it."""
+    if q.dim() != 4 or q.shape[2] != 1:
+        raise SvooError("q must be [B, H, 1, d]: one token per sequence")
+    if idx is not None and cfg is None:
+        raise SvooError("idx needs the BlockConfig that it was selected with")
+    if idx is not None and weight is not None:
+        raise SvooError("weights are summed over whole caches only: idx and weight exclude each other")
+    sh = _block_shape(q, k, v, cfg if cfg is not None else _WHOLE, lengths, 0)
+    if idx is not None:
+        _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, 1, cfg.n_sel), idx)
+    if weight is not None and sh.cap != sh.Nk:
+        raise SvooError("weights need k and v as whole buffers")
+    _need("weight", torch.float32, q.device, (sh.B, sh.Hkv, sh.Nk), weight)
+    _need("out", torch.bfloat16, q.device, q.shape, out)
+    L = load()
+    if workspace is None:
+        workspace = torch.empty(L.svoo_cache_attn_workspace_size(ctypes.byref(sh), idx is not None, weight is not None),
+                                dtype=torch.uint8, device=q.device)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(sh.B, sh.H, 1, dtype=torch.float32, device=q.device)
+    with _on_device(q):
+        _check(L.svoo_cache_attn(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(idx),
+                                 _block_scale(cfg, sh.d), _ptr(weight), _ptr(out), _ptr(lse), _ptr(workspace),
+                                 workspace.numel(), _ptr(dev_err), _stream(stream)), "svoo_cache_attn")
+    return out, lse
+
+
+_WHOLE = BlockConfig()
+
+
+def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: int = 0, workspace=None,
+                stream=None):
+    """Brings every sequence of a cache with more than `keep` slots down to `keep`, in place (k, v, weight,
+    pos and lengths; see svoo_cache_evict): the first `sink` and last `recent` positions stay, then the
+    heaviest slots of each key head. Block means of the cache are to be made anew afterwards."""
+    if k.dim() != 4 or not k.is_cuda:
+        raise SvooError("k must be a bf16 [B, Hkv, cap, d] tensor on a CUDA device")
+    B, Hkv, cap, d = k.shape
+    _need("k", torch.bfloat16, k.device, (B, Hkv, cap, d), k)
+    _need("v", torch.bfloat16, k.device, (B, Hkv, cap, d), v)
+    _need("weight", torch.float32, k.device, (B, Hkv, cap), weight)
+    _need("pos", torch.int32, k.device, (B, Hkv, cap), pos)
+    _need("lengths", torch.int32, k.device, (B,), lengths)
+    L = load()
+    if workspace is None:
+        workspace = torch.empty(L.svoo_cache_evict_workspace_size(B, Hkv, cap, keep), dtype=torch.uint8,
+                                device=k.device)
+    with _on_device(k):
+        _check(L.svoo_cache_evict(B, Hkv, cap, d, keep, sink, recent, _ptr(k), _ptr(v), _ptr(weight), _ptr(pos),
+                                  _ptr(lengths), _ptr(workspace), workspace.numel(), _stream(stream)),
+               "svoo_cache_evict")

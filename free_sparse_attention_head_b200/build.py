@@ -20,9 +20,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsvoo.so")
 STALL_LIB = os.path.join(HERE, "libsvoo_stall.so")
-SOURCES = ["api.cu", "cluster.cu", "mask.cu", "permute.cu", "attn.cu", "psa.cu"]
+SOURCES = ["api.cu", "cluster.cu", "mask.cu", "permute.cu", "attn.cu", "psa.cu",
+           "block_select.cu", "block_attn.cu", "block_grad.cu", "cache.cu"]
 STALL_SOURCES = ["cluster.cu", "attn.cu"]  # the kernels with pipeline waits
-HEADERS = ["common.cuh", "internal.h"]
+HEADERS = ["common.cuh", "internal.h", "blocks.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC_FLAGS = [

@@ -1,0 +1,839 @@
+// block_grad.cu -- gradient of the block-selected attention, sm_100a. The
+// selection is a constant of the gradient.
+//
+//   P = exp(scale q K^T - lse), delta = rowsum(do * o), dS = P * (do V^T - delta)
+//   dq = scale dS K,   dk = scale dS^T q,   dv = P^T do
+//
+// P is computed again from lse in both kernels rather than kept: two products
+// of 64 keys cost less than its bytes.
+//
+//   row_delta_kernel     delta, one warp per row
+//   block_dq_kernel      dq: row tiles against the union of their blocks, as the
+//                        forward kernel walks it
+//   sel_hist / sel_scan / sel_items / sel_fill
+//                        for every block the list of the queries that selected
+//                        it, in a fixed order (no atomics decide a place)
+//   block_dkv_kernel     dk, dv: one key tile against its list's rows, gathered
+//                        128 at a time, so no row computes for nothing
+//   block_dkv_sum_kernel long lists (a block that every query keeps) are cut
+//                        into pieces; their parts are added in order
+//
+// Every sum runs in a fixed order: two calls give the same bits.
+#include "blocks.cuh"
+
+namespace svoo {
+
+namespace {
+
+// ------------------------------------------------------------------ delta
+
+// one warp per row of [rows, D]; D / 32 elements per lane
+template <int D>
+__global__ void __launch_bounds__(256)
+    row_delta_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ go, size_t rows,
+                     float* __restrict__ delta) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  constexpr int kE = D / 32;
+  float a = 0.f;
+  const uint32_t* po = reinterpret_cast<const uint32_t*>(o + row * D + lane * kE);
+  const uint32_t* pg = reinterpret_cast<const uint32_t*>(go + row * D + lane * kE);
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) {
+    const uint32_t x = po[i], y = pg[i];
+    a = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), a);
+    a = fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), a);
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) a += __shfl_xor_sync(0xffffffffu, a, s);
+  if (lane == 0) delta[row] = a;
+}
+
+// ------------------------------------------------------------------ dq
+
+constexpr int kDqThreads = 192;
+
+struct DqSmem {
+  uint64_t kv_full, kv_empty, s_full, ds_full, mma_final;
+  uint32_t tmem_base;
+  int abort;
+  int max_limit;
+  int limit[kRowTile];
+  int count[kRowTile];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kDqThreads, 2)
+    block_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
+                    const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
+                    const uint16_t* __restrict__ go, const float* __restrict__ lse, const float* __restrict__ delta,
+                    const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths, float scale,
+                    float scale_log2, uint16_t* __restrict__ dq, int* __restrict__ err) {
+  constexpr int kSub = D / 64;
+  constexpr int kKvBytes = kKeyTile * D * 2;
+  constexpr int kRowBytes = kRowTile * D * 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = base;
+  uint8_t* g_s = q_s + kRowBytes;
+  uint8_t* k_s = g_s + kRowBytes;
+  uint8_t* v_s = k_s + kKvBytes;
+  DqSmem* S = reinterpret_cast<DqSmem*>(v_s + kKvBytes);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(S + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  const int b = blockIdx.y / p.Hkv, hk = blockIdx.y - b * p.Hkv;
+  const int t0 = blockIdx.x * p.tpt;
+  const int nt = min(p.tpt, p.Nq - t0);
+  const int len = seq_len(p, lengths, b);
+  const int32_t* slots = idx + (static_cast<size_t>(blockIdx.y) * p.Nq + t0) * p.n_sel;
+
+  for (int i = tid; i < (p.nb + 31) / 32; i += kDqThreads) bits[i] = 0;
+  if (tid == 0) {
+    S->abort = 0;
+    S->max_limit = 0;
+    mbar_init(smem_u32(&S->kv_full), 1);
+    mbar_init(smem_u32(&S->kv_empty), 1);
+    mbar_init(smem_u32(&S->s_full), 1);
+    mbar_init(smem_u32(&S->ds_full), 4);
+    mbar_init(smem_u32(&S->mma_final), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  bool bad = false;
+  for (int ti = warp; ti < nt; ti += kDqThreads / 32) {
+    const int lim = query_limit(p, len, t0 + ti);
+    const int n = walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
+      if (blk * p.block < lim) atomicOr(&bits[blk >> 5], 1u << (blk & 31));
+    });
+    if (lane == 0) {
+      S->limit[ti] = lim;
+      S->count[ti] = n;
+      atomicMax(&S->max_limit, lim);
+    }
+  }
+  if (bad && lane == 0) report_error(err, kErrBadPlan);
+  load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kDqThreads);
+  load_query_rows<D>(g_s, go, p, b, hk, t0, tid, kDqThreads);
+  fence_proxy_async_smem();
+  if (warp == 5) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&S->tmem_base), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = S->tmem_base;
+  volatile int* abort = &S->abort;
+  const uint32_t q_u = smem_u32(q_s), g_u = smem_u32(g_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
+  TileIter it(bits, p.nb, p.nsub, S->max_limit);
+  int armed = -1;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- producer
+    const size_t row0 = static_cast<size_t>(blockIdx.y) * p.cap;
+    if (lane == 0) {
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+    for (int j = 0; it.next(); ++j) {
+      const int key0 = it.tile() * kKeyTile;
+      if (j >= 1) {
+        int okl = 1;
+        if (lane == 0) okl = mbar_wait(smem_u32(&S->kv_empty), (j - 1) & 1, abort) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, okl, 0)) break;
+      }
+      const uint32_t bar = smem_u32(&S->kv_full);
+      if (len - key0 >= kKeyTile) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * kKvBytes);
+          for (int s = 0; s < kSub; ++s) {
+            tma_load_2d(&kmap, k_u + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
+            tma_load_2d(&vmap, v_u + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
+          }
+        }
+      } else {
+        load_key_rows<D>(k_s, k, row0 + key0, len - key0, lane, 32);
+        load_key_rows<D>(v_s, v, row0 + key0, len - key0, lane, 32);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      }
+      armed = j;
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
+      const uint32_t idesc_q = idesc_bf16_f32(kRowTile, D, false, true);
+      for (int j = 0; it.next(); ++j) {
+        if (!mbar_wait(smem_u32(&S->kv_full), j & 1, abort)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
+          umma_f16(tmem, sw128_desc(q_u + ro, 16, 1024), sw128_desc(k_u + ko, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+          umma_f16(tmem + 64, sw128_desc(g_u + ro, 16, 1024), sw128_desc(v_u + ko, 16, 1024), idesc_s,
+                   kk > 0 ? 1u : 0u);
+        }
+        umma_commit(smem_u32(&S->s_full));
+        if (!mbar_wait(smem_u32(&S->ds_full), j & 1, abort)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kKeyTile / 16; ++kk)
+          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(k_u + kk * 16 * 128, kKeyTile * 128, 1024), idesc_q,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&S->kv_empty));
+      }
+      umma_commit(smem_u32(&S->mma_final));
+      mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
+    }
+  } else {
+    // ---------------------------------------------------------------- dS
+    const int r = tid;
+    const int ti = r / p.G, g = r - ti * p.G;
+    const bool live = ti < nt;
+    const int lim = live ? S->limit[ti] : 0;
+    const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
+    const float lse2 = lse[row] * 1.4426950408889634f, dl = delta[row];
+    SlotCursor mine(slots + static_cast<size_t>(live ? ti : 0) * p.n_sel, live ? S->count[ti] : 0);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    bool ok = true;
+    int j = 0;
+    for (; it.next(); ++j) {
+      const int nv = mine.has(it.blk) ? max(0, min(kKeyTile, lim - it.tile() * kKeyTile)) : 0;
+      const bool some = __any_sync(0xffffffffu, nv > 0);
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t pk[32];
+      if (some) {
+        float s[32], x[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld32f(lane_base + h * 32, s);
+          tmem_ld32f(lane_base + 64 + h * 32, x);
+          tmem_wait_ld_f(s);
+          tmem_wait_ld_f(x);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int c0 = h * 32 + 2 * c;
+            const float e0 = ex2_approx(fmaf(s[2 * c], scale_log2, -lse2)) * (x[2 * c] - dl);
+            const float e1 = ex2_approx(fmaf(s[2 * c + 1], scale_log2, -lse2)) * (x[2 * c + 1] - dl);
+            // what is masked may be infinite or NaN: chosen, not multiplied
+            pk[h * 16 + c] = pack_bf16x2(c0 < nv ? e0 : 0.f, c0 + 1 < nv ? e1 : 0.f);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = 0u;
+      }
+      tmem_st32(lane_base, pk);  // over S, which this warp has read
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->ds_full));
+    }
+    if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->kv_empty), (j - 1) & 1, abort));
+    if (ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < D / 32; ++c0) {
+        uint32_t x[32];
+        if (j > 0) {
+          tmem_ld32(lane_base + 128 + c0 * 32, x);
+          tmem_wait_ld_regs(x);
+        }
+        if (live) {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (j > 0) {
+              w.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * scale, __uint_as_float(x[c8 * 8 + 1]) * scale);
+              w.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * scale, __uint_as_float(x[c8 * 8 + 3]) * scale);
+              w.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * scale, __uint_as_float(x[c8 * 8 + 5]) * scale);
+              w.w = pack_bf16x2(__uint_as_float(x[c8 * 8 + 6]) * scale, __uint_as_float(x[c8 * 8 + 7]) * scale);
+            }
+            reinterpret_cast<uint4*>(dq + row * D + c0 * 32)[c8] = w;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort) {
+    if (tid == 0) report_error(err, kErrTimeoutAttn);
+    if (warp == 4 && lane == 0 && armed >= 0) mbar_wait_cleanup(smem_u32(&S->kv_full), armed & 1);
+    __syncthreads();
+  }
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ------------------------------------------------------------------ inverse lists
+
+// A warp takes `chunk` queries of one (sequence, key head) in order, 32 at a
+// time and slot by slot; lanes with the same block are ranked by lane. Both
+// passes walk the same way, so a place depends on the selection alone.
+template <bool kFill>
+__global__ void __launch_bounds__(32)
+    sel_walk_kernel(BlockDims p, const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths, int chunk,
+                    int nchunk, int32_t* __restrict__ hist, const int32_t* __restrict__ start,
+                    int32_t* __restrict__ list) {
+  extern __shared__ int cnt[];
+  const int lane = threadIdx.x, c = blockIdx.x, bh = blockIdx.y;
+  const int len = seq_len(p, lengths, bh / p.Hkv);
+  int32_t* h = hist + (static_cast<size_t>(bh) * nchunk + c) * p.nb;
+  for (int i = lane; i < p.nb; i += 32) cnt[i] = kFill ? start[static_cast<size_t>(bh) * p.nb + i] + h[i] : 0;
+  __syncwarp();
+  const int t1 = min(p.Nq, (c + 1) * chunk);
+  for (int t0 = c * chunk; t0 < t1; t0 += 32) {
+    const int t = t0 + lane;
+    const int lim = t < t1 ? query_limit(p, len, t) : 0;
+    const int32_t* mine = idx + (static_cast<size_t>(bh) * p.Nq + (t < t1 ? t : 0)) * p.n_sel;
+    int prev = -1;
+    bool go = t < t1;
+    for (int s = 0; s < p.n_sel; ++s) {
+      const int blk = go ? mine[s] : -1;
+      go = go && blk > prev && blk < p.nb;
+      prev = blk;
+      if (!__any_sync(0xffffffffu, go)) break;
+      const bool take = go && blk * p.block < lim;
+      const unsigned same = __match_any_sync(0xffffffffu, take ? blk : -1 - lane);
+      if (take) {
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        if (kFill) list[static_cast<size_t>(bh) * p.Nq * p.n_sel + cnt[blk] + rank] = t;
+      }
+      __syncwarp();
+      if (take && (same & ((1u << lane) - 1u)) == 0) cnt[blk] += __popc(same);
+      __syncwarp();
+    }
+  }
+  if (!kFill)
+    for (int i = lane; i < p.nb; i += 32) h[i] = cnt[i];
+}
+
+// per block: running sums of the chunks' counts (in place) and the total
+__global__ void __launch_bounds__(256)
+    sel_scan_kernel(BlockDims p, int nchunk, int32_t* __restrict__ hist, int32_t* __restrict__ total) {
+  const int blk = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
+  if (blk >= p.nb) return;
+  int32_t* h = hist + static_cast<size_t>(bh) * nchunk * p.nb + blk;
+  int a = 0;
+#pragma unroll 8
+  for (int c = 0; c < nchunk; ++c) {
+    const int x = h[static_cast<size_t>(c) * p.nb];
+    h[static_cast<size_t>(c) * p.nb] = a;
+    a += x;
+  }
+  total[static_cast<size_t>(bh) * p.nb + blk] = a;
+}
+
+// Exclusive sums over a block of 1024 threads, each with its own value.
+__device__ __forceinline__ int block_exclusive(int x, int* warp_sums, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *all = warp_sums[31];
+  const int r = inc - x + (warp ? warp_sums[warp - 1] : 0);
+  __syncthreads();
+  return r;
+}
+
+// Where each block's list starts (per (sequence, key head)), and the work
+// items: every key tile's list in pieces of at most `piece` rows (one piece
+// where there are none). items: tile, piece, pieces, slot of the piece's part
+// (-1 where it is the only one). One block of 1024 threads.
+__global__ void __launch_bounds__(1024)
+    sel_items_kernel(BlockDims p, int ktiles, int piece, const int32_t* __restrict__ total, int32_t* __restrict__ start,
+                     int4* __restrict__ items, int32_t* __restrict__ counts) {
+  __shared__ int sums[32];
+  const int BH = p.B * p.Hkv;
+  for (int bh = 0; bh < BH; ++bh) {
+    int base = 0;
+    for (int i0 = 0; i0 < p.nb; i0 += 1024) {
+      const int i = i0 + threadIdx.x;
+      int all;
+      const int x = block_exclusive(i < p.nb ? total[static_cast<size_t>(bh) * p.nb + i] : 0, sums, &all);
+      if (i < p.nb) start[static_cast<size_t>(bh) * p.nb + i] = base + x;
+      base += all;
+    }
+  }
+  int n_items = 0, n_slots = 0;
+  const int tiles = BH * ktiles;
+  for (int i0 = 0; i0 < tiles; i0 += 1024) {
+    const int i = i0 + threadIdx.x;
+    int pieces = 0;
+    if (i < tiles) {
+      const int bh = i / ktiles, kt = i - bh * ktiles;
+      const long long rows = static_cast<long long>(total[static_cast<size_t>(bh) * p.nb + kt / p.nsub]) * p.G;
+      pieces = max(1, static_cast<int>((rows + piece - 1) / piece));
+    }
+    int all, all_slots;
+    int at = block_exclusive(pieces, sums, &all) + n_items;
+    const int slot = block_exclusive(pieces > 1 ? pieces : 0, sums, &all_slots) + n_slots;
+    for (int c = 0; c < pieces; ++c) items[at + c] = make_int4(i, c, pieces, pieces > 1 ? slot + c : -1);
+    n_items += all;
+    n_slots += all_slots;
+  }
+  if (threadIdx.x == 0) {
+    counts[0] = n_items;
+    counts[1] = n_slots;
+  }
+}
+
+// ------------------------------------------------------------------ dk, dv
+
+constexpr int kDkvThreads = 416;  // warps 0-3, 4-7: dS of even / odd row tiles; 8-11: loads; 12: MMA issuer
+
+struct DkvSmem {
+  uint64_t full[2], free_[2], s_full[2], ds_full[2], mma_final;
+  uint32_t tmem_base;
+  int abort;
+  float lse2[2][kRowTile];
+  float delta[2][kRowTile];
+  uint8_t nv[2][kRowTile];  // valid keys of the row in this key tile
+};
+
+template <int D>
+constexpr size_t dkv_tile_bytes() {
+  return 2 * static_cast<size_t>(kKeyTile) * D * 2 + 4 * static_cast<size_t>(kRowTile) * D * 2 +
+         4 * static_cast<size_t>(kRowTile) * kKeyTile * 2;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Per row tile: S = Q K^T and dP = dO V^T (rows x 64 keys) into tensor memory;
+// P and dS back to shared memory in bf16; dV^T += dO^T P and dK^T += Q^T dS
+// with the model dimension as the product's 128 rows (d = 64: dO and Q side by
+// side, each product uses its own half of the lanes), so that a tile of 64
+// keys runs at M = 128.
+// TMEM: S, dP of stage s at s * 128 + {0, 64}; dV^T at 256, dK^T at 320.
+template <int D>
+__global__ void __launch_bounds__(kDkvThreads, 1)
+    block_dkv_kernel(BlockDims p, int ktiles, int piece, const uint16_t* __restrict__ q,
+                     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const uint16_t* __restrict__ go,
+                     const float* __restrict__ lse, const float* __restrict__ delta,
+                     const int32_t* __restrict__ lengths, const int32_t* __restrict__ total,
+                     const int32_t* __restrict__ start, const int32_t* __restrict__ list,
+                     const int4* __restrict__ items, const int32_t* __restrict__ counts, float scale,
+                     float scale_log2, uint16_t* __restrict__ dk, uint16_t* __restrict__ dv,
+                     float* __restrict__ parts, int* __restrict__ err) {
+  constexpr int kRowBytes = kRowTile * D * 2;
+  constexpr int kKvBytes = kKeyTile * D * 2;
+  constexpr int kPBytes = kRowTile * kKeyTile * 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // no room to round up in: the declared alignment has to hold
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) report_error(err, kErrBadPlan);
+    return;
+  }
+  uint8_t* row_s = smem_raw;             // stage s: dO at s * 2 * kRowBytes, Q behind it
+  uint8_t* p_s = row_s + 4 * kRowBytes;  // stage s: P, dS
+  uint8_t* k_s = p_s + 4 * kPBytes;
+  uint8_t* v_s = k_s + kKvBytes;
+  DkvSmem* S = reinterpret_cast<DkvSmem*>(v_s + kKvBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= counts[0]) return;
+  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  const int4 item = items[blockIdx.x];
+  const int bh = item.x / ktiles, kt = item.x - bh * ktiles, key0 = kt * kKeyTile;
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int len = seq_len(p, lengths, b);
+  const size_t at = static_cast<size_t>(bh) * p.nb + kt / p.nsub;
+  const int32_t* toks = list + static_cast<size_t>(bh) * p.Nq * p.n_sel + start[at];
+  const long long all_rows = static_cast<long long>(total[at]) * p.G;
+  const long long row0 = static_cast<long long>(item.y) * piece;
+  const int rows = static_cast<int>(min(static_cast<long long>(piece), all_rows - row0));
+  const int nj = (max(rows, 0) + kRowTile - 1) / kRowTile;
+
+  if (tid == 0) {
+    S->abort = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&S->full[s]), 128);
+      mbar_init(smem_u32(&S->free_[s]), 1);
+      mbar_init(smem_u32(&S->s_full[s]), 1);
+      mbar_init(smem_u32(&S->ds_full[s]), 4);
+    }
+    mbar_init(smem_u32(&S->mma_final), 1);
+    fence_mbar_init();
+  }
+  if (nj > 0) {
+    const size_t krow = static_cast<size_t>(bh) * p.cap + key0;
+    load_key_rows<D>(k_s, k, krow, len - key0, tid, kDkvThreads);
+    load_key_rows<D>(v_s, v, krow, len - key0, tid, kDkvThreads);
+    fence_proxy_async_smem();
+  }
+  if (warp == 12) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&S->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  volatile int* abort = &S->abort;
+  const uint32_t row_u = smem_u32(row_s), p_u = smem_u32(p_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
+
+  if (warp >= 8 && warp < 12) {
+    // ---------------------------------------------------------------- row gather
+    const int t = tid - 256;  // one row's scalars per thread
+    constexpr int kChunks = D / 8;
+    for (int j = 0; j < nj; ++j) {
+      const int st = j & 1;
+      if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->free_[st]), ((j - 2) >> 1) & 1, abort))) break;
+      {
+        const int f = j * kRowTile + t;
+        int nv = 0;
+        float l2 = 0.f, dl = 0.f;
+        if (f < rows) {
+          const long long fr = row0 + f;
+          const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
+          const int tok = toks[e];
+          const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + tok;
+          nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
+          l2 = lse[row] * 1.4426950408889634f;
+          dl = delta[row];
+        }
+        S->nv[st][t] = static_cast<uint8_t>(nv);
+        S->lse2[st][t] = l2;
+        S->delta[st][t] = dl;
+      }
+      const uint32_t g_dst = row_u + st * 2 * kRowBytes, q_dst = g_dst + kRowBytes;
+#pragma unroll 4
+      for (int c = t; c < kRowTile * kChunks; c += 128) {
+        const int r = c / kChunks, ch = c - r * kChunks;
+        const int f = j * kRowTile + r;
+        const uint32_t off = sw128_offset(r, ch * 8, kRowTile);
+        if (f < rows) {
+          const long long fr = row0 + f;
+          const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
+          const size_t src = ((static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + toks[e]) * D + ch * 8;
+          cp_async16(g_dst + off, go + src);
+          cp_async16(q_dst + off, q + src);
+        } else {
+          *reinterpret_cast<uint4*>(row_s + (g_dst - row_u) + off) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(row_s + (q_dst - row_u) + off) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&S->full[st]));  // this thread's part of row tile j is in
+    }
+  } else if (warp == 12) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
+      const uint32_t idesc_g = idesc_bf16_f32(128, kKeyTile, true, true);
+      bool ok = true;
+      for (int j = 0; j <= nj && ok; ++j) {
+        if (j < nj) {
+          const int st = j & 1;
+          const uint32_t g_u = row_u + st * 2 * kRowBytes, q_u = g_u + kRowBytes;
+          if (!(ok = mbar_wait(smem_u32(&S->full[st]), (j >> 1) & 1, abort))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32;
+            const uint32_t ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
+            umma_f16(tmem + st * 128, sw128_desc(q_u + ro, 16, 1024), sw128_desc(k_u + ko, 16, 1024), idesc_s,
+                     kk > 0 ? 1u : 0u);
+            umma_f16(tmem + st * 128 + 64, sw128_desc(g_u + ro, 16, 1024), sw128_desc(v_u + ko, 16, 1024), idesc_s,
+                     kk > 0 ? 1u : 0u);
+          }
+          umma_commit(smem_u32(&S->s_full[st]));
+        }
+        if (j >= 1) {
+          const int st = (j - 1) & 1;
+          const uint32_t g_u = row_u + st * 2 * kRowBytes;
+          const uint32_t a_v = g_u, a_k = D == 128 ? g_u + kRowBytes : g_u;
+          if (!(ok = mbar_wait(smem_u32(&S->ds_full[st]), ((j - 1) >> 1) & 1, abort))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kRowTile / 16; ++kk) {
+            const uint32_t step = kk * 16 * 128;
+            const uint64_t bp = sw128_desc(p_u + st * 2 * kPBytes + step, 16, 1024);
+            const uint64_t bs = sw128_desc(p_u + st * 2 * kPBytes + kPBytes + step, 16, 1024);
+            umma_f16(tmem + 256, sw128_desc(a_v + step, kRowTile * 128, 1024), bp, idesc_g,
+                     (j > 1 || kk > 0) ? 1u : 0u);
+            umma_f16(tmem + 320, sw128_desc(a_k + step, kRowTile * 128, 1024), bs, idesc_g,
+                     (j > 1 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(smem_u32(&S->free_[st]));
+        }
+      }
+      umma_commit(smem_u32(&S->mma_final));
+      mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- P, dS
+    const int st = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + st * 128;
+    uint8_t* prow = p_s + st * 2 * kPBytes;
+    bool ok = true;
+    for (int j = st; j < nj; j += 2) {
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort));
+      if (!ok) break;
+      tc_fence_after();
+      // the row's scalars came with its tile, which S was computed from
+      const int nv = S->nv[st][r];
+      const float lse2 = S->lse2[st][r], dl = S->delta[st][r];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float s[32], x[32];
+        tmem_ld32f(lane_base + h * 32, s);
+        tmem_ld32f(lane_base + 64 + h * 32, x);
+        tmem_wait_ld_f(s);
+        tmem_wait_ld_f(x);
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) {
+          uint32_t pp[4], ds[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = c8 * 8 + 2 * c, col = h * 32 + i;
+            const float e0 = col < nv ? ex2_approx(fmaf(s[i], scale_log2, -lse2)) : 0.f;
+            const float e1 = col + 1 < nv ? ex2_approx(fmaf(s[i + 1], scale_log2, -lse2)) : 0.f;
+            pp[c] = pack_bf16x2(e0, e1);
+            ds[c] = pack_bf16x2(col < nv ? e0 * (x[i] - dl) : 0.f, col + 1 < nv ? e1 * (x[i + 1] - dl) : 0.f);
+          }
+          const uint32_t off = sw128_offset(r, h * 32 + c8 * 8, kRowTile);
+          *reinterpret_cast<uint4*>(prow + off) = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+          *reinterpret_cast<uint4*>(prow + kPBytes + off) = make_uint4(ds[0], ds[1], ds[2], ds[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->ds_full[st]));
+    }
+    // ---------------------------------------------------------------- epilogue
+    // warps 0-3 write dv, 4-7 dk: thread = one model dimension (TMEM lane)
+    if (ok && nj > 0) {
+      const int last = nj - 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->free_[last & 1]), (last >> 1) & 1, abort));
+    }
+    if (ok) {
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 + st * 64;
+      const int dim = D == 128 ? r : r - st * 64;  // d = 64: dv in lanes 0-63, dk in lanes 64-127
+      const bool mine = D == 128 || (dim >= 0 && dim < 64);
+      const float mul = st ? scale : 1.f;
+      uint16_t* dst = st ? dk : dv;
+      const int nkeys = min(kKeyTile, p.Nk - key0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[32];
+        if (nj > 0) {
+          tmem_ld32(acc + h * 32, x);
+          tmem_wait_ld_regs(x);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = 0u;
+        }
+        if (!mine) continue;
+        if (item.w >= 0) {
+          float* o = parts + (static_cast<size_t>(item.w) * 2 + st) * kKeyTile * D + dim;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[(h * 32 + c) * D] = __uint_as_float(x[c]) * mul;
+        } else {
+          uint16_t* o = dst + (static_cast<size_t>(bh) * p.Nk + key0) * D + dim;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c < nkeys)
+              o[static_cast<size_t>(h * 32 + c) * D] =
+                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(x[c]) * mul, 0.f) & 0xffffu);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) report_error(err, kErrTimeoutAttn);
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// adds the parts of the key tiles whose list was cut, in order
+template <int D>
+__global__ void __launch_bounds__(256)
+    block_dkv_sum_kernel(BlockDims p, int ktiles, const int4* __restrict__ items, const int32_t* __restrict__ counts,
+                         const float* __restrict__ parts, uint16_t* __restrict__ dk, uint16_t* __restrict__ dv) {
+  if (static_cast<int>(blockIdx.x) >= counts[0]) return;
+  const int4 item = items[blockIdx.x];
+  if (item.z < 2 || item.y != 0) return;
+  const int bh = item.x / ktiles, key0 = (item.x - bh * ktiles) * kKeyTile;
+  const int nkeys = min(kKeyTile, p.Nk - key0);
+  const float* src = parts + static_cast<size_t>(item.w) * 2 * kKeyTile * D;
+  for (int i = threadIdx.x * 2; i < 2 * kKeyTile * D; i += 512) {
+    float a = 0.f, b = 0.f;
+    for (int c = 0; c < item.z; ++c) {
+      const float2 x = *reinterpret_cast<const float2*>(src + static_cast<size_t>(c) * 2 * kKeyTile * D + i);
+      a += x.x;
+      b += x.y;
+    }
+    const int which = i / (kKeyTile * D), rest = i - which * kKeyTile * D, key = rest / D;
+    if (key < nkeys)
+      *reinterpret_cast<uint32_t*>((which ? dk : dv) + (static_cast<size_t>(bh) * p.Nk + key0) * D + rest) =
+          pack_bf16x2(a, b);
+  }
+}
+
+static_assert(dkv_tile_bytes<128>() + sizeof(DkvSmem) <= 232448, "dk, dv: shared memory of one SM");
+
+// ------------------------------------------------------------------ host side
+
+// Rows of one piece: an eighth of an SM's share of all rows, so that a block
+// which every query keeps does not leave one SM with the last word, and at
+// least 32 tiles, below which a piece's own start and its part's bytes show.
+inline int piece_rows(const BlockDims& p) {
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.Nq * p.n_sel * p.nsub * p.G;
+  long long piece = rows / (148 * 8);
+  piece = (piece + kRowTile - 1) / kRowTile * kRowTile;
+  if (piece < 32 * kRowTile) piece = 32 * kRowTile;
+  return static_cast<int>(piece < (1 << 28) ? piece : (1 << 28));
+}
+
+struct GradPlan {
+  int ktiles, chunk, nchunk, piece;
+  long long max_items, max_slots;
+  float *delta, *parts;
+  int32_t *hist, *total, *start, *list, *counts;
+  int4* items;
+  size_t bytes;
+};
+
+GradPlan grad_plan(const BlockDims& p, int d, void* ws) {
+  GradPlan g;
+  const long long BHk = static_cast<long long>(p.B) * p.Hkv;
+  const long long rows = BHk * p.Nq * p.n_sel * p.nsub * p.G;  // over all key tiles, at most
+  g.ktiles = (p.Nk + kKeyTile - 1) / kKeyTile;
+  g.chunk = p.nb > 256 ? (p.nb + 31) / 32 * 32 : 256;  // the counts stay below one per key
+  g.nchunk = (p.Nq + g.chunk - 1) / g.chunk;
+  g.piece = piece_rows(p);
+  g.max_items = BHk * g.ktiles + rows / g.piece;
+  g.max_slots = 2 * (rows / g.piece);  // a cut list has more rows than one piece
+  Carver c(ws);
+  g.delta = c.take<float>(static_cast<size_t>(p.B) * p.H * p.Nq);
+  g.hist = c.take<int32_t>(static_cast<size_t>(BHk) * g.nchunk * p.nb);
+  g.total = c.take<int32_t>(static_cast<size_t>(BHk) * p.nb);
+  g.start = c.take<int32_t>(static_cast<size_t>(BHk) * p.nb);
+  g.list = c.take<int32_t>(static_cast<size_t>(BHk) * p.Nq * p.n_sel);
+  g.counts = c.take<int32_t>(2);
+  g.items = c.take<int4>(static_cast<size_t>(g.max_items));
+  g.parts = c.take<float>(static_cast<size_t>(g.max_slots) * 2 * kKeyTile * d);
+  g.bytes = (c.used + 255) / 256 * 256;
+  return g;
+}
+
+template <int D>
+svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, const void* v, const void* o,
+                              const float* lse, const void* go, const int32_t* idx, const int32_t* lengths,
+                              float scale, void* dq, void* dk, void* dv, void* ws, int32_t* dev_err,
+                              cudaStream_t st) {
+  const GradPlan g = grad_plan(p, D, ws);
+  const int BHk = p.B * p.Hkv;
+  const size_t rows = static_cast<size_t>(p.B) * p.H * p.Nq;
+  const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
+                 *vp = static_cast<const uint16_t*>(v), *gp = static_cast<const uint16_t*>(go);
+  CUtensorMap km, vm;
+  const uint64_t krows = static_cast<uint64_t>(BHk) * p.cap;
+  if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
+      encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
+    return SVOO_ERR_CUDA;
+  const size_t dq_smem = 1024 + 2 * static_cast<size_t>(kRowTile + kKeyTile) * D * 2 + sizeof(DqSmem) +
+                         static_cast<size_t>((p.nb + 31) / 32) * 4;
+  const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
+  const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
+  if (cudaFuncSetAttribute(block_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(dq_smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(block_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(dkv_smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(sel_walk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(sel_walk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+          cudaSuccess)
+    return SVOO_ERR_CUDA;
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (p.Nq > 0) {
+    row_delta_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(static_cast<const uint16_t*>(o), gp,
+                                                                               rows, g.delta);
+    sel_walk_kernel<false><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
+                                                                      nullptr, nullptr);
+  }
+  sel_scan_kernel<<<dim3((p.nb + 255) / 256, BHk), 256, 0, st>>>(p, g.nchunk, g.hist, g.total);
+  sel_items_kernel<<<1, 1024, 0, st>>>(p, g.ktiles, g.piece, g.total, g.start, g.items, g.counts);
+  if (p.Nq > 0) {
+    sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
+                                                                     g.start, g.list);
+    block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
+        km, vm, p, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+  }
+  block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
+      p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,
+      scale_log2, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv), g.parts, dev_err);
+  if (g.max_slots > 0)
+    block_dkv_sum_kernel<D><<<static_cast<unsigned>(g.max_items), 256, 0, st>>>(
+        p, g.ktiles, g.items, g.counts, g.parts, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv));
+  return launch_status();
+}
+
+}  // namespace
+
+}  // namespace svoo
+
+using namespace svoo;
+
+extern "C" size_t svoo_block_attn_backward_workspace_size(const svoo_block_shape* shape) {
+  if (!block_shape_ok(shape)) return 0;
+  return grad_plan(block_dims(shape), shape->d, nullptr).bytes;
+}
+
+extern "C" svoo_status svoo_block_attn_backward(const svoo_block_shape* shape, const void* q, const void* k,
+                                                const void* v, const void* o, const float* lse, const void* grad_o,
+                                                const int32_t* idx, const int32_t* lengths, float scale, void* dq,
+                                                void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                                int32_t* dev_err, void* stream) {
+  if (!block_shape_ok(shape) || !q || !k || !v || !o || !lse || !grad_o || !idx || !dq || !dk || !dv || !workspace ||
+      !scale_ok(scale))
+    return SVOO_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, o, grad_o, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                        static_cast<const void*>(dv)})
+    if (!aligned(x, 16)) return SVOO_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || !aligned(idx, 4) || !aligned(lse, 4)) return SVOO_ERR_INVALID_ARG;
+  const BlockDims p = block_dims(shape);
+  if (workspace_bytes < grad_plan(p, shape->d, nullptr).bytes) return SVOO_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (shape->d == 128)
+    return launch_block_grad<128>(p, q, k, v, o, lse, grad_o, idx, lengths, scale, dq, dk, dv, workspace, dev_err, st);
+  return launch_block_grad<64>(p, q, k, v, o, lse, grad_o, idx, lengths, scale, dq, dk, dv, workspace, dev_err, st);
+}

@@ -1,0 +1,217 @@
+// blocks.cuh -- what the kernels of the block-selected attention share: the
+// shape as the device sees it, the limit of a query row, the walk over a tile
+// of queries' selected blocks, row gathers into swizzled shared memory.
+//
+// Rows. A key head is shared by G = H / Hkv query heads, which select the same
+// blocks. A row is one (query, head of the group) pair; a 128-row MMA tile
+// holds tpt = 128 / G consecutive queries, query-major (row = query * G +
+// head), so that the rows of a warp belong to few queries and a warp often has
+// nothing to do for a block that only other queries selected.
+//
+// Keys come in tiles of 64 (kKeyTile); a block is a run of `nsub` tiles.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace svoo {
+
+constexpr int kRowTile = 128;
+constexpr int kKeyTile = 64;
+constexpr int kMaxSel = 256;      // slots of a query
+constexpr int kMaxBlocks = 16384;  // blocks of a sequence
+constexpr int kNoBlock = 0x7fffffff;
+
+struct BlockDims {
+  int B, H, Hkv, G;
+  int Nq, Nk, cap;  // queries, keys, key rows from one head to the next
+  int nb, block, nsub, n_sel;
+  int sink, local, causal, q_start;
+  int tpt;  // queries of a row tile
+};
+
+inline bool block_shape_ok(const svoo_block_shape* s) {
+  if (!s) return false;
+  if (s->B < 1 || s->H < 1 || s->Hkv < 1 || s->H % s->Hkv || s->H / s->Hkv > kRowTile) return false;
+  if (s->Nq < 0 || s->Nk < 1 || s->cap < s->Nk || s->cap > (1 << 20) || s->Nq > (1 << 20)) return false;
+  if (s->d != 64 && s->d != 128) return false;
+  if (s->block < kKeyTile || s->block % kKeyTile || s->block > 1024) return false;
+  if (s->n_sel < 1 || s->n_sel > kMaxSel) return false;
+  if (s->causal != 0 && s->causal != 1) return false;
+  if (s->sink < 0 || s->local < 0 || s->sink > s->n_sel || s->local > s->n_sel || s->sink + s->local > s->n_sel)
+    return false;
+  if (s->causal ? s->local < 1 : s->local != 0) return false;
+  if (s->q_start < -1 || s->q_start > (1 << 20)) return false;
+  if (static_cast<long long>(s->B) * s->H > 65535) return false;  // grid.y limit
+  // rows of q and of k, v: TMA row coordinates and row indices are int32
+  if (static_cast<long long>(s->B) * s->H * (s->Nq > 1 ? s->Nq : 1) >= (1LL << 31) - 256) return false;
+  if (static_cast<long long>(s->B) * s->Hkv * s->cap >= (1LL << 31) - 256) return false;
+  return true;
+}
+
+inline BlockDims block_dims(const svoo_block_shape* s) {
+  BlockDims p;
+  p.B = s->B;
+  p.H = s->H;
+  p.Hkv = s->Hkv;
+  p.G = s->H / s->Hkv;
+  p.Nq = s->Nq;
+  p.Nk = s->Nk;
+  p.cap = s->cap;
+  p.block = s->block;
+  p.nsub = s->block / kKeyTile;
+  p.nb = (s->Nk + s->block - 1) / s->block;
+  p.n_sel = s->n_sel;
+  p.sink = s->sink;
+  p.local = s->local;
+  p.causal = s->causal;
+  p.q_start = s->q_start;
+  p.tpt = kRowTile / p.G;
+  return p;
+}
+
+inline bool scale_ok(float scale) { return scale > 0.f && scale < INFINITY; }
+
+#ifdef __CUDACC__
+
+// keys of sequence b, clamped to what the buffers hold
+__device__ __forceinline__ int seq_len(const BlockDims& p, const int32_t* lengths, int b) {
+  return lengths ? max(0, min(p.Nk, lengths[b])) : p.Nk;
+}
+
+__device__ __forceinline__ int query_pos(const BlockDims& p, int len, int i) {
+  return p.q_start >= 0 ? p.q_start + i : len - p.Nq + i;
+}
+
+// Query i attends to keys below this: its own position + 1 (nothing for a
+// query outside its sequence), or the whole sequence when not causal.
+__device__ __forceinline__ int query_limit(const BlockDims& p, int len, int i) {
+  if (!p.causal) return len;
+  const int pos = query_pos(p, len, i);
+  return pos >= 0 && pos < len ? pos + 1 : 0;
+}
+
+// A query's slots hold ascending block ids, then -1. The list ends at the first
+// entry that is out of range or not above the one before it; *bad is raised
+// when that entry is not -1. A warp calls it together; f(block) is called by
+// the lane that holds the block. Returns the list's length.
+template <class F>
+__device__ __forceinline__ int walk_slots(const int32_t* slots, int n, int nb, bool* bad, F f) {
+  const int lane = threadIdx.x & 31;
+  int count = 0, carry = -1;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int s = s0 + lane;
+    const int v = s < n ? slots[s] : -1;
+    int prev = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) prev = carry;
+    const bool ok = v >= 0 && v < nb && v > prev;
+    const unsigned bal = __ballot_sync(0xffffffffu, ok);
+    const int pre = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
+    if (lane < pre) f(v);
+    count += pre;
+    if (pre < 32) {
+      if (__shfl_sync(0xffffffffu, v, pre) != -1) *bad = true;
+      break;
+    }
+    carry = __shfl_sync(0xffffffffu, v, 31);
+  }
+  return count;
+}
+
+// The key tiles of a row tile's selected blocks, ascending: set bits of a
+// bitmap over the blocks, `nsub` tiles each, up to the last tile that any row
+// may look at.
+struct TileIter {
+  const uint32_t* bits;
+  int words, nsub, tiles;  // tiles: ceil(largest limit / kKeyTile)
+  int w, blk, sub;
+  uint32_t cur;
+  __device__ __forceinline__ TileIter(const uint32_t* bits_, int nb, int nsub_, int max_limit)
+      : bits(bits_), words((nb + 31) / 32), nsub(nsub_), tiles((max_limit + kKeyTile - 1) / kKeyTile), w(-1),
+        blk(-1), sub(0), cur(0) {}
+  __device__ __forceinline__ bool next() {
+    if (blk >= 0 && sub + 1 < nsub && blk * nsub + sub + 1 < tiles) {
+      ++sub;
+      return true;
+    }
+    while (cur == 0) {
+      if (++w >= words) return false;
+      cur = bits[w];
+    }
+    const int bit = __ffs(cur) - 1;
+    cur &= cur - 1;
+    blk = w * 32 + bit;
+    sub = 0;
+    return true;
+  }
+  __device__ __forceinline__ int tile() const { return blk * nsub + sub; }
+};
+
+// One row's own walk through its slots beside the tile walk.
+struct SlotCursor {
+  const int32_t* slots;
+  int ptr, count, cur, nxt;
+  __device__ __forceinline__ SlotCursor(const int32_t* s, int n) : slots(s), ptr(0), count(n) {
+    cur = n > 0 ? s[0] : kNoBlock;
+    nxt = n > 1 ? s[1] : kNoBlock;
+  }
+  __device__ __forceinline__ bool has(int blk) {  // blk ascending from call to call
+    while (cur < blk) {
+      cur = nxt;
+      ++ptr;
+      nxt = ptr + 1 < count ? slots[ptr + 1] : kNoBlock;
+    }
+    return cur == blk;
+  }
+};
+
+// 64 key rows from `row0` of a [rows, D] bf16 matrix into a swizzled tile, rows
+// from `valid` on as zeros (what lies behind a sequence may hold anything, and
+// 0 * NaN would reach every row). `lanes` threads take part.
+template <int D>
+__device__ __forceinline__ void load_key_rows(uint8_t* dst, const uint16_t* src, size_t row0, int valid, int tid,
+                                              int lanes) {
+  constexpr int kChunks = D / 8;
+#pragma unroll 8
+  for (int c = tid; c < kKeyTile * kChunks; c += lanes) {
+    const int r = c / kChunks, ch = c - r * kChunks;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < valid) x = *reinterpret_cast<const uint4*>(src + (row0 + r) * D + ch * 8);
+    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch * 8, kKeyTile)) = x;
+  }
+}
+
+// The rows of a row tile (query-major, see above) of a [B, H, Nq, D] bf16
+// tensor into a swizzled 128-row tile; rows without a query as zeros.
+template <int D>
+__device__ __forceinline__ void load_query_rows(uint8_t* dst, const uint16_t* src, const BlockDims& p, int b, int hk,
+                                                int t0, int tid, int threads) {
+  constexpr int kChunks = D / 8;
+#pragma unroll 4
+  for (int c = tid; c < kRowTile * kChunks; c += threads) {
+    const int r = c / kChunks, ch = c - r * kChunks;
+    const int ti = r / p.G, g = r - ti * p.G;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (ti < p.tpt && t0 + ti < p.Nq)
+      x = *reinterpret_cast<const uint4*>(
+          src + ((static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti) * D + ch * 8);
+    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch * 8, kRowTile)) = x;
+  }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, A read from tensor memory.
+__device__ __forceinline__ void umma_f16_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#endif  // __CUDACC__
+
+}  // namespace svoo

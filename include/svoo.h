@@ -48,7 +48,7 @@
  *    4 = plan metadata out of range, 8 = cluster label out of range. While a
  *    timeout bit (1 or 2) is set, the pipelined kernels skip their work, so
  *    clear the word after handling a timeout.
- *  - Limits: 1 <= B*H <= 65535, B*H*N < 2^31 - 256, 1 <= N - n_text, N <= 2^20,
+ *  - Limits (of the calls that take a svoo_shape): 1 <= B*H <= 65535, B*H*N < 2^31 - 256, 1 <= N - n_text, N <= 2^20,
  *    d in {64, 128},
  *    1 <= n_qc, n_kc <= 256, block_q in {64, 128}, 0 <= n_text, iters >= 1.
  *    Inputs must be finite. Centroid member sums are exact (fp64, with
@@ -290,6 +290,110 @@ svoo_status svoo_sparse_attn(const svoo_shape *shape, const void *qp, const void
  * shift > 0; otherwise SVOO_ERR_INVALID_ARG and p is left untouched. */
 svoo_status svoo_snr_top_p(int steps, int warmup, double p_min, double tau, double shift,
                            float *p);
+
+/* ------------------------------------------------------------------ block-selected attention
+ * Attention of language models over the key blocks that every query selects by
+ * a cheap score, its gradient, and its form for single tokens over a cache.
+ * The H query heads form groups of H / Hkv that share a key head and one
+ * selection; the N-token shape limits of this header's other calls do not
+ * apply, those of svoo_block_shape do. */
+
+/* Shape of one call.
+ *  q, o : bf16 [B][H][Nq][d];  k, v : bf16 [B][Hkv][cap][d], of which the first
+ *  Nk rows of every head are keys (cap > Nk: a view into a longer buffer).
+ *  lengths (int32 [B], DEVICE, may be NULL = Nk): the valid keys of every
+ *  sequence, 0 <= lengths[b] <= Nk (clamped). What lies behind them is never
+ *  used and may hold anything, NaN included.
+ *  Position of query i: q_start + i, or with q_start = -1 lengths[b] - Nq + i
+ *  (the queries are the last Nq tokens of their sequence). Causal: a query sees
+ *  the keys up to its own position, and nothing when its position is outside
+ *  [0, lengths[b]). Not causal: every query sees all keys of its sequence.
+ *  Limits: 1 <= H / Hkv <= 128, B*H <= 65535, 0 <= Nq, 1 <= Nk <= cap <= 2^20,
+ *  B*H*Nq and B*Hkv*cap < 2^31 - 256, d in {64, 128}, block a multiple of 64
+ *  up to 1024, 1 <= n_sel <= 256, sink + local <= n_sel, local >= 1 when causal
+ *  and 0 when not. Valid rows of q, k, v must be finite. */
+typedef struct {
+    int B, H, Hkv;
+    int Nq, Nk, cap;
+    int d;
+    int block;   /* keys per block */
+    int n_sel;   /* blocks per query, forced ones included */
+    int sink;    /* the first blocks, kept by every query */
+    int local;   /* causal: the query's own block and the local - 1 before it */
+    int causal;  /* 0 or 1 */
+    int q_start; /* position of query 0, or -1 */
+} svoo_block_shape;
+
+/* pool[b][hk][c] = mean of block c's valid keys: fp32 [B][Hkv][ceil(Nk / block)][d],
+ * summed in fp64 and rounded once; a block without keys gets zeros. last > 0
+ * renews only the last `last` blocks that hold keys of each sequence (after a
+ * token was appended, 1), and leaves the others as they are. Uses B, Hkv, Nk,
+ * cap, d and block of the shape. */
+svoo_status svoo_block_pool(const svoo_block_shape *shape, const void *k, const int32_t *lengths,
+                            int last, float *pool, void *stream);
+
+/* idx: int32 [B][Hkv][Nq][n_sel], ascending block ids, then -1. The forced
+ * blocks and the best of the others by
+ *   score(t, c) = (sum over the group's heads of q[t]) . pool[c],
+ * equal scores to the lower block; decided as in fp64. Causal: the blocks up to
+ * the query's own, which is always kept and never scored. A query outside its
+ * sequence selects nothing. */
+svoo_status svoo_block_select(const svoo_block_shape *shape, const void *q, const float *pool,
+                              const int32_t *lengths, int32_t *idx, void *stream);
+
+/* o = softmax(scale q K^T) V and lse (fp32 [B][H][Nq]) = log of the softmax's
+ * denominator, over the keys that the query sees in its selected blocks. idx as
+ * above, from svoo_block_select or anywhere else: a query's list ends at the
+ * first entry that is out of range or not above the one before it, and an entry
+ * other than -1 there sets bit 4 in dev_err. A query without keys gets o = 0,
+ * lse = -inf. sink and local are not used. fp32 softmax and sums; P is rounded
+ * to bf16 for the second product. */
+svoo_status svoo_block_attn(const svoo_block_shape *shape, const void *q, const void *k,
+                            const void *v, const int32_t *idx, const int32_t *lengths, float scale,
+                            void *o, float *lse, int32_t *dev_err, void *stream);
+
+/* Gradient of svoo_block_attn with respect to q, k and v (the selection is a
+ * constant): dq bf16 [B][H][Nq][d]; dk, dv bf16 [B][Hkv][Nk][d], contiguous
+ * whatever cap is, zero for keys that no query attends to. o, lse: what the
+ * forward call wrote. grad_o: bf16 [B][H][Nq][d]. Every sum runs in a fixed
+ * order, so equal calls give equal bits. The workspace (256-byte aligned) must
+ * not be shared by calls that overlap on the GPU. */
+size_t svoo_block_attn_backward_workspace_size(const svoo_block_shape *shape);
+svoo_status svoo_block_attn_backward(const svoo_block_shape *shape, const void *q, const void *k,
+                                     const void *v, const void *o, const float *lse,
+                                     const void *grad_o, const int32_t *idx, const int32_t *lengths,
+                                     float scale, void *dq, void *dk, void *dv, void *workspace,
+                                     size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/* One token per sequence (Nq = 1) over a cache of cap slots, all valid ones
+ * visible (the order of the slots does not matter; causal and q_start are not
+ * used): o bf16 [B][H][1][d], lse fp32 [B][H][1].
+ *  idx (int32 [B][Hkv][1][n_sel], may be NULL): only the slots of those blocks.
+ *  weight (fp32 [B][Hkv][cap], may be NULL): weight[slot] += sum over the
+ *  group's heads of the slot's softmax weight, for every valid slot. idx and
+ *  weight together are SVOO_ERR_UNSUPPORTED.
+ * Workspace: svoo_cache_attn_workspace_size(shape, idx != NULL, weight != NULL)
+ * bytes, 256-byte aligned, not shared by calls that overlap on the GPU. */
+size_t svoo_cache_attn_workspace_size(const svoo_block_shape *shape, int selected, int weights);
+svoo_status svoo_cache_attn(const svoo_block_shape *shape, const void *q, const void *k,
+                            const void *v, const int32_t *lengths, const int32_t *idx, float scale,
+                            float *weight, void *o, float *lse, void *workspace,
+                            size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/* Brings every sequence that holds more than `keep` slots down to `keep`, in
+ * place and for each key head by itself. Kept are the slots of the first `sink`
+ * positions (pos < sink), those of the last `recent` (of the largest position
+ * in the cache), then the heaviest by weight; equal weights keep the lower slot,
+ * NaN counts as the lightest. Kept rows stay where they are, except that the
+ * i-th evicted slot below `keep` receives the i-th kept one at or behind it: k,
+ * v (bf16 [B][Hkv][cap][d]), weight (fp32 [B][Hkv][cap]) and pos (int32
+ * [B][Hkv][cap], the token position of every slot) move together. Slots at or
+ * behind `keep` are left as they were. lengths[b] becomes min(lengths[b], keep).
+ * Requires 1 <= keep, 0 <= sink, recent, sink + recent <= keep. */
+size_t svoo_cache_evict_workspace_size(int B, int Hkv, int cap, int keep);
+svoo_status svoo_cache_evict(int B, int Hkv, int cap, int d, int keep, int sink, int recent,
+                             void *k, void *v, float *weight, int32_t *pos, int32_t *lengths,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 const char *svoo_status_string(svoo_status s);
 
