@@ -83,7 +83,8 @@ _SIGS = {
     "svoo_psa_mask": (_I, [_SP, _I, _I, _I, _I, _I, _I, _P, _I, _PP, _P, _P, _P]),
     "svoo_snr_top_p": (_I, [_I, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P]),
     "svoo_block_pool": (_I, [_BP, _P, _P, _I, _P, _P]),
-    "svoo_block_select": (_I, [_BP, _P, _P, _P, _P, _P]),
+    "svoo_block_select_workspace_size": (_SZ, [_BP]),
+    "svoo_block_select": (_I, [_BP, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "svoo_block_attn": (_I, [_BP, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P]),
     "svoo_block_attn_backward_workspace_size": (_SZ, [_BP]),
     "svoo_block_attn_backward": (_I, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _SZ, _P, _P]),
@@ -561,7 +562,7 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
 
 
 def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: Optional[int] = None,
-                 idx=None, stream=None) -> torch.Tensor:
+                 idx=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
     """The blocks that every query selects: int32 [B, Hkv, Nq, n_sel], ascending, -1 behind them.
 
     n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
@@ -578,9 +579,13 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
         idx = torch.empty(B, Hkv, Nq, max(cfg.n_sel, 0), dtype=torch.int32, device=q.device)
     sh = BlockShape(B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local,
                     1 if cfg.causal else 0, n_keys - Nq if q_start is None else q_start)
+    L = load()
+    if workspace is None:
+        workspace = torch.empty(L.svoo_block_select_workspace_size(ctypes.byref(sh)), dtype=torch.uint8,
+                                device=q.device)
     with _on_device(q):
-        _check(load().svoo_block_select(ctypes.byref(sh), _ptr(q), _ptr(pool), _ptr(lengths), _ptr(idx),
-                                        _stream(stream)), "svoo_block_select")
+        _check(L.svoo_block_select(ctypes.byref(sh), _ptr(q), _ptr(pool), _ptr(lengths), _ptr(idx), _ptr(workspace),
+                                   workspace.numel(), _ptr(dev_err), _stream(stream)), "svoo_block_select")
     return idx
 
 
@@ -650,7 +655,7 @@ def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[i
     with torch.no_grad():
         err = _err_buf(dev_err, q.device)
         pool = block_pool(k, cfg, lengths)
-        idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start)
+        idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start, dev_err=err)
     o, lse = _BlockAttn.apply(q, k, v, idx, cfg, lengths, q_start, err)
     return o, dict(idx=idx, lse=lse, pool=pool, dev_err=err)
 

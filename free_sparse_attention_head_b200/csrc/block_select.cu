@@ -295,6 +295,580 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 }
 
+// ------------------------------------------------------------------ select, many queries
+//
+// 128 queries of one key head per CTA, their scores from the tensor cores: the
+// queries' group sums and the means are split into two bf16 parts each (hi, lo;
+// what is left is below 2^-16 of the value), and hi.hi + hi.lo + lo.hi
+// accumulate in fp32. With u = 2^-16 a part product's neglected rest is at most
+// 3 u sum |q_d pool_d|, the 3 D additions at most 3 D 2^-23 of the same sum, and
+// the sum at most |q||pool|: that is the error bound of the border test.
+//
+// A thread owns a query (= TMEM lane) and streams its scores, 64 blocks a step,
+// through a list of at most kList candidates: a score enters when it is not
+// below the running cut; when the list runs full, the cut rises to just below
+// the m-th best so far (minus the border) and the list is packed. Scores never
+// leave the SM. Two CTAs share an SM, so one streams while the other loads.
+// Warps 0-3 stream, 4 loads the means (TMA), 5 issues the products.
+// TMEM: A hi [0, 64), A lo [64, 128), scores [128, 192) and [192, 256).
+
+constexpr int kMmaSelThreads = 192;
+constexpr int kList = 64;         // candidates of a query
+constexpr int kGroup = 16;        // scores between two looks at the list's room
+constexpr int kMaxChosen = 40;    // blocks chosen by score: leaves room for a group and eight ties
+constexpr int kMmaMaxBlocks = 6144;  // exact scores of a whole row fit where the lists were
+
+struct MmaSelSmem {
+  uint64_t full[2], empty[2], s_full[2], s_empty[2], mma_final;
+  uint32_t tmem_base;
+  int abort;
+  int hard;             // queries whose ties overran the list
+  float pool_norm2;
+};
+
+template <int D>
+__host__ __device__ constexpr size_t sel_stage_bytes() {
+  return 2 * static_cast<size_t>(kKeyTile) * D * 2;  // 64 blocks, hi and lo
+}
+template <int D>
+__host__ __device__ constexpr size_t sel_area_bytes() {  // the stages; at other times the group sums, and the selected ids
+  const size_t st = 2 * sel_stage_bytes<D>(), ids = 128 * static_cast<size_t>(64) * 4;
+  return st > ids ? st : ids;
+}
+template <int D>
+constexpr size_t mma_sel_smem() {
+  return sel_area_bytes<D>() + static_cast<size_t>(kList) * 128 * 6 + sizeof(MmaSelSmem);
+}
+static_assert(2 * (mma_sel_smem<128>() + 1024) <= 233472, "two CTAs on an SM");
+
+// fp32 means as bf16 hi and lo parts, 64 blocks per CTA (zeros behind the last
+// block), and the largest squared norm among them
+template <int D>
+__global__ void __launch_bounds__(256)
+    pool_split_kernel(int nb, int nbp, size_t lo_at, const float* __restrict__ pool, uint16_t* __restrict__ parts,
+                      float* __restrict__ norms) {
+  constexpr int kT = D / 4;  // threads per row
+  const int c0 = blockIdx.x * 64, bh = blockIdx.y;
+  __shared__ float best[8];
+  float big = 0.f;
+  for (int i = threadIdx.x; i < 64 * kT; i += 256) {
+    const int c = c0 + i / kT, d = (i % kT) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < nb) x = *reinterpret_cast<const float4*>(pool + (static_cast<size_t>(bh) * nb + c) * D + d);
+    const uint32_t h0 = pack_bf16x2(x.x, x.y), h1 = pack_bf16x2(x.z, x.w);
+    const uint32_t l0 = pack_bf16x2(x.x - __uint_as_float(h0 << 16), x.y - __uint_as_float(h0 & 0xffff0000u));
+    const uint32_t l1 = pack_bf16x2(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xffff0000u));
+    uint16_t* dst = parts + (static_cast<size_t>(bh) * nbp + c) * D + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>(dst + lo_at) = make_uint2(l0, l1);
+    float n2 = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w;
+#pragma unroll
+    for (int o = kT / 2 < 16 ? kT / 2 : 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    big = fmaxf(big, n2);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  if ((threadIdx.x & 31) == 0) best[threadIdx.x >> 5] = big;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) big = fmaxf(big, best[w]);
+    norms[static_cast<size_t>(bh) * gridDim.x + blockIdx.x] = big;
+  }
+}
+
+__device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+template <int D>
+__global__ void __launch_bounds__(kMmaSelThreads, 2)
+    mma_select_kernel(const __grid_constant__ CUtensorMap pmap, BlockDims p, int nbp, const uint16_t* __restrict__ q,
+                      const float* __restrict__ pool, const float* __restrict__ norms,
+                      const int32_t* __restrict__ lengths, int32_t* __restrict__ idx, int* __restrict__ err) {
+  constexpr int kSub = D / 64;
+  constexpr int kTile = kKeyTile * D * 2;     // one part of a stage
+  constexpr int kHalf = kRowTile * D * 2;     // group sums, one part
+  extern __shared__ __align__(1024) uint8_t sel_smem[];
+  uint8_t* stage = sel_smem;
+  float* lv = reinterpret_cast<float*>(sel_smem + sel_area_bytes<D>());  // [kList][128]
+  uint16_t* li = reinterpret_cast<uint16_t*>(lv + kList * 128);
+  MmaSelSmem* S = reinterpret_cast<MmaSelSmem*>(li + kList * 128);
+  int32_t* ids = reinterpret_cast<int32_t*>(sel_smem);  // [128][n_sel], once the products are done
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(sel_smem) & 1023u) {  // the declared alignment has to hold
+    if (tid == 0) report_error(err, kErrBadPlan);
+    return;
+  }
+  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  const int b = blockIdx.y / p.Hkv, hk = blockIdx.y - b * p.Hkv;
+  const int len = seq_len(p, lengths, b);
+  const int t0 = blockIdx.x * kRowTile, nt = min(kRowTile, p.Nq - t0);
+  const uint16_t* qh = q + (static_cast<size_t>(b) * p.H + hk * p.G) * p.Nq * D;
+  const size_t head = static_cast<size_t>(p.Nq) * D;
+  int most = (len + p.block - 1) / p.block;
+  if (p.causal) {
+    const int pos = min(query_pos(p, len, t0 + nt - 1), len - 1);
+    most = pos >= 0 ? pos / p.block + 1 : 0;
+  }
+  const int steps = most > p.n_sel ? (most - p.local + kKeyTile - 1) / kKeyTile : 0;
+
+  if (tid == 0) {
+    S->abort = 0;
+    S->hard = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&S->full[s]), 1);
+      mbar_init(smem_u32(&S->empty[s]), 1);
+      mbar_init(smem_u32(&S->s_full[s]), 1);
+      mbar_init(smem_u32(&S->s_empty[s]), 4);
+    }
+    mbar_init(smem_u32(&S->mma_final), 1);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    float big = 0.f;
+    for (int i = lane; i < nbp / 64; i += 32)
+      big = fmaxf(big, norms[static_cast<size_t>(blockIdx.y) * (nbp / 64) + i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    if (lane == 0) S->pool_norm2 = big;
+  }
+  if (warp == 5) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&S->tmem_base), 256);
+    tmem_relinquish();
+  }
+  if (steps > 0) {
+    // group sums: coalesced loads, fp32 sums, bf16 parts to shared memory
+    constexpr int kChunks = D / 8;
+    for (int c = tid; c < kRowTile * kChunks; c += kMmaSelThreads) {
+      const int r = c / kChunks, ch = c - r * kChunks;
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (r < nt) {
+        const uint16_t* src = qh + static_cast<size_t>(t0 + r) * D + ch * 8;
+#pragma unroll 4
+        for (int g = 0; g < p.G; ++g) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + g * head);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[2 * i] += __uint_as_float(w[i] << 16);
+            a[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+          }
+        }
+      }
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
+        l[i] = pack_bf16x2(a[2 * i] - __uint_as_float(h[i] << 16), a[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+      }
+      const uint32_t off = r * D * 2 + ((ch ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(stage + off) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(stage + kHalf + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  volatile int* abort = &S->abort;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  float q2 = 0.f;
+  if (steps > 0 && warp < 4) {
+    // this query's parts into tensor memory, and its norm
+#pragma unroll
+    for (int c4 = 0; c4 < D / 32; ++c4) {
+      uint32_t h[16], l[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t off = tid * D * 2 + (((c4 * 4 + i) ^ (tid & 7)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + off);
+        const uint4 y = *reinterpret_cast<const uint4*>(stage + kHalf + off);
+        h[4 * i] = x.x, h[4 * i + 1] = x.y, h[4 * i + 2] = x.z, h[4 * i + 3] = x.w;
+        l[4 * i] = y.x, l[4 * i + 1] = y.y, l[4 * i + 2] = y.z, l[4 * i + 3] = y.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = __uint_as_float(h[i] << 16) + __uint_as_float(l[i] << 16);
+        const float y = __uint_as_float(h[i] & 0xffff0000u) + __uint_as_float(l[i] & 0xffff0000u);
+        q2 = fmaf(x, x, fmaf(y, y, q2));
+      }
+      tmem_st16(lane_base + c4 * 16, h);
+      tmem_st16(lane_base + 64 + c4 * 16, l);
+    }
+    tmem_wait_st();
+  }
+  fence_proxy_async_smem();  // the staging area goes to the TMA
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int armed = -1;
+
+  const Candidates cd = warp < 4 && tid < nt ? candidates(p, len, t0 + tid) : Candidates{0, 0, 0};
+  const bool all = cd.nc <= p.n_sel;                  // no choice to make
+  const int m = p.n_sel - (cd.nc - (cd.hi - cd.lo));  // to be chosen by score
+  // twice the error bound, with a tenth more for the fp32 norms and this product
+  const float e2 = 2.2f * (3.f * 1.52587890625e-5f + 3.f * D * 1.1920929e-7f) * sqrtf(q2) * sqrtf(S->pool_norm2);
+  int cnt = 0;
+  bool hard = false;
+  float* mv = lv + (tid & 127);
+  uint16_t* mi = li + (tid & 127);
+
+  if (warp == 4) {
+    if (lane == 0 && steps > 0) {
+      tma_prefetch_desc(&pmap);
+      const int row0 = blockIdx.y * nbp, lo_row = p.B * p.Hkv * nbp;
+      for (int j = 0; j < steps; ++j) {
+        const int st = j & 1;
+        if (j >= 2 && !mbar_wait(smem_u32(&S->empty[st]), ((j - 2) >> 1) & 1, abort)) break;
+        const uint32_t bar = smem_u32(&S->full[st]), dst = smem_u32(stage) + st * 2 * kTile;
+        mbar_arrive_expect_tx(bar, 2 * kTile);
+        for (int s = 0; s < kSub; ++s) {
+          tma_load_2d(&pmap, dst + s * kKeyTile * 128, bar, s * 64, row0 + j * kKeyTile);
+          tma_load_2d(&pmap, dst + kTile + s * kKeyTile * 128, bar, s * 64, lo_row + row0 + j * kKeyTile);
+        }
+        armed = j;
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
+      for (int j = 0; j < steps; ++j) {
+        const int st = j & 1;
+        if (!mbar_wait(smem_u32(&S->full[st]), (j >> 1) & 1, abort)) break;
+        if (j >= 2 && !mbar_wait(smem_u32(&S->s_empty[st]), ((j - 2) >> 1) & 1, abort)) break;
+        tc_fence_after();
+        const uint32_t u = smem_u32(stage) + st * 2 * kTile, d = tmem + 128 + st * 64;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
+          const uint64_t bh = sw128_desc(u + off, 16, 1024), bl = sw128_desc(u + kTile + off, 16, 1024);
+          umma_f16_a_tmem(d, tmem + kk * 8, bh, idesc, kk > 0 ? 1u : 0u);
+          umma_f16_a_tmem(d, tmem + kk * 8, bl, idesc, 1u);
+          umma_f16_a_tmem(d, tmem + 64 + kk * 8, bh, idesc, 1u);
+        }
+        umma_commit(smem_u32(&S->s_full[st]));
+        umma_commit(smem_u32(&S->empty[st]));
+      }
+      umma_commit(smem_u32(&S->mma_final));
+      mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
+    }
+  } else {
+    const int lo_c = all || m <= 0 ? 0 : cd.lo, hi_c = all || m <= 0 ? 0 : cd.hi;
+    float cut = -3.402823466e38f;  // nothing below it can be among the m best
+    auto prune = [&]() {
+      // a value that m to m + 6 of the list's entries reach
+      const int nmax = warp_max(cnt);
+      float lo = INFINITY, hi = -INFINITY;
+      for (int i = 0; i < nmax; ++i) {
+        const float x = mv[i * 128];
+        if (i < cnt) {
+          lo = fminf(lo, x);
+          hi = fmaxf(hi, x);
+        }
+      }
+      bool go = cnt > m + 6;
+      for (int it = 0; it < 32 && __any_sync(0xffffffffu, go); ++it) {
+        const float mid = 0.5f * lo + 0.5f * hi;
+        int n = 0;
+#pragma unroll 8
+        for (int i = 0; i < nmax; ++i) n += i < cnt && mv[i * 128] >= mid;
+        if (go) {
+          if (mid <= lo || mid >= hi) go = false;
+          else if (n >= m) {
+            lo = mid;
+            go = n > m + 6;
+          } else {
+            hi = mid;
+          }
+        }
+      }
+      if (cnt > m) cut = fmaxf(cut, lo - e2);
+      int w = 0;
+      for (int i = 0; i < nmax; ++i) {
+        const float x = mv[i * 128];
+        const uint16_t c = mi[i * 128];
+        if (i < cnt && x >= cut) {
+          mv[w * 128] = x;
+          mi[w * 128] = c;
+          ++w;
+        }
+      }
+      cnt = w;
+      if (cnt + kGroup > kList) {  // more ties than the list holds
+        hard = true;
+        cnt = 0;
+        cut = INFINITY;
+      }
+    };
+    for (int j = 0; j < steps; ++j) {
+      const int st = j & 1, c0 = j * kKeyTile;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort))) break;
+      tc_fence_after();
+      float s[kKeyTile];
+      tmem_ld32f(lane_base + 128 + st * 64, s);
+      tmem_ld32f(lane_base + 128 + st * 64 + 32, s + 32);
+      tmem_wait_ld_f(s);
+      tmem_wait_ld_f(s + 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->s_empty[st]));
+      if (!__all_sync(0xffffffffu, lo_c <= c0 && hi_c >= c0 + kKeyTile)) {
+#pragma unroll
+        for (int c = 0; c < kKeyTile; ++c)
+          if (c0 + c < lo_c || c0 + c >= hi_c) s[c] = -INFINITY;
+      }
+#pragma unroll
+      for (int g = 0; g < kKeyTile / kGroup; ++g) {
+        if (__any_sync(0xffffffffu, cnt + kGroup > kList)) prune();
+#pragma unroll
+        for (int c = 0; c < kGroup; ++c) {
+          const float x = s[g * kGroup + c];
+          if (x >= cut) {
+            mv[cnt * 128] = x;
+            mi[cnt * 128] = static_cast<uint16_t>(c0 + g * kGroup + c);
+            ++cnt;
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort) {
+    if (tid == 0) report_error(err, kErrTimeoutAttn);
+    if (warp == 4 && lane == 0)
+      for (int j = max(0, armed - 1); j <= armed; ++j) mbar_wait_cleanup(smem_u32(&S->full[j & 1]), (j >> 1) & 1);
+  } else if (warp < 4) {
+    // m-th best of the list, and whether the border is clear
+    const bool pick = !all && m > 0 && !hard && cnt > m;
+    const int nmax = warp_max(pick ? cnt : 0);
+    float lo = INFINITY, hi = -INFINITY;
+    for (int i = 0; i < nmax; ++i) {
+      const float x = mv[i * 128];
+      if (i < cnt) {
+        lo = fminf(lo, x);
+        hi = fmaxf(hi, x);
+      }
+    }
+    bool go = pick;
+    int n = cnt;
+    for (int it = 0; it < 40 && __any_sync(0xffffffffu, go); ++it) {
+      const float mid = 0.5f * lo + 0.5f * hi;
+      int k = 0;
+#pragma unroll 8
+      for (int i = 0; i < nmax; ++i) k += i < cnt && mv[i * 128] >= mid;
+      if (go) {
+        if (mid <= lo || mid >= hi) go = false;
+        else if (k >= m) {
+          lo = mid;
+          n = k;
+          go = k != m;
+        } else {
+          hi = mid;
+        }
+      }
+    }
+    float tau = INFINITY, out = -INFINITY;  // smallest taken, largest left out
+    for (int i = 0; i < nmax; ++i) {
+      const float x = mv[i * 128];
+      if (i < cnt) {
+        if (x >= lo) tau = fminf(tau, x);
+        else out = fmaxf(out, x);
+      }
+    }
+    float above = pick ? tau : -INFINITY;  // scores from here on are taken
+    const bool unclear = pick && !(n == m && tau - out > e2);
+    unsigned todo = __ballot_sync(0xffffffffu, unclear);
+    while (todo) {
+      // one unclear query at a time, the whole warp: its border in fp64
+      const int src = __ffs(todo) - 1, r = (warp << 5) + src;
+      todo &= todo - 1;
+      const float tr = __shfl_sync(0xffffffffu, tau, src), er = __shfl_sync(0xffffffffu, e2, src);
+      const int nr = __shfl_sync(0xffffffffu, cnt, src), mr = __shfl_sync(0xffffffffu, m, src);
+      double qd[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        qd[i] = 0.;
+        for (int g = 0; g < p.G; ++g)
+          qd[i] += static_cast<double>(bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + r) * D + i * 32 + lane]));
+      }
+      int sure = 0, near_n = 0;
+      double ex[2] = {0., 0.};
+      bool near[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = h * 32 + lane;
+        const float x = i < nr ? lv[i * 128 + r] : -INFINITY;
+        sure += __popc(__ballot_sync(0xffffffffu, x > tr + er));
+        near[h] = i < nr && x <= tr + er && x >= tr - er;
+        unsigned bal = __ballot_sync(0xffffffffu, near[h]);
+        near_n += __popc(bal);
+        while (bal) {
+          const int at = __ffs(bal) - 1;
+          bal &= bal - 1;
+          const float* pc = pool + (static_cast<size_t>(blockIdx.y) * p.nb + li[(h * 32 + at) * 128 + r]) * D + lane;
+          double x64 = 0.;
+#pragma unroll
+          for (int d = 0; d < D / 32; ++d) x64 = fma(qd[d], static_cast<double>(pc[d * 32]), x64);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) x64 += __shfl_xor_sync(0xffffffffu, x64, o);
+          if (lane == at) ex[h] = x64;
+        }
+      }
+      const int need = mr - sure;
+      int rank[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        unsigned bal = __ballot_sync(0xffffffffu, near[h]);
+        while (bal) {
+          const int at = __ffs(bal) - 1;
+          bal &= bal - 1;
+          const double y = __shfl_sync(0xffffffffu, ex[h], at);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) rank[k] += y > ex[k] || (y == ex[k] && h * 32 + at < k * 32 + lane);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (near[h]) lv[(h * 32 + lane) * 128 + r] = rank[h] < need ? INFINITY : -INFINITY;
+      if (lane == src) above = tr + er;
+      __syncwarp();
+    }
+    if (tid < nt) {
+      int32_t* row = ids + tid * p.n_sel;
+      int w = 0;
+      if (all) {
+        for (; w < cd.nc; ++w) row[w] = w;
+      } else if (!hard) {
+        for (; w < cd.lo; ++w) row[w] = w;
+        if (m > 0)
+          for (int i = 0; i < cnt; ++i)
+            if (mv[i * 128] >= above && w < p.n_sel) row[w++] = mi[i * 128];
+        for (int c = cd.hi; c < cd.nc && w < p.n_sel; ++c) row[w++] = c;
+      }
+      for (; w < p.n_sel; ++w) row[w] = -1;
+    }
+    if (hard) atomicAdd(&S->hard, 1);
+  }
+  __syncthreads();
+  const bool fine = !*abort;
+  if (fine && S->hard && warp < 4) {
+    // Rows whose ties overran the list, one at a time: every free candidate in
+    // fp64 (a lane each) where the lists were, the m-th best by bisection.
+    double* ex = reinterpret_cast<double*>(lv);
+    for (int w = 0; w < 4; ++w) {
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (warp != w) continue;
+      unsigned todo = __ballot_sync(0xffffffffu, hard);
+      while (todo) {
+        const int src = __ffs(todo) - 1, r = (warp << 5) + src;
+        todo &= todo - 1;
+        const int lo_c = __shfl_sync(0xffffffffu, cd.lo, src), hi_c = __shfl_sync(0xffffffffu, cd.hi, src);
+        const int nc = __shfl_sync(0xffffffffu, cd.nc, src), mr = __shfl_sync(0xffffffffu, m, src);
+        unsigned long long lo = ~0ull, hi = 0ull;
+        auto key = [](double x) {
+          const unsigned long long u = x == 0. ? 0ull : __double_as_longlong(x);
+          return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+        };
+        for (int c = lo_c + lane; c < hi_c; c += 32) {
+          double x = 0.;
+          for (int d = 0; d < D; ++d) {
+            double a = 0.;
+            for (int g = 0; g < p.G; ++g)
+              a += static_cast<double>(bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + r) * D + d]));
+            x = fma(a, static_cast<double>(pool[(static_cast<size_t>(blockIdx.y) * p.nb + c) * D + d]), x);
+          }
+          ex[c] = x;
+          lo = min(lo, key(x));
+          hi = max(hi, key(x));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        __syncwarp();
+        while (lo < hi) {
+          const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+          int k = 0;
+          for (int c = lo_c + lane; c < hi_c; c += 32) k += key(ex[c]) >= mid;
+          k = __reduce_add_sync(0xffffffffu, k);
+          if (k >= mr) lo = mid;
+          else hi = mid - 1;
+        }
+        int over = 0;
+        for (int c = lo_c + lane; c < hi_c; c += 32) over += key(ex[c]) > lo;
+        over = __reduce_add_sync(0xffffffffu, over);
+        int equal = 0, at = 0;
+        for (int c0 = 0; c0 < nc; c0 += 32) {
+          const int c = c0 + lane;
+          const bool forced = c < nc && (c < lo_c || c >= hi_c), open = c < nc && !forced;
+          const unsigned eq = __ballot_sync(0xffffffffu, open && key(ex[c]) == lo);
+          const bool take = forced || (open && (key(ex[c]) > lo || (((eq >> lane) & 1u) &&
+                                                                    equal + __popc(eq & ((1u << lane) - 1u)) < mr - over)));
+          equal += __popc(eq);
+          const unsigned bal = __ballot_sync(0xffffffffu, take);
+          const int to = at + __popc(bal & ((1u << lane) - 1u));
+          if (take && to < p.n_sel) ids[r * p.n_sel + to] = c;
+          at += __popc(bal);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncthreads();
+  if (fine) {
+    int32_t* out = idx + (static_cast<size_t>(blockIdx.y) * p.Nq + t0) * p.n_sel;
+    for (int i = tid; i < nt * p.n_sel; i += kMmaSelThreads) out[i] = ids[i];
+  }
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// The tensor-core kernel from 64 queries on, while its lists and ids fit; below
+// that its 128-query tile would be mostly empty.
+inline bool mma_select(const BlockDims& p) {
+  return p.Nq >= 64 && p.n_sel <= 64 && p.n_sel - p.sink - p.local <= kMaxChosen && p.nb <= kMmaMaxBlocks;
+}
+
+struct SelectPlan {
+  int nbp;
+  uint16_t* parts;
+  float* norms;
+  size_t bytes;
+};
+SelectPlan select_plan(const BlockDims& p, int d, void* ws) {
+  SelectPlan s;
+  s.nbp = (p.nb + 63) / 64 * 64;
+  const size_t rows = static_cast<size_t>(p.B) * p.Hkv * s.nbp;
+  Carver c(ws);
+  const bool mma = mma_select(p);
+  s.parts = c.take<uint16_t>(mma ? 2 * rows * d : 0);
+  s.norms = c.take<float>(mma ? rows / 64 : 0);
+  s.bytes = (c.used + 255) / 256 * 256;
+  return s;
+}
+
+template <int D>
+svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* pool, const int32_t* lengths,
+                              int32_t* idx, void* ws, int32_t* dev_err, cudaStream_t st) {
+  const SelectPlan s = select_plan(p, D, ws);
+  const int BHk = p.B * p.Hkv;
+  const uint64_t rows = static_cast<uint64_t>(BHk) * s.nbp;
+  CUtensorMap pm;
+  if (encode_tiled_2d(&pm, s.parts, 2 * rows, D, kKeyTile, 64) != CUDA_SUCCESS) return SVOO_ERR_CUDA;
+  if (cudaFuncSetAttribute(mma_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(mma_sel_smem<D>())) != cudaSuccess)
+    return SVOO_ERR_CUDA;
+  pool_split_kernel<D><<<dim3(s.nbp / 64, BHk), 256, 0, st>>>(p.nb, s.nbp, rows * D, pool, s.parts, s.norms);
+  mma_select_kernel<D><<<dim3((p.Nq + kRowTile - 1) / kRowTile, BHk), kMmaSelThreads, mma_sel_smem<D>(), st>>>(
+      pm, p, s.nbp, static_cast<const uint16_t*>(q), pool, s.norms, lengths, idx, dev_err);
+  return launch_status();
+}
+
 template <int D, int TQ>
 svoo_status launch_select(const BlockDims& p, const void* q, const float* pool, const int32_t* lengths, int32_t* idx,
                           cudaStream_t st) {
@@ -339,13 +913,26 @@ extern "C" svoo_status svoo_block_pool(const svoo_block_shape* shape, const void
   return launch_status();
 }
 
+extern "C" size_t svoo_block_select_workspace_size(const svoo_block_shape* shape) {
+  if (!block_shape_ok(shape)) return 0;
+  const size_t n = select_plan(block_dims(shape), shape->d, nullptr).bytes;
+  return n ? n : 256;
+}
+
 extern "C" svoo_status svoo_block_select(const svoo_block_shape* shape, const void* q, const float* pool,
-                                         const int32_t* lengths, int32_t* idx, void* stream) {
-  if (!block_shape_ok(shape) || !q || !pool || !idx) return SVOO_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4)) return SVOO_ERR_INVALID_ARG;
-  if (shape->Nq == 0) return SVOO_OK;
+                                         const int32_t* lengths, int32_t* idx, void* workspace, size_t workspace_bytes,
+                                         int32_t* dev_err, void* stream) {
+  if (!block_shape_ok(shape) || !q || !pool || !idx || !workspace) return SVOO_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
+    return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
+  if (workspace_bytes < select_plan(p, shape->d, nullptr).bytes) return SVOO_ERR_WORKSPACE;
+  if (shape->Nq == 0) return SVOO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (mma_select(p)) {
+    if (shape->d == 128) return launch_mma_select<128>(p, q, pool, lengths, idx, workspace, dev_err, st);
+    return launch_mma_select<64>(p, q, pool, lengths, idx, workspace, dev_err, st);
+  }
   if (shape->d == 128) return launch_select_d<128>(p, q, pool, lengths, idx, st);
   return launch_select_d<64>(p, q, pool, lengths, idx, st);
 }

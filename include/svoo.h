@@ -337,9 +337,12 @@ svoo_status svoo_block_pool(const svoo_block_shape *shape, const void *k, const 
  *   score(t, c) = (sum over the group's heads of q[t]) . pool[c],
  * equal scores to the lower block; decided as in fp64. Causal: the blocks up to
  * the query's own, which is always kept and never scored. A query outside its
- * sequence selects nothing. */
+ * sequence selects nothing. The workspace (256-byte aligned) must not be shared
+ * by calls that overlap on the GPU. */
+size_t svoo_block_select_workspace_size(const svoo_block_shape *shape);
 svoo_status svoo_block_select(const svoo_block_shape *shape, const void *q, const float *pool,
-                              const int32_t *lengths, int32_t *idx, void *stream);
+                              const int32_t *lengths, int32_t *idx, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_err, void *stream);
 
 /* o = softmax(scale q K^T) V and lse (fp32 [B][H][Nq]) = log of the softmax's
  * denominator, over the keys that the query sees in its selected blocks. idx as

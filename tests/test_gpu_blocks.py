@@ -105,3 +105,35 @@ def test_gradient(case):
         assert ((x - y).abs() <= tol).all(), (name, float((x - y).abs().max()), float(y.abs().max()))
         if float(y.norm()) > 0:
             assert float((x - y).norm() / y.norm()) <= 2 * U, (name, float((x - y).norm() / y.norm()))
+
+
+@pytest.mark.parametrize("kind", ["plain", "rising", "ties", "equal", "zero", "close", "far"])
+@pytest.mark.parametrize("shape", [(1, 3, 1, 1000, 64, 64, 6), (1, 4, 2, 700, 128, 64, 12), (2, 2, 2, 3000, 64, 64, 44),
+                                   (1, 2, 1, 65 * 64, 64, 64, 60)])
+def test_selection_of_many_queries(shape, kind):
+    """Orders of scores that a streaming choice can trip over: rising along the sequence, few distinct blocks,
+    all equal, differences below fp32's, magnitudes far apart."""
+    B, H, Hkv, N, d, block, n_sel = shape
+    q, k, _ = make(B, H, Hkv, N, N, d, seed=11)
+    nb = -(-N // block)
+    g = torch.Generator().manual_seed(12)
+    base = torch.randn(B, Hkv, 1, d, generator=g)
+    if kind == "rising":  # the mean grows along the queries' common direction
+        q = (q.float() * 0.1 + base.repeat_interleave(H // Hkv, 1)).bfloat16()
+        k = (k.float() * 0.01 + base * torch.arange(N)[:, None] / N).bfloat16()
+    if kind in ("ties", "equal"):
+        n = 3 if kind == "ties" else 1
+        rows = torch.randn(B, Hkv, n, d, generator=g)
+        which = torch.randint(n, (nb,), generator=g).repeat_interleave(block)[:N]
+        k = rows[:, :, which].bfloat16()
+    if kind == "zero":
+        k = torch.zeros_like(k)
+    if kind == "close":  # one key of each block in its last bit off a common block
+        k = torch.randn(B, Hkv, block, d, generator=g).bfloat16().repeat(1, 1, nb, 1)[:, :, :N].clone()
+        k.view(torch.int16)[:, :, ::block, ::7] ^= torch.randint(2, k[:, :, ::block, ::7].shape, generator=g, dtype=torch.int16)
+    if kind == "far":
+        k = (k.float() * 10.0 ** torch.randint(-6, 7, (B, Hkv, nb, 1), generator=g).repeat_interleave(block, 2)[:, :, :N]).bfloat16()
+    cfg = svoo.BlockConfig(block=block, n_sel=n_sel, sink=1, local=2)
+    pool = svoo.block_pool(k.cuda(), cfg)
+    idx = svoo.block_select(q.cuda(), pool, cfg, N)
+    assert torch.equal(idx.cpu(), ref.select(q, pool.cpu(), cfg, N))
