@@ -203,9 +203,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     // m: running maximum in log2 units, moved when it grows by more than 2^8
     // (P stays at most 2^8); l: sum of P in 32 bits, before P is rounded to
-    // bf16 for the second product; lr: sum of the rounded P, which o is
-    // divided by, so that its numerator and denominator saw the same rounding
-    float m = -INFINITY, l = 0.f, lr = 0.f;
+    // bf16 for the second product
+    float m = -INFINITY, l = 0.f;
     bool ok = true;
     int j = 0;
     for (; it.next(); ++j) {
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const uint32_t s_col = lane_base + st * 64;
       const int nv = mine.has(it.blk) ? max(0, min(kKeyTile, lim - it.tile() * kKeyTile)) : 0;
       const bool some = __any_sync(0xffffffffu, nv > 0);
-      const bool all = __all_sync(0xffffffffu, nv == kKeyTile);
+      const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort));
       if (!ok) break;
       tc_fence_after();
@@ -224,14 +223,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tmem_ld32f(s_col + 32, s + 32);
         tmem_wait_ld_f(s);
         tmem_wait_ld_f(s + 32);
-        if (!all) {
+        if (!whole) {  // a row's own limit falls into this tile
 #pragma unroll
           for (int c = 0; c < kKeyTile; ++c)
             if (c >= nv) s[c] = -INFINITY;
         }
         float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c + 7 < kKeyTile + 4; c += 8) {
+        for (int c = 4; c < kKeyTile; c += 8) {
           m4[0] = fmax3(m4[0], s[c], s[c + 1]);
           m4[1] = fmax3(m4[1], s[c + 2], s[c + 3]);
           if (c + 4 < kKeyTile) {
@@ -239,16 +238,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             m4[3] = fmax3(m4[3], s[c + 6], s[c + 7]);
           }
         }
-        const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * scale_log2;
+        const float mx = nv > 0 ? fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * scale_log2 : -INFINITY;
         if (m == -INFINITY) {
           m = mx;  // nothing accumulated yet
         } else if (mx > m + kFwdRescaleLog2) {
           alpha = ex2_approx(m - mx);
           m = mx;
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        const uint64_t sc2 = f2pack(scale_log2, scale_log2), nm2 = f2pack(-ms, -ms);
-        float a8[4] = {0.f, 0.f, 0.f, 0.f}, r8[4] = {0.f, 0.f, 0.f, 0.f};
+        // a row that does not take part: 2^(s - inf) = 0
+        const float nm = nv > 0 ? -m : -INFINITY;
+        const uint64_t sc2 = f2pack(scale_log2, scale_log2), nm2 = f2pack(nm, nm);
+        uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[16];
@@ -259,13 +259,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
             pk[c] = pack_bf16x2(x0, x1);
-            a8[c & 3] += x0 + x1;
-            r8[c & 3] += __uint_as_float(pk[c] << 16) + __uint_as_float(pk[c] & 0xffff0000u);
+            sum2[c & 1] = f2add(f2pack(x0, x1), sum2[c & 1]);
           }
           tmem_st16(s_col + h * 16, pk);
         }
-        l = l * alpha + ((a8[0] + a8[1]) + (a8[2] + a8[3]));
-        lr = lr * alpha + ((r8[0] + r8[1]) + (r8[2] + r8[3]));
+        float a0, a1, a2, a3;
+        f2unpack(sum2[0], a0, a1);
+        f2unpack(sum2[1], a2, a3);
+        l = l * alpha + ((a0 + a1) + (a2 + a3));
       } else {
         uint32_t z[16];
 #pragma unroll
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     if (ok) {
       tc_fence_after();
       const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti;
-      const float inv = lr > 0.f ? 1.f / lr : 0.f;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t x[32];
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
           for (int c8 = 0; c8 < 4; ++c8) {
             uint4 pk = make_uint4(0, 0, 0, 0);
-            if (lr > 0.f) {
+            if (l > 0.f) {
               pk.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * inv, __uint_as_float(x[c8 * 8 + 1]) * inv);
               pk.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * inv, __uint_as_float(x[c8 * 8 + 3]) * inv);
               pk.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * inv, __uint_as_float(x[c8 * 8 + 5]) * inv);

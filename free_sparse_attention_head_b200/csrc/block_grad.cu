@@ -55,12 +55,12 @@ __global__ void __launch_bounds__(256)
 constexpr int kDqThreads = 192;
 
 struct DqSmem {
-  uint64_t kv_full, kv_empty, s_full, ds_full, mma_final;
+  uint64_t k_full[2], k_empty[2], v_full, s_full, ds_full, mma_final;
   uint32_t tmem_base;
   int abort;
   int max_limit;
   int limit[kRowTile];
-  int count[kRowTile];
+  uint16_t count[kRowTile];
 };
 
 template <int D>
@@ -74,11 +74,15 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   constexpr int kKvBytes = kKeyTile * D * 2;
   constexpr int kRowBytes = kRowTile * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* q_s = base;
+  // no room to round up in, if two CTAs are to share an SM: the declared alignment has to hold
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) report_error(err, kErrBadPlan);
+    return;
+  }
+  uint8_t* q_s = smem_raw;
   uint8_t* g_s = q_s + kRowBytes;
-  uint8_t* k_s = g_s + kRowBytes;
-  uint8_t* v_s = k_s + kKvBytes;
+  uint8_t* k_s = g_s + kRowBytes;  // 2 stages
+  uint8_t* v_s = k_s + 2 * kKvBytes;
   DqSmem* S = reinterpret_cast<DqSmem*>(v_s + kKvBytes);
   uint32_t* bits = reinterpret_cast<uint32_t*>(S + 1);
 
@@ -94,8 +98,11 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   if (tid == 0) {
     S->abort = 0;
     S->max_limit = 0;
-    mbar_init(smem_u32(&S->kv_full), 1);
-    mbar_init(smem_u32(&S->kv_empty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&S->k_full[s]), 1);
+      mbar_init(smem_u32(&S->k_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&S->v_full), 1);
     mbar_init(smem_u32(&S->s_full), 1);
     mbar_init(smem_u32(&S->ds_full), 4);
     mbar_init(smem_u32(&S->mma_final), 1);
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kDqThreads, 2)
     });
     if (lane == 0) {
       S->limit[ti] = lim;
-      S->count[ti] = n;
+      S->count[ti] = static_cast<uint16_t>(n);
       atomicMax(&S->max_limit, lim);
     }
   }
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   volatile int* abort = &S->abort;
   const uint32_t q_u = smem_u32(q_s), g_u = smem_u32(g_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
   TileIter it(bits, p.nb, p.nsub, S->max_limit);
-  int armed = -1;
+  int k_armed = -1, v_armed = -1;
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
@@ -140,30 +147,34 @@ __global__ void __launch_bounds__(kDqThreads, 2)
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
     }
-    for (int j = 0; it.next(); ++j) {
-      const int key0 = it.tile() * kKeyTile;
-      if (j >= 1) {
-        int okl = 1;
-        if (lane == 0) okl = mbar_wait(smem_u32(&S->kv_empty), (j - 1) & 1, abort) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, okl, 0)) break;
-      }
-      const uint32_t bar = smem_u32(&S->kv_full);
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      int okl = 1;
+      if (lane == 0) okl = mbar_wait(bar, parity, abort) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, okl, 0) != 0;
+    };
+    auto fill = [&](const CUtensorMap* map, const uint16_t* src, uint8_t* dst, uint32_t bar, int key0) {
       if (len - key0 >= kKeyTile) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar, 2 * kKvBytes);
-          for (int s = 0; s < kSub; ++s) {
-            tma_load_2d(&kmap, k_u + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
-            tma_load_2d(&vmap, v_u + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
-          }
+          mbar_arrive_expect_tx(bar, kKvBytes);
+          for (int s = 0; s < kSub; ++s)
+            tma_load_2d(map, smem_u32(dst) + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
         }
       } else {
-        load_key_rows<D>(k_s, k, row0 + key0, len - key0, lane, 32);
-        load_key_rows<D>(v_s, v, row0 + key0, len - key0, lane, 32);
+        load_key_rows<D>(dst, src, row0 + key0, len - key0, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       }
-      armed = j;
+    };
+    for (int j = 0; it.next(); ++j) {
+      const int st = j & 1, key0 = it.tile() * kKeyTile;
+      if (j >= 2 && !warp_wait(smem_u32(&S->k_empty[st]), ((j - 2) >> 1) & 1)) break;
+      fill(&kmap, k, k_s + st * kKvBytes, smem_u32(&S->k_full[st]), key0);
+      k_armed = j;
+      // V is done with once S and dP are there
+      if (j >= 1 && !warp_wait(smem_u32(&S->s_full), (j - 1) & 1)) break;
+      fill(&vmap, v, v_s, smem_u32(&S->v_full), key0);
+      v_armed = j;
     }
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA issuer
@@ -171,12 +182,19 @@ __global__ void __launch_bounds__(kDqThreads, 2)
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
       const uint32_t idesc_q = idesc_bf16_f32(kRowTile, D, false, true);
       for (int j = 0; it.next(); ++j) {
-        if (!mbar_wait(smem_u32(&S->kv_full), j & 1, abort)) break;
+        const uint32_t kt = k_u + (j & 1) * kKvBytes;
+        if (!mbar_wait(smem_u32(&S->k_full[j & 1]), (j >> 1) & 1, abort)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
-          umma_f16(tmem, sw128_desc(q_u + ro, 16, 1024), sw128_desc(k_u + ko, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+          umma_f16(tmem, sw128_desc(q_u + ro, 16, 1024), sw128_desc(kt + ko, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        if (!mbar_wait(smem_u32(&S->v_full), j & 1, abort)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
           umma_f16(tmem + 64, sw128_desc(g_u + ro, 16, 1024), sw128_desc(v_u + ko, 16, 1024), idesc_s,
                    kk > 0 ? 1u : 0u);
         }
@@ -185,9 +203,9 @@ __global__ void __launch_bounds__(kDqThreads, 2)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kKeyTile / 16; ++kk)
-          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(k_u + kk * 16 * 128, kKeyTile * 128, 1024), idesc_q,
+          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(kt + kk * 16 * 128, kKeyTile * 128, 1024), idesc_q,
                           (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(smem_u32(&S->kv_empty));
+        umma_commit(smem_u32(&S->k_empty[j & 1]));
       }
       umma_commit(smem_u32(&S->mma_final));
       mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
@@ -207,11 +225,16 @@ __global__ void __launch_bounds__(kDqThreads, 2)
     for (; it.next(); ++j) {
       const int nv = mine.has(it.blk) ? max(0, min(kKeyTile, lim - it.tile() * kKeyTile)) : 0;
       const bool some = __any_sync(0xffffffffu, nv > 0);
+      const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort));
       if (!ok) break;
       tc_fence_after();
       uint32_t pk[32];
       if (some) {
+        // P = 2^(s - lse), dS = P (dP - delta); a row that does not take part:
+        // 2^(s - inf) = 0
+        const float nl = nv > 0 ? -lse2 : -INFINITY;
+        const uint64_t sc2 = f2pack(scale_log2, scale_log2), nl2 = f2pack(nl, nl), nd2 = f2pack(-dl, -dl);
         float s[32], x[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -219,13 +242,18 @@ __global__ void __launch_bounds__(kDqThreads, 2)
           tmem_ld32f(lane_base + 64 + h * 32, x);
           tmem_wait_ld_f(s);
           tmem_wait_ld_f(x);
+          if (!whole) {  // the row's own limit falls into this tile
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (h * 32 + c >= nv) s[c] = -INFINITY;
+          }
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const int c0 = h * 32 + 2 * c;
-            const float e0 = ex2_approx(fmaf(s[2 * c], scale_log2, -lse2)) * (x[2 * c] - dl);
-            const float e1 = ex2_approx(fmaf(s[2 * c + 1], scale_log2, -lse2)) * (x[2 * c + 1] - dl);
-            // what is masked may be infinite or NaN: chosen, not multiplied
-            pk[h * 16 + c] = pack_bf16x2(c0 < nv ? e0 : 0.f, c0 + 1 < nv ? e1 : 0.f);
+            float e0, e1;
+            f2unpack(f2fma(f2pack(s[2 * c], s[2 * c + 1]), sc2, nl2), e0, e1);
+            const uint64_t d2 = f2mul(f2pack(ex2_approx(e0), ex2_approx(e1)), f2add(f2pack(x[2 * c], x[2 * c + 1]), nd2));
+            f2unpack(d2, e0, e1);
+            pk[h * 16 + c] = pack_bf16x2(e0, e1);
           }
         }
       } else {
@@ -238,7 +266,7 @@ __global__ void __launch_bounds__(kDqThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->ds_full));
     }
-    if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->kv_empty), (j - 1) & 1, abort));
+    if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->k_empty[(j - 1) & 1]), ((j - 1) >> 1) & 1, abort));
     if (ok) {
       tc_fence_after();
 #pragma unroll
@@ -268,7 +296,11 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   __syncthreads();
   if (*abort) {
     if (tid == 0) report_error(err, kErrTimeoutAttn);
-    if (warp == 4 && lane == 0 && armed >= 0) mbar_wait_cleanup(smem_u32(&S->kv_full), armed & 1);
+    if (warp == 4 && lane == 0) {
+      for (int j = max(0, k_armed - 1); j <= k_armed; ++j)
+        mbar_wait_cleanup(smem_u32(&S->k_full[j & 1]), (j >> 1) & 1);
+      if (v_armed >= 0) mbar_wait_cleanup(smem_u32(&S->v_full), v_armed & 1);
+    }
     __syncthreads();
   }
   if (warp == 5) {
@@ -416,6 +448,7 @@ struct DkvSmem {
   float lse2[2][kRowTile];
   float delta[2][kRowTile];
   uint8_t nv[2][kRowTile];  // valid keys of the row in this key tile
+  int row[kRowTile];        // gather: the rows of the tile being loaded
 };
 
 template <int D>
@@ -424,8 +457,22 @@ constexpr size_t dkv_tile_bytes() {
          4 * static_cast<size_t>(kRowTile) * kKeyTile * 2;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// barrier of the four loader warps, with a vote
+__device__ __forceinline__ bool loaders_agree(bool ok) {
+  uint32_t r;
+  __syncwarp();  // bar takes a warp's threads together
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -505,48 +552,47 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
   if (warp >= 8 && warp < 12) {
     // ---------------------------------------------------------------- row gather
-    const int t = tid - 256;  // one row's scalars per thread
+    const int t = tid - 256;  // one row's list entry and scalars per thread
     constexpr int kChunks = D / 8;
+    const int ch = t % kChunks, r0 = t / kChunks;
+    // row of [B, H, Nq] behind row f of the piece, -1 behind the last; its limit
+    int next = -1, next_nv = 0;
+    auto look = [&](int f) {
+      next = -1;
+      next_nv = 0;
+      if (f < rows) {
+        const long long fr = row0 + f;
+        const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
+        const int tok = toks[e];
+        next = (b * p.H + hk * p.G + g) * p.Nq + tok;
+        next_nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
+      }
+    };
+    if (nj > 0) look(t);
     for (int j = 0; j < nj; ++j) {
       const int st = j & 1;
-      if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->free_[st]), ((j - 2) >> 1) & 1, abort))) break;
-      {
-        const int f = j * kRowTile + t;
-        int nv = 0;
-        float l2 = 0.f, dl = 0.f;
-        if (f < rows) {
-          const long long fr = row0 + f;
-          const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
-          const int tok = toks[e];
-          const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + tok;
-          nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
-          l2 = lse[row] * 1.4426950408889634f;
-          dl = delta[row];
-        }
-        S->nv[st][t] = static_cast<uint8_t>(nv);
-        S->lse2[st][t] = l2;
-        S->delta[st][t] = dl;
-      }
+      const bool free = j < 2 || mbar_wait(smem_u32(&S->free_[st]), ((j - 2) >> 1) & 1, abort);
+      const int row = next, nv = next_nv;
+      S->row[t] = row;
+      if (!loaders_agree(free)) break;  // all four warps go on or leave together
       const uint32_t g_dst = row_u + st * 2 * kRowBytes, q_dst = g_dst + kRowBytes;
-#pragma unroll 4
-      for (int c = t; c < kRowTile * kChunks; c += 128) {
-        const int r = c / kChunks, ch = c - r * kChunks;
-        const int f = j * kRowTile + r;
+#pragma unroll 8
+      for (int r = r0; r < kRowTile; r += 128 / kChunks) {
+        const int src = S->row[r];
         const uint32_t off = sw128_offset(r, ch * 8, kRowTile);
-        if (f < rows) {
-          const long long fr = row0 + f;
-          const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
-          const size_t src = ((static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + toks[e]) * D + ch * 8;
-          cp_async16(g_dst + off, go + src);
-          cp_async16(q_dst + off, q + src);
-        } else {
-          *reinterpret_cast<uint4*>(row_s + (g_dst - row_u) + off) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(row_s + (q_dst - row_u) + off) = make_uint4(0, 0, 0, 0);
-        }
+        const size_t at = static_cast<size_t>(src < 0 ? 0 : src) * D + ch * 8;
+        cp_async16_or_zero(g_dst + off, go + at, src >= 0);
+        cp_async16_or_zero(q_dst + off, q + at, src >= 0);
       }
+      // a row that does not take part has lse = inf, so P = 0
+      S->nv[st][t] = static_cast<uint8_t>(nv);
+      S->lse2[st][t] = nv > 0 ? lse[row] * 1.4426950408889634f : INFINITY;
+      S->delta[st][t] = nv > 0 ? delta[row] : 0.f;
+      look((j + 1) * kRowTile + t);
       cp_async_wait_all();
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&S->full[st]));  // this thread's part of row tile j is in
+      loaders_agree(true);  // S->row is free again
     }
   } else if (warp == 12) {
     // ---------------------------------------------------------------- MMA issuer
@@ -606,6 +652,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       // the row's scalars came with its tile, which S was computed from
       const int nv = S->nv[st][r];
       const float lse2 = S->lse2[st][r], dl = S->delta[st][r];
+      const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
+      const uint64_t sc2 = f2pack(scale_log2, scale_log2), nl2 = f2pack(-lse2, -lse2), nd2 = f2pack(-dl, -dl);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float s[32], x[32];
@@ -613,16 +661,24 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         tmem_ld32f(lane_base + 64 + h * 32, x);
         tmem_wait_ld_f(s);
         tmem_wait_ld_f(x);
+        if (!whole) {  // a row's own limit falls into this tile
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c >= nv) s[c] = -INFINITY;
+        }
 #pragma unroll
         for (int c8 = 0; c8 < 4; ++c8) {
           uint32_t pp[4], ds[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int i = c8 * 8 + 2 * c, col = h * 32 + i;
-            const float e0 = col < nv ? ex2_approx(fmaf(s[i], scale_log2, -lse2)) : 0.f;
-            const float e1 = col + 1 < nv ? ex2_approx(fmaf(s[i + 1], scale_log2, -lse2)) : 0.f;
+            const int i = c8 * 8 + 2 * c;
+            float e0, e1;
+            f2unpack(f2fma(f2pack(s[i], s[i + 1]), sc2, nl2), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
             pp[c] = pack_bf16x2(e0, e1);
-            ds[c] = pack_bf16x2(col < nv ? e0 * (x[i] - dl) : 0.f, col + 1 < nv ? e1 * (x[i + 1] - dl) : 0.f);
+            f2unpack(f2mul(f2pack(e0, e1), f2add(f2pack(x[i], x[i + 1]), nd2)), e0, e1);
+            ds[c] = pack_bf16x2(e0, e1);
           }
           const uint32_t off = sw128_offset(r, h * 32 + c8 * 8, kRowTile);
           *reinterpret_cast<uint4*>(prow + off) = make_uint4(pp[0], pp[1], pp[2], pp[3]);
@@ -636,10 +692,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     // ---------------------------------------------------------------- epilogue
     // warps 0-3 write dv, 4-7 dk: thread = one model dimension (TMEM lane)
-    if (ok && nj > 0) {
-      const int last = nj - 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->free_[last & 1]), (last >> 1) & 1, abort));
-    }
+    // (not free_: this group may be a phase behind it, and a parity tells no more)
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
     if (ok) {
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 + st * 64;
@@ -770,7 +824,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t dq_smem = 1024 + 2 * static_cast<size_t>(kRowTile + kKeyTile) * D * 2 + sizeof(DqSmem) +
+  const size_t dq_smem = static_cast<size_t>(2 * kRowTile + 3 * kKeyTile) * D * 2 + sizeof(DqSmem) +
                          static_cast<size_t>((p.nb + 31) / 32) * 4;
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
   const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
