@@ -30,7 +30,7 @@ constexpr float kFwdRescaleLog2 = 8.0f;
 
 struct FwdSmem {
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done, mma_final;
+  uint64_t s_full[2], p_full[2], mma_final;
   uint32_t tmem_base;
   int abort;
   int max_limit;
@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       mbar_init(smem_u32(&S->s_full[s]), 1);
       mbar_init(smem_u32(&S->p_full[s]), 4);
     }
-    mbar_init(smem_u32(&S->pv_done), 1);
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
@@ -187,7 +186,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           umma_f16_a_tmem(tmem + 128, tmem + st * 64 + kk * 8, bd, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         }
         umma_commit(smem_u32(&S->v_empty[st]));
-        umma_commit(smem_u32(&S->pv_done));
       }
       // every MMA of this thread done before the tensor memory goes back
       umma_commit(smem_u32(&S->mma_final));
@@ -274,30 +272,31 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tmem_st16(s_col, z);
         tmem_st16(s_col + 16, z);
       }
-      if (j > 0) {
+      // every phase is waited for in turn (v_empty: PV done), or a parity would say too little
+      if (j > 1) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->v_empty[st]), ((j - 2) >> 1) & 1, abort));
+      if (j > 0 && ok && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O may be touched only between products
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->pv_done), (j - 1) & 1, abort));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->v_empty[st ^ 1]), ((j - 1) >> 1) & 1, abort));
         if (!ok) break;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          tc_fence_after();
+        tc_fence_after();
 #pragma unroll
-          for (int c0 = 0; c0 < D / 16; ++c0) {
-            uint32_t x[16];
-            tmem_ld16(lane_base + 128 + c0 * 16, x);
-            tmem_wait_ld();
+        for (int c0 = 0; c0 < D / 16; ++c0) {
+          uint32_t x[16];
+          tmem_ld16(lane_base + 128 + c0 * 16, x);
+          tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * alpha);
-            tmem_st16(lane_base + 128 + c0 * 16, x);
-          }
+          for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * alpha);
+          tmem_st16(lane_base + 128 + c0 * 16, x);
         }
       }
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->p_full[st]));
     }
     // ---------------------------------------------------------------- epilogue
-    if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->pv_done), (j - 1) & 1, abort));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
     if (ok) {
       tc_fence_after();
       const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti;

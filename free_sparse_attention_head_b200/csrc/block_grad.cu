@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kDqThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->ds_full));
     }
-    if (ok && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->k_empty[(j - 1) & 1]), ((j - 1) >> 1) & 1, abort));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
     if (ok) {
       tc_fence_after();
 #pragma unroll
@@ -555,24 +555,37 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const int t = tid - 256;  // one row's list entry and scalars per thread
     constexpr int kChunks = D / 8;
     const int ch = t % kChunks, r0 = t / kChunks;
-    // row of [B, H, Nq] behind row f of the piece, -1 behind the last; its limit
-    int next = -1, next_nv = 0;
-    auto look = [&](int f) {
-      next = -1;
-      next_nv = 0;
-      if (f < rows) {
-        const long long fr = row0 + f;
-        const int e = static_cast<int>(fr / p.G), g = static_cast<int>(fr - static_cast<long long>(e) * p.G);
-        const int tok = toks[e];
-        next = (b * p.H + hk * p.G + g) * p.Nq + tok;
-        next_nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
+    // Read ahead, so that no load is waited for where it is issued: the list
+    // entry of tile j + 2, and the scalars of tile j + 1.
+    auto entry = [&](int j) {  // the query of this thread's row in tile j, -1 behind the last
+      const int f = j * kRowTile + t;
+      return f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
+    };
+    int row = -1, nv = 0;
+    float l2 = INFINITY, dl = 0.f;
+    auto scalars = [&](int j, int tok) {
+      row = -1;
+      nv = 0;
+      l2 = INFINITY;  // a row that does not take part: P = 2^(s - inf) = 0
+      dl = 0.f;
+      if (tok >= 0) {
+        const int g = static_cast<int>((row0 + j * kRowTile + t) % p.G);
+        row = (b * p.H + hk * p.G + g) * p.Nq + tok;
+        nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
+        if (nv > 0) {
+          l2 = lse[row];
+          dl = delta[row];
+        }
       }
     };
-    if (nj > 0) look(t);
+    int tok = -1;
+    if (nj > 0) {
+      scalars(0, entry(0));
+      tok = entry(1);
+    }
     for (int j = 0; j < nj; ++j) {
       const int st = j & 1;
       const bool free = j < 2 || mbar_wait(smem_u32(&S->free_[st]), ((j - 2) >> 1) & 1, abort);
-      const int row = next, nv = next_nv;
       S->row[t] = row;
       if (!loaders_agree(free)) break;  // all four warps go on or leave together
       const uint32_t g_dst = row_u + st * 2 * kRowBytes, q_dst = g_dst + kRowBytes;
@@ -584,11 +597,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         cp_async16_or_zero(g_dst + off, go + at, src >= 0);
         cp_async16_or_zero(q_dst + off, q + at, src >= 0);
       }
-      // a row that does not take part has lse = inf, so P = 0
       S->nv[st][t] = static_cast<uint8_t>(nv);
-      S->lse2[st][t] = nv > 0 ? lse[row] * 1.4426950408889634f : INFINITY;
-      S->delta[st][t] = nv > 0 ? delta[row] : 0.f;
-      look((j + 1) * kRowTile + t);
+      S->lse2[st][t] = l2 * 1.4426950408889634f;
+      S->delta[st][t] = dl;
+      scalars(j + 1, tok);
+      tok = entry(j + 2);
       cp_async_wait_all();
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&S->full[st]));  // this thread's part of row tile j is in
