@@ -612,12 +612,15 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
       const uint32_t idesc_g = idesc_bf16_f32(128, kKeyTile, true, true);
-      bool ok = true;
-      for (int j = 0; j <= nj && ok; ++j) {
-        if (j < nj) {
-          const int st = j & 1;
+      // S, dP of tile js and the sums of tile jg, whichever can go first: a tile
+      // that has not landed does not hold back the sums that its stage waits for
+      int js = 0, jg = 0;
+      long long since = clock64();
+      while (jg < nj) {
+        bool did = false;
+        if (js < nj && js < jg + 2 && mbar_try_wait(smem_u32(&S->full[js & 1]), (js >> 1) & 1)) {
+          const int st = js & 1;
           const uint32_t g_u = row_u + st * 2 * kRowBytes, q_u = g_u + kRowBytes;
-          if (!(ok = mbar_wait(smem_u32(&S->full[st]), (j >> 1) & 1, abort))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -629,12 +632,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                      kk > 0 ? 1u : 0u);
           }
           umma_commit(smem_u32(&S->s_full[st]));
+          ++js;
+          did = true;
         }
-        if (j >= 1) {
-          const int st = (j - 1) & 1;
+        if (jg < js && mbar_try_wait(smem_u32(&S->ds_full[jg & 1]), (jg >> 1) & 1)) {
+          const int st = jg & 1;
           const uint32_t g_u = row_u + st * 2 * kRowBytes;
           const uint32_t a_v = g_u, a_k = D == 128 ? g_u + kRowBytes : g_u;
-          if (!(ok = mbar_wait(smem_u32(&S->ds_full[st]), ((j - 1) >> 1) & 1, abort))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kRowTile / 16; ++kk) {
@@ -642,11 +646,19 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             const uint64_t bp = sw128_desc(p_u + st * 2 * kPBytes + step, 16, 1024);
             const uint64_t bs = sw128_desc(p_u + st * 2 * kPBytes + kPBytes + step, 16, 1024);
             umma_f16(tmem + 256, sw128_desc(a_v + step, kRowTile * 128, 1024), bp, idesc_g,
-                     (j > 1 || kk > 0) ? 1u : 0u);
+                     (jg > 0 || kk > 0) ? 1u : 0u);
             umma_f16(tmem + 320, sw128_desc(a_k + step, kRowTile * 128, 1024), bs, idesc_g,
-                     (j > 1 || kk > 0) ? 1u : 0u);
+                     (jg > 0 || kk > 0) ? 1u : 0u);
           }
           umma_commit(smem_u32(&S->free_[st]));
+          ++jg;
+          did = true;
+        }
+        if (did) {
+          since = clock64();
+        } else if (*abort || clock64() - since > kWaitBudgetCycles) {
+          *abort = 1;
+          break;
         }
       }
       umma_commit(smem_u32(&S->mma_final));
