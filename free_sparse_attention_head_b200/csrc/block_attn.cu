@@ -34,8 +34,9 @@ struct FwdSmem {
   uint32_t tmem_base;
   int abort;
   int max_limit;
-  int limit[kRowTile];   // per query of the tile
-  int count[kRowTile];   // valid slots per query
+  int tiles;                 // of the list
+  int limit[kRowTile];       // per query of the tile
+  uint16_t count[kRowTile];  // valid slots per query
 };
 
 template <int D>
@@ -46,7 +47,7 @@ constexpr size_t fwd_tile_bytes() {
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     block_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      BlockDims p, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                      BlockDims p, int cap, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
                       const uint16_t* __restrict__ v, const int32_t* __restrict__ idx,
                       const int32_t* __restrict__ lengths, float scale_log2, uint16_t* __restrict__ o,
                       float* __restrict__ lse, int* __restrict__ err) {
@@ -58,7 +59,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint8_t* k_s = q_s + kRowTile * D * 2;  // 2 stages
   uint8_t* v_s = k_s + 2 * kKvBytes;      // 2 stages
   FwdSmem* S = reinterpret_cast<FwdSmem*>(v_s + 2 * kKvBytes);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(S + 1);
+  uint16_t* list = reinterpret_cast<uint16_t*>(S + 1);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(list + cap);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     });
     if (lane == 0) {
       S->limit[ti] = lim;
-      S->count[ti] = n;
+      S->count[ti] = static_cast<uint16_t>(n);
       atomicMax(&S->max_limit, lim);
     }
   }
@@ -104,6 +106,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
+  __syncthreads();
+  if (warp == 4) {
+    const int n = list_tiles(bits, p.nb, p.nsub, S->max_limit, list);
+    if (lane == 0) S->tiles = n;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t q_u = smem_u32(q_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
-  TileIter it(bits, p.nb, p.nsub, S->max_limit);
+  const int tiles = S->tiles;
   int k_armed = -1, v_armed = -1;
 
   if (warp == 4) {
@@ -141,8 +148,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
     }
-    for (int j = 0; it.next(); ++j) {
-      const int st = j & 1, key0 = it.tile() * kKeyTile;
+    for (int j = 0; j < tiles; ++j) {
+      const int st = j & 1, key0 = list[j] * kKeyTile;
       if (j >= 2 && !warp_wait(smem_u32(&S->k_empty[st]), ((j - 2) >> 1) & 1)) break;
       fill(&kmap, k, k_s + st * kKvBytes, smem_u32(&S->k_full[st]), key0);
       k_armed = j;
@@ -169,13 +176,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         umma_commit(smem_u32(&S->k_empty[st]));
         return true;
       };
-      bool more = it.next();
-      bool ok = more ? issue_s(0) : true;
-      for (int j = 0; more && ok; ++j) {
+      bool ok = tiles > 0 && issue_s(0);
+      for (int j = 0; j < tiles && ok; ++j) {
         const int st = j & 1;
-        more = it.next();
         // S(j+1) goes where P(j-1) was: its product is ahead in the queue
-        if (more && !(ok = issue_s(j + 1))) break;
+        if (j + 1 < tiles && !(ok = issue_s(j + 1))) break;
         ok = mbar_wait(smem_u32(&S->p_full[st]), (j >> 1) & 1, abort) &&
              mbar_wait(smem_u32(&S->v_full[st]), (j >> 1) & 1, abort);
         if (!ok) break;
@@ -204,11 +209,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // bf16 for the second product
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    int j = 0;
-    for (; it.next(); ++j) {
+    auto visible = [&](int j) {  // keys of tile j that the row sees
+      const int t = list[j];
+      return mine.has(p.nsub == 1 ? t : t / p.nsub) ? max(0, min(kKeyTile, lim - t * kKeyTile)) : 0;
+    };
+    int nv = tiles > 0 ? visible(0) : 0;
+    for (int j = 0; j < tiles; ++j) {
       const int st = j & 1;
       const uint32_t s_col = lane_base + st * 64;
-      const int nv = mine.has(it.blk) ? max(0, min(kKeyTile, lim - it.tile() * kKeyTile)) : 0;
       const bool some = __any_sync(0xffffffffu, nv > 0);
       const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort));
@@ -294,6 +302,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->p_full[st]));
+      if (j + 1 < tiles) nv = visible(j + 1);
     }
     // ---------------------------------------------------------------- epilogue
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t x[32];
-        if (j > 0) {
+        if (tiles > 0) {
           tmem_ld32(lane_base + 128 + c0 * 32, x);
           tmem_wait_ld_regs(x);
         }
@@ -352,13 +361,14 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   if (encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + static_cast<size_t>((p.nb + 31) / 32) * 4;
+  const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + list_cap(p) * 2 +
+                      static_cast<size_t>((p.nb + 31) / 32) * 4;
   if (cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv), kFwdThreads, smem, st>>>(
-      km, vm, p, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+      km, vm, p, static_cast<int>(list_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
       idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, dev_err);
   return launch_status();
 }

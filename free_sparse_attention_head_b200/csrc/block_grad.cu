@@ -52,39 +52,56 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ dq
 
-constexpr int kDqThreads = 192;
+// Row tiles and steps of two 64-key tiles as in the forward kernel; P needs no
+// maximum here, so the two tiles of a step are two groups of warps that never
+// meet. One CTA per SM: S alternates between two buffers, so S(j+1) is computed
+// under dS(j); dP has one, whose next product goes ahead of dQ(j).
+// Warps: 0-3, 4-7 dS of a step's first / second tile (thread = row), 8 key and
+// value producer, 9 MMA issuer.
+// TMEM: S [0,128) and [128,256), dS over the first half of each tile's scores;
+// dP [256,384); dQ [384,384+D).
+
+constexpr int kDqThreads = 320;
+constexpr int kDqPair = 2 * kKeyTile;
+
+constexpr int kDqK = 3;  // stages of K: dQ(j-1) may still read one while S(j+1) needs the next but one
 
 struct DqSmem {
-  uint64_t k_full[2], k_empty[2], v_full, s_full, ds_full, mma_final;
+  uint64_t k_full[kDqK], k_empty[kDqK], v_full[2], v_empty[2];
+  uint64_t s_full[2], dp_full, ds_full, mma_final;
   uint32_t tmem_base;
   int abort;
   int max_limit;
+  int tiles;
   int limit[kRowTile];
   uint16_t count[kRowTile];
 };
 
 template <int D>
-__global__ void __launch_bounds__(kDqThreads, 2)
+__global__ void __launch_bounds__(kDqThreads, 1)
     block_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
-                    const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                    const uint16_t* __restrict__ go, const float* __restrict__ lse, const float* __restrict__ delta,
-                    const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths, float scale,
-                    float scale_log2, uint16_t* __restrict__ dq, int* __restrict__ err) {
+                    int cap, int v_stages, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                    const uint16_t* __restrict__ v, const uint16_t* __restrict__ go, const float* __restrict__ lse,
+                    const float* __restrict__ delta, const int32_t* __restrict__ idx,
+                    const int32_t* __restrict__ lengths, float scale, float scale_log2, uint16_t* __restrict__ dq,
+                    int* __restrict__ err) {
   constexpr int kSub = D / 64;
-  constexpr int kKvBytes = kKeyTile * D * 2;
+  constexpr int kHalfBytes = kKeyTile * D * 2;
+  constexpr int kPairBytes = 2 * kHalfBytes;
   constexpr int kRowBytes = kRowTile * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  // no room to round up in, if two CTAs are to share an SM: the declared alignment has to hold
+  // no room to round up in: the declared alignment has to hold
   if (smem_u32(smem_raw) & 1023u) {
     if (threadIdx.x == 0) report_error(err, kErrBadPlan);
     return;
   }
   uint8_t* q_s = smem_raw;
   uint8_t* g_s = q_s + kRowBytes;
-  uint8_t* k_s = g_s + kRowBytes;  // 2 stages
-  uint8_t* v_s = k_s + 2 * kKvBytes;
-  DqSmem* S = reinterpret_cast<DqSmem*>(v_s + kKvBytes);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(S + 1);
+  uint8_t* k_s = g_s + kRowBytes;
+  uint8_t* v_s = k_s + kDqK * kPairBytes;
+  DqSmem* S = reinterpret_cast<DqSmem*>(v_s + v_stages * kPairBytes);
+  uint16_t* list = reinterpret_cast<uint16_t*>(S + 1);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(list + cap);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
@@ -98,13 +115,17 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   if (tid == 0) {
     S->abort = 0;
     S->max_limit = 0;
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kDqK; ++s) {
       mbar_init(smem_u32(&S->k_full[s]), 1);
       mbar_init(smem_u32(&S->k_empty[s]), 1);
     }
-    mbar_init(smem_u32(&S->v_full), 1);
-    mbar_init(smem_u32(&S->s_full), 1);
-    mbar_init(smem_u32(&S->ds_full), 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&S->v_full[s]), 1);
+      mbar_init(smem_u32(&S->v_empty[s]), 1);
+      mbar_init(smem_u32(&S->s_full[s]), 1);
+    }
+    mbar_init(smem_u32(&S->dp_full), 1);
+    mbar_init(smem_u32(&S->ds_full), 8);  // one arrival per dS warp
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
@@ -125,10 +146,15 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kDqThreads);
   load_query_rows<D>(g_s, go, p, b, hk, t0, tid, kDqThreads);
   fence_proxy_async_smem();
-  if (warp == 5) {
+  if (warp == 9) {
     __syncwarp();
-    tmem_alloc(smem_u32(&S->tmem_base), 256);
+    tmem_alloc(smem_u32(&S->tmem_base), 512);
     tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    const int n = list_tiles(bits, p.nb, p.nsub, S->max_limit, list);
+    if (lane == 0) S->tiles = n;
   }
   tc_fence_before();
   __syncthreads();
@@ -137,156 +163,175 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t q_u = smem_u32(q_s), g_u = smem_u32(g_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
-  TileIter it(bits, p.nb, p.nsub, S->max_limit);
+  const int tiles = S->tiles, steps = (tiles + 1) / 2;
   int k_armed = -1, v_armed = -1;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---------------------------------------------------------------- producer
     const size_t row0 = static_cast<size_t>(blockIdx.y) * p.cap;
-    if (lane == 0) {
-      tma_prefetch_desc(&kmap);
-      tma_prefetch_desc(&vmap);
-    }
     auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
       int okl = 1;
       if (lane == 0) okl = mbar_wait(bar, parity, abort) ? 1 : 0;
       return __shfl_sync(0xffffffffu, okl, 0) != 0;
     };
-    auto fill = [&](const CUtensorMap* map, const uint16_t* src, uint8_t* dst, uint32_t bar, int key0) {
-      if (len - key0 >= kKeyTile) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, kKvBytes);
-          for (int s = 0; s < kSub; ++s)
-            tma_load_2d(map, smem_u32(dst) + s * kKeyTile * 128, bar, s * 64, static_cast<int>(row0 + key0));
-        }
-      } else {
-        load_key_rows<D>(dst, src, row0 + key0, len - key0, lane, 32);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      }
-    };
-    for (int j = 0; it.next(); ++j) {
-      const int st = j & 1, key0 = it.tile() * kKeyTile;
-      if (j >= 2 && !warp_wait(smem_u32(&S->k_empty[st]), ((j - 2) >> 1) & 1)) break;
-      fill(&kmap, k, k_s + st * kKvBytes, smem_u32(&S->k_full[st]), key0);
+    if (lane == 0) {
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+    for (int j = 0; j < steps; ++j) {
+      const int ks = j % kDqK, vs = j % v_stages;
+      const int key[2] = {list[2 * j] * kKeyTile, 2 * j + 1 < tiles ? list[2 * j + 1] * kKeyTile : -1};
+      if (j >= kDqK && !warp_wait(smem_u32(&S->k_empty[ks]), (j / kDqK - 1) & 1)) break;
+      load_key_pair<D>(&kmap, k, k_s + ks * kPairBytes, smem_u32(&S->k_full[ks]), row0, len, key);
       k_armed = j;
-      // V is done with once S and dP are there
-      if (j >= 1 && !warp_wait(smem_u32(&S->s_full), (j - 1) & 1)) break;
-      fill(&vmap, v, v_s, smem_u32(&S->v_full), key0);
+      if (j >= v_stages && !warp_wait(smem_u32(&S->v_empty[vs]), (j / v_stages - 1) & 1)) break;
+      load_key_pair<D>(&vmap, v, v_s + vs * kPairBytes, smem_u32(&S->v_full[vs]), row0, len, key);
       v_armed = j;
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
+      const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kDqPair, false, false);
       const uint32_t idesc_q = idesc_bf16_f32(kRowTile, D, false, true);
-      for (int j = 0; it.next(); ++j) {
-        const uint32_t kt = k_u + (j & 1) * kKvBytes;
-        if (!mbar_wait(smem_u32(&S->k_full[j & 1]), (j >> 1) & 1, abort)) break;
-        tc_fence_after();
+      auto rows_by_keys = [&](uint32_t d, uint32_t a_u, uint32_t b_u) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
-          umma_f16(tmem, sw128_desc(q_u + ro, 16, 1024), sw128_desc(kt + ko, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
-        }
-        if (!mbar_wait(smem_u32(&S->v_full), j & 1, abort)) break;
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16(d, sw128_desc(a_u + (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, 16, 1024),
+                   sw128_desc(b_u + (kk >> 2) * kDqPair * 128 + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+      };
+      auto issue_s = [&](int j) -> bool {  // over dS(j-2), whose product is ahead in the queue
+        if (!mbar_wait(smem_u32(&S->k_full[j % kDqK]), (j / kDqK) & 1, abort)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ro = (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, ko = (kk >> 2) * kKeyTile * 128 + (kk & 3) * 32;
-          umma_f16(tmem + 64, sw128_desc(g_u + ro, 16, 1024), sw128_desc(v_u + ko, 16, 1024), idesc_s,
-                   kk > 0 ? 1u : 0u);
-        }
-        umma_commit(smem_u32(&S->s_full));
+        rows_by_keys(tmem + (j & 1) * 128, q_u, k_u + (j % kDqK) * kPairBytes);
+        umma_commit(smem_u32(&S->s_full[j & 1]));
+        return true;
+      };
+      auto issue_dp = [&](int j) -> bool {  // dP(j-1) has been read
+        const int vs = j % v_stages;
+        if (!mbar_wait(smem_u32(&S->v_full[vs]), (j / v_stages) & 1, abort)) return false;
+        tc_fence_after();
+        rows_by_keys(tmem + 256, g_u, v_u + vs * kPairBytes);
+        umma_commit(smem_u32(&S->dp_full));
+        umma_commit(smem_u32(&S->v_empty[vs]));
+        return true;
+      };
+      bool ok = steps > 0 && issue_s(0) && issue_dp(0);
+      for (int j = 0; j < steps && ok; ++j) {
+        const bool more = j + 1 < steps;
+        if (more && !issue_s(j + 1)) break;
         if (!mbar_wait(smem_u32(&S->ds_full), j & 1, abort)) break;
         tc_fence_after();
+        if (more && !issue_dp(j + 1)) break;
+        const uint32_t kt = k_u + (j % kDqK) * kPairBytes;
 #pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)
-          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(kt + kk * 16 * 128, kKeyTile * 128, 1024), idesc_q,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(smem_u32(&S->k_empty[j & 1]));
+        for (int kk = 0; kk < kDqPair / 16; ++kk)
+          umma_f16_a_tmem(tmem + 384, tmem + (j & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                          sw128_desc(kt + kk * 16 * 128, kDqPair * 128, 1024), idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&S->k_empty[j % kDqK]));
       }
       umma_commit(smem_u32(&S->mma_final));
       mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
     }
   } else {
     // ---------------------------------------------------------------- dS
-    const int r = tid;
+    const int h = warp >> 2, r = tid & 127;  // tile of the step, row
     const int ti = r / p.G, g = r - ti * p.G;
     const bool live = ti < nt;
     const int lim = live ? S->limit[ti] : 0;
     const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
     const float lse2 = lse[row] * 1.4426950408889634f, dl = delta[row];
     SlotCursor mine(slots + static_cast<size_t>(live ? ti : 0) * p.n_sel, live ? S->count[ti] : 0);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    auto visible = [&](int j) {  // keys of this thread's tile in step j that the row sees
+      if (2 * j + h >= tiles) return 0;
+      const int t = list[2 * j + h];
+      const int blk = p.nsub == 1 ? t : t / p.nsub;
+      return mine.has(blk) ? max(0, min(kKeyTile, lim - t * kKeyTile)) : 0;
+    };
+    const uint64_t sc2 = f2pack(scale_log2, scale_log2), nd2 = f2pack(-dl, -dl);
     bool ok = true;
-    int j = 0;
-    for (; it.next(); ++j) {
-      const int nv = mine.has(it.blk) ? max(0, min(kKeyTile, lim - it.tile() * kKeyTile)) : 0;
+    int nv = steps > 0 ? visible(0) : 0;
+    for (int j = 0; j < steps; ++j) {
       const bool some = __any_sync(0xffffffffu, nv > 0);
       const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort));
+      const uint32_t s_col = lane_base + (j & 1) * 128 + h * kKeyTile;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[j & 1]), (j >> 1) & 1, abort));
+      if (!ok) break;
+      tc_fence_after();
+      float s[kKeyTile];
+      if (some) {
+        // P = 2^(s - lse); a row that does not take part: 2^(s - inf) = 0
+        tmem_ld32f(s_col, s);
+        tmem_ld32f(s_col + 32, s + 32);
+        tmem_wait_ld_f(s);
+        tmem_wait_ld_f(s + 32);
+        if (!whole) {  // the row's own limit falls into this tile
+#pragma unroll
+          for (int c = 0; c < kKeyTile; ++c)
+            if (c >= nv) s[c] = -INFINITY;
+        }
+        const float nl = nv > 0 ? -lse2 : -INFINITY;
+        const uint64_t nl2 = f2pack(nl, nl);
+#pragma unroll
+        for (int c = 0; c < kKeyTile; c += 2) {
+          f2unpack(f2fma(f2pack(s[c], s[c + 1]), sc2, nl2), s[c], s[c + 1]);
+          s[c] = ex2_approx(s[c]);
+          s[c + 1] = ex2_approx(s[c + 1]);
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->dp_full), j & 1, abort));
       if (!ok) break;
       tc_fence_after();
       uint32_t pk[32];
       if (some) {
-        // P = 2^(s - lse), dS = P (dP - delta); a row that does not take part:
-        // 2^(s - inf) = 0
-        const float nl = nv > 0 ? -lse2 : -INFINITY;
-        const uint64_t sc2 = f2pack(scale_log2, scale_log2), nl2 = f2pack(nl, nl), nd2 = f2pack(-dl, -dl);
-        float s[32], x[32];
+        // dS = P (dP - delta)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          tmem_ld32f(lane_base + h * 32, s);
-          tmem_ld32f(lane_base + 64 + h * 32, x);
-          tmem_wait_ld_f(s);
+        for (int q4 = 0; q4 < 2; ++q4) {
+          float x[32];
+          tmem_ld32f(lane_base + 256 + h * kKeyTile + q4 * 32, x);
           tmem_wait_ld_f(x);
-          if (!whole) {  // the row's own limit falls into this tile
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (h * 32 + c >= nv) s[c] = -INFINITY;
-          }
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             float e0, e1;
-            f2unpack(f2fma(f2pack(s[2 * c], s[2 * c + 1]), sc2, nl2), e0, e1);
-            const uint64_t d2 = f2mul(f2pack(ex2_approx(e0), ex2_approx(e1)), f2add(f2pack(x[2 * c], x[2 * c + 1]), nd2));
-            f2unpack(d2, e0, e1);
-            pk[h * 16 + c] = pack_bf16x2(e0, e1);
+            f2unpack(f2mul(f2pack(s[q4 * 32 + 2 * c], s[q4 * 32 + 2 * c + 1]),
+                           f2add(f2pack(x[2 * c], x[2 * c + 1]), nd2)),
+                     e0, e1);
+            pk[q4 * 16 + c] = pack_bf16x2(e0, e1);
           }
         }
       } else {
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }
-      tmem_st32(lane_base, pk);  // over S, which this warp has read
+      tmem_st32(s_col, pk);  // over scores that this warp alone has read
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->ds_full));
+      if (j + 1 < steps) nv = visible(j + 1);
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
     if (ok) {
       tc_fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < D / 32; ++c0) {
+      for (int c0 = 0; c0 < D / 64; ++c0) {  // half of the columns each
+        const int col = h * (D / 2) + c0 * 32;
         uint32_t x[32];
-        if (j > 0) {
-          tmem_ld32(lane_base + 128 + c0 * 32, x);
+        if (steps > 0) {
+          tmem_ld32(lane_base + 384 + col, x);
           tmem_wait_ld_regs(x);
         }
         if (live) {
 #pragma unroll
           for (int c8 = 0; c8 < 4; ++c8) {
             uint4 w = make_uint4(0, 0, 0, 0);
-            if (j > 0) {
+            if (steps > 0) {
               w.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * scale, __uint_as_float(x[c8 * 8 + 1]) * scale);
               w.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * scale, __uint_as_float(x[c8 * 8 + 3]) * scale);
               w.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * scale, __uint_as_float(x[c8 * 8 + 5]) * scale);
               w.w = pack_bf16x2(__uint_as_float(x[c8 * 8 + 6]) * scale, __uint_as_float(x[c8 * 8 + 7]) * scale);
             }
-            reinterpret_cast<uint4*>(dq + row * D + c0 * 32)[c8] = w;
+            reinterpret_cast<uint4*>(dq + row * D + col)[c8] = w;
           }
         }
       }
@@ -296,16 +341,17 @@ __global__ void __launch_bounds__(kDqThreads, 2)
   __syncthreads();
   if (*abort) {
     if (tid == 0) report_error(err, kErrTimeoutAttn);
-    if (warp == 4 && lane == 0) {
-      for (int j = max(0, k_armed - 1); j <= k_armed; ++j)
-        mbar_wait_cleanup(smem_u32(&S->k_full[j & 1]), (j >> 1) & 1);
-      if (v_armed >= 0) mbar_wait_cleanup(smem_u32(&S->v_full), v_armed & 1);
+    if (warp == 8 && lane == 0) {  // copies still in flight land before the shared memory goes away
+      for (int j = max(0, k_armed - kDqK + 1); j <= k_armed; ++j)
+        mbar_wait_cleanup(smem_u32(&S->k_full[j % kDqK]), (j / kDqK) & 1);
+      for (int j = max(0, v_armed - v_stages + 1); j <= v_armed; ++j)
+        mbar_wait_cleanup(smem_u32(&S->v_full[j % v_stages]), (j / v_stages) & 1);
     }
     __syncthreads();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -787,7 +833,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-static_assert(dkv_tile_bytes<128>() + sizeof(DkvSmem) <= 232448, "dk, dv: shared memory of one SM");
+static_assert(dkv_tile_bytes<128>() + sizeof(DkvSmem) <= kMaxSmem, "dk, dv: shared memory of one SM");
 
 // ------------------------------------------------------------------ host side
 
@@ -849,8 +895,11 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t dq_smem = static_cast<size_t>(2 * kRowTile + 3 * kKeyTile) * D * 2 + sizeof(DqSmem) +
-                         static_cast<size_t>((p.nb + 31) / 32) * 4;
+  // two stages of V where the list of tiles leaves the room
+  size_t dq_smem = static_cast<size_t>(2 * kRowTile + (kDqK + 2) * kDqPair) * D * 2 + sizeof(DqSmem) + list_cap(p) * 2 +
+                   static_cast<size_t>((p.nb + 31) / 32) * 4;
+  const int v_stages = dq_smem <= kMaxSmem ? 2 : 1;
+  if (v_stages == 1) dq_smem -= static_cast<size_t>(kDqPair) * D * 2;
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
   const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
   if (cudaFuncSetAttribute(block_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -875,7 +924,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
     sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        km, vm, p, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+        km, vm, p, static_cast<int>(list_cap(p)), v_stages, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
       p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,

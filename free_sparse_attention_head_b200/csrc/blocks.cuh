@@ -23,6 +23,7 @@ constexpr int kKeyTile = 64;
 constexpr int kMaxSel = 256;      // slots of a query
 constexpr int kMaxBlocks = 16384;  // blocks of a sequence
 constexpr int kNoBlock = 0x7fffffff;
+constexpr size_t kMaxSmem = 232448;  // dynamic shared memory of one CTA
 
 struct BlockDims {
   int B, H, Hkv, G;
@@ -120,34 +121,44 @@ __device__ __forceinline__ int walk_slots(const int32_t* slots, int n, int nb, b
   return count;
 }
 
-// The key tiles of a row tile's selected blocks, ascending: set bits of a
-// bitmap over the blocks, `nsub` tiles each, up to the last tile that any row
-// may look at.
-struct TileIter {
-  const uint32_t* bits;
-  int words, nsub, tiles;  // tiles: ceil(largest limit / kKeyTile)
-  int w, blk, sub;
-  uint32_t cur;
-  __device__ __forceinline__ TileIter(const uint32_t* bits_, int nb, int nsub_, int max_limit)
-      : bits(bits_), words((nb + 31) / 32), nsub(nsub_), tiles((max_limit + kKeyTile - 1) / kKeyTile), w(-1),
-        blk(-1), sub(0), cur(0) {}
-  __device__ __forceinline__ bool next() {
-    if (blk >= 0 && sub + 1 < nsub && blk * nsub + sub + 1 < tiles) {
-      ++sub;
-      return true;
+// The key tiles of a row tile's selected blocks, ascending, from the set bits of
+// a bitmap over the blocks: `nsub` tiles each, up to the last tile that any row
+// may look at. One warp; returns their number. (Walking the bitmap step by step
+// in every role instead cost the forward kernel 700 cycles of a 4600-cycle step.)
+__device__ __forceinline__ int list_tiles(const uint32_t* bits, int nb, int nsub, int max_limit, uint16_t* list) {
+  const int lane = threadIdx.x & 31, tiles = (max_limit + kKeyTile - 1) / kKeyTile;
+  int base = 0;
+  for (int w0 = 0; w0 * 32 < nb; w0 += 32) {
+    const int w = w0 + lane;
+    uint32_t word = w * 32 < nb ? bits[w] : 0u;
+    // only the last block of all can reach behind `tiles`, and only in part
+    int n = __popc(word) * nsub;
+    if (word) {
+      const int last = w * 32 + 31 - __clz(word);
+      n -= max(0, (last + 1) * nsub - tiles);
     }
-    while (cur == 0) {
-      if (++w >= words) return false;
-      cur = bits[w];
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    const int bit = __ffs(cur) - 1;
-    cur &= cur - 1;
-    blk = w * 32 + bit;
-    sub = 0;
-    return true;
+    int at = base + inc - n;
+    while (word) {
+      const int blk = w * 32 + __ffs(word) - 1;
+      word &= word - 1;
+      for (int s = 0; s < nsub && blk * nsub + s < tiles; ++s) list[at++] = static_cast<uint16_t>(blk * nsub + s);
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  __device__ __forceinline__ int tile() const { return blk * nsub + sub; }
-};
+  return base;
+}
+
+// entries that list_tiles can write
+inline size_t list_cap(const BlockDims& p) {
+  const size_t all = static_cast<size_t>(p.nb) * p.nsub, chosen = static_cast<size_t>(p.tpt) * p.n_sel * p.nsub;
+  return ((all < chosen ? all : chosen) + 7) / 8 * 8;
+}
 
 // One row's own walk through its slots beside the tile walk.
 struct SlotCursor {
@@ -167,10 +178,10 @@ struct SlotCursor {
   }
 };
 
-// 64 key rows from `row0` of a [rows, D] bf16 matrix into a swizzled tile, rows
-// from `valid` on as zeros (what lies behind a sequence may hold anything, and
-// 0 * NaN would reach every row). `lanes` threads take part.
-template <int D>
+// 64 key rows from `row0` of a [rows, D] bf16 matrix into a swizzled tile of
+// `kRows` rows, rows from `valid` on as zeros (what lies behind a sequence may
+// hold anything, and 0 * NaN would reach every row). `lanes` threads take part.
+template <int D, int kRows = kKeyTile>
 __device__ __forceinline__ void load_key_rows(uint8_t* dst, const uint16_t* src, size_t row0, int valid, int tid,
                                               int lanes) {
   constexpr int kChunks = D / 8;
@@ -179,8 +190,47 @@ __device__ __forceinline__ void load_key_rows(uint8_t* dst, const uint16_t* src,
     const int r = c / kChunks, ch = c - r * kChunks;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < valid) x = *reinterpret_cast<const uint4*>(src + (row0 + r) * D + ch * 8);
-    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch * 8, kKeyTile)) = x;
+    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch * 8, kRows)) = x;
   }
+}
+
+// The two 64-key tiles of a step (first keys key[0], key[1]; below 0: none,
+// zeros) into one swizzled 128-row tile, completing on `bar` (one arrival). A
+// tile that the sequence ends in goes through plain loads, zeros behind its end.
+// One warp.
+template <int D>
+__device__ __forceinline__ void load_key_pair(const CUtensorMap* map, const uint16_t* src, uint8_t* dst, uint32_t bar,
+                                              size_t row0, int len, const int (&key)[2]) {
+  constexpr int kRows = 2 * kKeyTile;
+  const int lane = threadIdx.x & 31;
+  uint32_t bytes = 0;
+  bool slow = false;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (key[h] >= 0 && len - key[h] >= kKeyTile) {
+      bytes += kKeyTile * D * 2;
+    } else {
+      load_key_rows<D, kRows>(dst + h * kKeyTile * 128, src, row0 + max(key[h], 0), key[h] < 0 ? 0 : len - key[h], lane,
+                              32);
+      slow = true;
+    }
+  }
+  if (slow) {
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  if (lane != 0) return;
+  if (bytes == 0) {
+    mbar_arrive(bar);
+    return;
+  }
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (key[h] >= 0 && len - key[h] >= kKeyTile)
+      for (int s = 0; s < D / 64; ++s)
+        tma_load_2d(map, smem_u32(dst) + s * kRows * 128 + h * kKeyTile * 128, bar, s * 64,
+                    static_cast<int>(row0 + key[h]));
 }
 
 // The rows of a row tile (query-major, see above) of a [B, H, Nq, D] bf16
