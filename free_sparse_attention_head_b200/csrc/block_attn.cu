@@ -26,7 +26,10 @@ namespace svoo {
 namespace {
 
 constexpr int kFwdThreads = 192;
-constexpr float kFwdRescaleLog2 = 8.0f;
+// The running maximum stays until it is outgrown by 2^32: P (bf16, fp32's range)
+// and its sums lose nothing by being large, at most 2^52 here, and the rescaling
+// that a smaller bound (2^8) asked for stalled most steps on the last product.
+constexpr float kFwdRescaleLog2 = 32.0f;
 
 struct FwdSmem {
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
@@ -35,8 +38,7 @@ struct FwdSmem {
   int abort;
   int max_limit;
   int tiles;                 // of the list
-  int limit[kRowTile];       // per query of the tile
-  uint16_t count[kRowTile];  // valid slots per query
+  int limit[kRowTile];  // per query of the tile
 };
 
 template <int D>
@@ -59,8 +61,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint8_t* k_s = q_s + kRowTile * D * 2;  // 2 stages
   uint8_t* v_s = k_s + 2 * kKvBytes;      // 2 stages
   FwdSmem* S = reinterpret_cast<FwdSmem*>(v_s + 2 * kKvBytes);
-  uint16_t* list = reinterpret_cast<uint16_t*>(S + 1);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(list + cap);
+  const TileList tl = tile_list(p, cap, S + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
@@ -70,10 +71,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int len = seq_len(p, lengths, b);
   const int32_t* slots = idx + (static_cast<size_t>(blockIdx.y) * p.Nq + t0) * p.n_sel;
 
-  for (int i = tid; i < (p.nb + 31) / 32; i += kFwdThreads) bits[i] = 0;
   if (tid == 0) {
     S->abort = 0;
-    S->max_limit = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&S->k_full[s]), 1);
       mbar_init(smem_u32(&S->v_full[s]), 1);
@@ -85,20 +84,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  bool bad = false;
-  for (int ti = warp; ti < nt; ti += kFwdThreads / 32) {
-    const int lim = query_limit(p, len, t0 + ti);
-    const int n = walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
-      if (blk * p.block < lim) atomicOr(&bits[blk >> 5], 1u << (blk & 31));
-    });
-    if (lane == 0) {
-      S->limit[ti] = lim;
-      S->count[ti] = static_cast<uint16_t>(n);
-      atomicMax(&S->max_limit, lim);
-    }
-  }
-  if (bad && lane == 0) report_error(err, kErrBadPlan);
   load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kFwdThreads);
   fence_proxy_async_smem();
   if (warp == 5) {
@@ -106,11 +91,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
-  __syncthreads();
-  if (warp == 4) {
-    const int n = list_tiles(bits, p.nb, p.nsub, S->max_limit, list);
-    if (lane == 0) S->tiles = n;
-  }
+  const int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -118,7 +99,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t q_u = smem_u32(q_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
-  const int tiles = S->tiles;
   int k_armed = -1, v_armed = -1;
 
   if (warp == 4) {
@@ -149,7 +129,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tma_prefetch_desc(&vmap);
     }
     for (int j = 0; j < tiles; ++j) {
-      const int st = j & 1, key0 = list[j] * kKeyTile;
+      const int st = j & 1, key0 = static_cast<int>(tl.list[j] & 0xffffu) * kKeyTile;
       if (j >= 2 && !warp_wait(smem_u32(&S->k_empty[st]), ((j - 2) >> 1) & 1)) break;
       fill(&kmap, k, k_s + st * kKvBytes, smem_u32(&S->k_full[st]), key0);
       k_armed = j;
@@ -202,16 +182,16 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const int ti = r / p.G, g = r - ti * p.G;
     const bool live = ti < nt;
     const int lim = live ? S->limit[ti] : 0;
-    SlotCursor mine(slots + static_cast<size_t>(live ? ti : 0) * p.n_sel, live ? S->count[ti] : 0);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // m: running maximum in log2 units, moved when it grows by more than 2^8
-    // (P stays at most 2^8); l: sum of P in 32 bits, before P is rounded to
+    // m: running maximum in log2 units, moved when it is outgrown; l: sum of P in 32 bits, before P is rounded to
     // bf16 for the second product
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    const uint32_t* my_word = tl.mask + (live ? ti >> 5 : 0);
     auto visible = [&](int j) {  // keys of tile j that the row sees
-      const int t = list[j];
-      return mine.has(p.nsub == 1 ? t : t / p.nsub) ? max(0, min(kKeyTile, lim - t * kKeyTile)) : 0;
+      const uint32_t e = tl.list[j];
+      const bool sel = live && ((my_word[(e >> 16) * tl.words] >> (ti & 31)) & 1u);
+      return sel ? max(0, min(kKeyTile, lim - static_cast<int>(e & 0xffffu) * kKeyTile)) : 0;
     };
     int nv = tiles > 0 ? visible(0) : 0;
     for (int j = 0; j < tiles; ++j) {
@@ -361,14 +341,13 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   if (encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + list_cap(p) * 2 +
-                      static_cast<size_t>((p.nb + 31) / 32) * 4;
+  const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + tile_list_bytes(p);
   if (cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv), kFwdThreads, smem, st>>>(
-      km, vm, p, static_cast<int>(list_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+      km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
       idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, dev_err);
   return launch_status();
 }

@@ -74,7 +74,6 @@ struct DqSmem {
   int max_limit;
   int tiles;
   int limit[kRowTile];
-  uint16_t count[kRowTile];
 };
 
 template <int D>
@@ -100,8 +99,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   uint8_t* k_s = g_s + kRowBytes;
   uint8_t* v_s = k_s + kDqK * kPairBytes;
   DqSmem* S = reinterpret_cast<DqSmem*>(v_s + v_stages * kPairBytes);
-  uint16_t* list = reinterpret_cast<uint16_t*>(S + 1);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(list + cap);
+  const TileList tl = tile_list(p, cap, S + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
@@ -111,10 +109,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const int len = seq_len(p, lengths, b);
   const int32_t* slots = idx + (static_cast<size_t>(blockIdx.y) * p.Nq + t0) * p.n_sel;
 
-  for (int i = tid; i < (p.nb + 31) / 32; i += kDqThreads) bits[i] = 0;
   if (tid == 0) {
     S->abort = 0;
-    S->max_limit = 0;
     for (int s = 0; s < kDqK; ++s) {
       mbar_init(smem_u32(&S->k_full[s]), 1);
       mbar_init(smem_u32(&S->k_empty[s]), 1);
@@ -129,20 +125,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  bool bad = false;
-  for (int ti = warp; ti < nt; ti += kDqThreads / 32) {
-    const int lim = query_limit(p, len, t0 + ti);
-    const int n = walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
-      if (blk * p.block < lim) atomicOr(&bits[blk >> 5], 1u << (blk & 31));
-    });
-    if (lane == 0) {
-      S->limit[ti] = lim;
-      S->count[ti] = static_cast<uint16_t>(n);
-      atomicMax(&S->max_limit, lim);
-    }
-  }
-  if (bad && lane == 0) report_error(err, kErrBadPlan);
   load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kDqThreads);
   load_query_rows<D>(g_s, go, p, b, hk, t0, tid, kDqThreads);
   fence_proxy_async_smem();
@@ -151,11 +133,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tmem_alloc(smem_u32(&S->tmem_base), 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  if (warp == 8) {
-    const int n = list_tiles(bits, p.nb, p.nsub, S->max_limit, list);
-    if (lane == 0) S->tiles = n;
-  }
+  const int tiles = make_tile_list<kDqThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
+  const int steps = (tiles + 1) / 2;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -163,7 +142,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t q_u = smem_u32(q_s), g_u = smem_u32(g_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
-  const int tiles = S->tiles, steps = (tiles + 1) / 2;
   int k_armed = -1, v_armed = -1;
 
   if (warp == 8) {
@@ -180,7 +158,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     }
     for (int j = 0; j < steps; ++j) {
       const int ks = j % kDqK, vs = j % v_stages;
-      const int key[2] = {list[2 * j] * kKeyTile, 2 * j + 1 < tiles ? list[2 * j + 1] * kKeyTile : -1};
+      const int key[2] = {static_cast<int>(tl.list[2 * j] & 0xffffu) * kKeyTile,
+                          2 * j + 1 < tiles ? static_cast<int>(tl.list[2 * j + 1] & 0xffffu) * kKeyTile : -1};
       if (j >= kDqK && !warp_wait(smem_u32(&S->k_empty[ks]), (j / kDqK - 1) & 1)) break;
       load_key_pair<D>(&kmap, k, k_s + ks * kPairBytes, smem_u32(&S->k_full[ks]), row0, len, key);
       k_armed = j;
@@ -240,13 +219,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int lim = live ? S->limit[ti] : 0;
     const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
     const float lse2 = lse[row] * 1.4426950408889634f, dl = delta[row];
-    SlotCursor mine(slots + static_cast<size_t>(live ? ti : 0) * p.n_sel, live ? S->count[ti] : 0);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t* my_word = tl.mask + (live ? ti >> 5 : 0);
     auto visible = [&](int j) {  // keys of this thread's tile in step j that the row sees
       if (2 * j + h >= tiles) return 0;
-      const int t = list[2 * j + h];
-      const int blk = p.nsub == 1 ? t : t / p.nsub;
-      return mine.has(blk) ? max(0, min(kKeyTile, lim - t * kKeyTile)) : 0;
+      const uint32_t e = tl.list[2 * j + h];
+      const bool sel = live && ((my_word[(e >> 16) * tl.words] >> (ti & 31)) & 1u);
+      return sel ? max(0, min(kKeyTile, lim - static_cast<int>(e & 0xffffu) * kKeyTile)) : 0;
     };
     const uint64_t sc2 = f2pack(scale_log2, scale_log2), nd2 = f2pack(-dl, -dl);
     bool ok = true;
@@ -896,8 +875,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
   // two stages of V where the list of tiles leaves the room
-  size_t dq_smem = static_cast<size_t>(2 * kRowTile + (kDqK + 2) * kDqPair) * D * 2 + sizeof(DqSmem) + list_cap(p) * 2 +
-                   static_cast<size_t>((p.nb + 31) / 32) * 4;
+  size_t dq_smem = static_cast<size_t>(2 * kRowTile + (kDqK + 2) * kDqPair) * D * 2 + sizeof(DqSmem) + tile_list_bytes(p);
   const int v_stages = dq_smem <= kMaxSmem ? 2 : 1;
   if (v_stages == 1) dq_smem -= static_cast<size_t>(kDqPair) * D * 2;
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
@@ -924,7 +902,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
     sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        km, vm, p, static_cast<int>(list_cap(p)), v_stages, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+        km, vm, p, static_cast<int>(union_cap(p)), v_stages, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
       p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,

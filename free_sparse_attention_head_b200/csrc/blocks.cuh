@@ -121,62 +121,108 @@ __device__ __forceinline__ int walk_slots(const int32_t* slots, int n, int nb, b
   return count;
 }
 
-// The key tiles of a row tile's selected blocks, ascending, from the set bits of
-// a bitmap over the blocks: `nsub` tiles each, up to the last tile that any row
-// may look at. One warp; returns their number. (Walking the bitmap step by step
-// in every role instead cost the forward kernel 700 cycles of a 4600-cycle step.)
-__device__ __forceinline__ int list_tiles(const uint32_t* bits, int nb, int nsub, int max_limit, uint16_t* list) {
-  const int lane = threadIdx.x & 31, tiles = (max_limit + kKeyTile - 1) / kKeyTile;
-  int base = 0;
-  for (int w0 = 0; w0 * 32 < nb; w0 += 32) {
-    const int w = w0 + lane;
-    uint32_t word = w * 32 < nb ? bits[w] : 0u;
-    // only the last block of all can reach behind `tiles`, and only in part
-    int n = __popc(word) * nsub;
-    if (word) {
-      const int last = w * 32 + 31 - __clz(word);
-      n -= max(0, (last + 1) * nsub - tiles);
-    }
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    int at = base + inc - n;
-    while (word) {
-      const int blk = w * 32 + __ffs(word) - 1;
-      word &= word - 1;
-      for (int s = 0; s < nsub && blk * nsub + s < tiles; ++s) list[at++] = static_cast<uint16_t>(blk * nsub + s);
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return base;
-}
-
-// entries that list_tiles can write
-inline size_t list_cap(const BlockDims& p) {
-  const size_t all = static_cast<size_t>(p.nb) * p.nsub, chosen = static_cast<size_t>(p.tpt) * p.n_sel * p.nsub;
-  return ((all < chosen ? all : chosen) + 7) / 8 * 8;
-}
-
-// One row's own walk through its slots beside the tile walk.
-struct SlotCursor {
-  const int32_t* slots;
-  int ptr, count, cur, nxt;
-  __device__ __forceinline__ SlotCursor(const int32_t* s, int n) : slots(s), ptr(0), count(n) {
-    cur = n > 0 ? s[0] : kNoBlock;
-    nxt = n > 1 ? s[1] : kNoBlock;
-  }
-  __device__ __forceinline__ bool has(int blk) {  // blk ascending from call to call
-    while (cur < blk) {
-      cur = nxt;
-      ++ptr;
-      nxt = ptr + 1 < count ? slots[ptr + 1] : kNoBlock;
-    }
-    return cur == blk;
-  }
+// What a row tile has to visit: the key tiles of the union of its queries'
+// blocks, ascending, and for every block of the union a bit per query. Walking
+// the blocks' bitmap and every query's slots step by step instead cost the
+// forward kernel a third of its time.
+//   list  tile | ordinal of its block in the union << 16
+//   mask  [block of the union][words] bits of the queries that selected it
+struct TileList {
+  uint32_t* list;
+  uint32_t* mask;
+  uint32_t* bits;   // a bit per block
+  uint16_t* rank;   // union blocks before each word of `bits`
+  int words;        // ceil(tpt / 32)
 };
+
+// blocks of the union, at most
+inline size_t union_cap(const BlockDims& p) {
+  const size_t chosen = static_cast<size_t>(p.tpt) * p.n_sel;
+  return static_cast<size_t>(p.nb) < chosen ? p.nb : chosen;
+}
+inline size_t tile_list_bytes(const BlockDims& p) {
+  const size_t words = (p.nb + 31) / 32;
+  return 4 * (union_cap(p) * (p.nsub + (p.tpt + 31) / 32) + words + (words + 1) / 2);
+}
+__device__ __forceinline__ TileList tile_list(const BlockDims& p, int cap, void* at) {
+  TileList t;
+  const int w = (p.nb + 31) / 32;
+  t.words = (p.tpt + 31) / 32;
+  t.list = static_cast<uint32_t*>(at);
+  t.mask = t.list + cap * p.nsub;
+  t.bits = t.mask + cap * t.words;
+  t.rank = reinterpret_cast<uint16_t*>(t.bits + w);
+  return t;
+}
+
+// Fills a CTA's list (all its threads; limits[] of the tile's queries are
+// written too). Returns the number of key tiles. `shared_max`, `shared_tiles`:
+// ints in shared memory.
+template <int kThreads>
+__device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList& t, const int32_t* slots, int t0,
+                                              int nt, int len, int* limits, int* shared_max, int* shared_tiles,
+                                              int* err) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int w_all = (p.nb + 31) / 32;
+  for (int i = tid; i < w_all; i += kThreads) t.bits[i] = 0;
+  if (tid == 0) *shared_max = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int ti = warp; ti < nt; ti += kThreads / 32) {
+    const int lim = query_limit(p, len, t0 + ti);
+    walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
+      if (blk * p.block < lim) atomicOr(&t.bits[blk >> 5], 1u << (blk & 31));
+    });
+    if (lane == 0) {
+      limits[ti] = lim;
+      atomicMax(shared_max, lim);
+    }
+  }
+  if (bad && lane == 0) report_error(err, kErrBadPlan);
+  __syncthreads();
+  const int tiles = (*shared_max + kKeyTile - 1) / kKeyTile;
+  if (warp == 0) {
+    int blocks = 0, n_tiles = 0;
+    for (int w0 = 0; w0 < w_all; w0 += 32) {
+      const int w = w0 + lane;
+      uint32_t word = w < w_all ? t.bits[w] : 0u;
+      const int n = __popc(word);
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      int ord = blocks + inc - n;
+      if (w < w_all) t.rank[w] = static_cast<uint16_t>(ord);
+      // only the last block of all can reach behind the last tile, and only in part
+      while (word) {
+        const int blk = w * 32 + __ffs(word) - 1;
+        word &= word - 1;
+        for (int s = 0; s < p.nsub && blk * p.nsub + s < tiles; ++s) {
+          t.list[ord * p.nsub + s] = static_cast<uint32_t>(blk * p.nsub + s) | static_cast<uint32_t>(ord) << 16;
+          n_tiles = ord * p.nsub + s + 1;
+        }
+        ++ord;
+      }
+      blocks += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    n_tiles = __reduce_max_sync(0xffffffffu, n_tiles);
+    for (int i = lane; i < blocks * t.words; i += 32) t.mask[i] = 0;
+    if (lane == 0) *shared_tiles = n_tiles;
+  }
+  __syncthreads();
+  for (int ti = warp; ti < nt; ti += kThreads / 32) {
+    const int lim = limits[ti];
+    walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
+      if (blk * p.block < lim) {
+        const int ord = t.rank[blk >> 5] + __popc(t.bits[blk >> 5] & ((1u << (blk & 31)) - 1u));
+        atomicOr(&t.mask[ord * t.words + (ti >> 5)], 1u << (ti & 31));
+      }
+    });
+  }
+  return *shared_tiles;
+}
 
 // 64 key rows from `row0` of a [rows, D] bf16 matrix into a swizzled tile of
 // `kRows` rows, rows from `valid` on as zeros (what lies behind a sequence may
