@@ -84,14 +84,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kFwdThreads);
-  fence_proxy_async_smem();
+  load_query_rows<D, kFwdThreads>(q_s, q, p, b, hk, t0);
   if (warp == 5) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
   const int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
+  cp_async_wait_all();
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   } else {
     // ---------------------------------------------------------------- softmax
     const int r = tid;
-    const int ti = r / p.G, g = r - ti * p.G;
+    const int ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
     const bool live = ti < nt;
     const int lim = live ? S->limit[ti] : 0;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);

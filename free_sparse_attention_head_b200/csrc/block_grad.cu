@@ -125,15 +125,16 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  load_query_rows<D>(q_s, q, p, b, hk, t0, tid, kDqThreads);
-  load_query_rows<D>(g_s, go, p, b, hk, t0, tid, kDqThreads);
-  fence_proxy_async_smem();
+  load_query_rows<D, kDqThreads>(q_s, q, p, b, hk, t0);
+  load_query_rows<D, kDqThreads>(g_s, go, p, b, hk, t0);
   if (warp == 9) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 512);
     tmem_relinquish();
   }
   const int tiles = make_tile_list<kDqThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
+  cp_async_wait_all();
+  fence_proxy_async_smem();
   const int steps = (tiles + 1) / 2;
   tc_fence_before();
   __syncthreads();
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   } else {
     // ---------------------------------------------------------------- dS
     const int h = warp >> 2, r = tid & 127;  // tile of the step, row
-    const int ti = r / p.G, g = r - ti * p.G;
+    const int ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
     const bool live = ti < nt;
     const int lim = live ? S->limit[ti] : 0;
     const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
@@ -482,9 +483,6 @@ constexpr size_t dkv_tile_bytes() {
          4 * static_cast<size_t>(kRowTile) * kKeyTile * 2;
 }
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 // barrier of the four loader warps, with a vote
 __device__ __forceinline__ bool loaders_agree(bool ok) {
   uint32_t r;
@@ -499,7 +497,6 @@ __device__ __forceinline__ bool loaders_agree(bool ok) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Per row tile: S = Q K^T and dP = dO V^T (rows x 64 keys) into tensor memory;
 // P and dS back to shared memory in bf16; dV^T += dO^T P and dK^T += Q^T dS

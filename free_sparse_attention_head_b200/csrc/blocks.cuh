@@ -22,7 +22,6 @@ constexpr int kRowTile = 128;
 constexpr int kKeyTile = 64;
 constexpr int kMaxSel = 256;      // slots of a query
 constexpr int kMaxBlocks = 16384;  // blocks of a sequence
-constexpr int kNoBlock = 0x7fffffff;
 constexpr size_t kMaxSmem = 232448;  // dynamic shared memory of one CTA
 
 struct BlockDims {
@@ -30,7 +29,8 @@ struct BlockDims {
   int Nq, Nk, cap;  // queries, keys, key rows from one head to the next
   int nb, block, nsub, n_sel;
   int sink, local, causal, q_start;
-  int tpt;  // queries of a row tile
+  int tpt;      // queries of a row tile
+  int inv_g;    // ceil(2^16 / G): r / G = r * inv_g >> 16 for r < 128
 };
 
 inline bool block_shape_ok(const svoo_block_shape* s) {
@@ -70,6 +70,7 @@ inline BlockDims block_dims(const svoo_block_shape* s) {
   p.causal = s->causal;
   p.q_start = s->q_start;
   p.tpt = kRowTile / p.G;
+  p.inv_g = (65536 + p.G - 1) / p.G;
   return p;
 }
 
@@ -121,6 +122,18 @@ __device__ __forceinline__ int walk_slots(const int32_t* slots, int n, int nb, b
   return count;
 }
 
+// The same for at most 32 slots, one a lane: the lane's block, or -1 behind the
+// list's end.
+__device__ __forceinline__ int counted_slot(int v, int nb, bool* bad) {
+  const int lane = threadIdx.x & 31;
+  int prev = __shfl_up_sync(0xffffffffu, v, 1);
+  if (lane == 0) prev = -1;
+  const unsigned bal = __ballot_sync(0xffffffffu, v >= 0 && v < nb && v > prev);
+  const int pre = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
+  if (__any_sync(0xffffffffu, lane == pre && v != -1)) *bad = true;
+  return lane < pre ? v : -1;
+}
+
 // What a row tile has to visit: the key tiles of the union of its queries'
 // blocks, ascending, and for every block of the union a bit per query. Walking
 // the blocks' bitmap and every query's slots step by step instead cost the
@@ -166,13 +179,35 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
   const int w_all = (p.nb + 31) / 32;
   for (int i = tid; i < w_all; i += kThreads) t.bits[i] = 0;
   if (tid == 0) *shared_max = 0;
+  // A warp's queries, all loads in flight at once; a lane holds a slot (where
+  // they are at most 32), -1 if it does not count
+  constexpr int kMine = (kRowTile + kThreads / 32 - 1) / (kThreads / 32);
+  const bool few = p.n_sel <= 32;
+  int held[kMine];
+  if (few) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int ti = warp + i * (kThreads / 32);
+      held[i] = ti < nt && lane < p.n_sel ? slots[static_cast<size_t>(ti) * p.n_sel + lane] : -1;
+    }
+  }
   __syncthreads();
   bool bad = false;
-  for (int ti = warp; ti < nt; ti += kThreads / 32) {
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int ti = warp + i * (kThreads / 32);
+    if (ti >= nt) break;
     const int lim = query_limit(p, len, t0 + ti);
-    walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
+    auto add = [&](int blk) {
       if (blk * p.block < lim) atomicOr(&t.bits[blk >> 5], 1u << (blk & 31));
-    });
+    };
+    if (few) {
+      held[i] = counted_slot(held[i], p.nb, &bad);
+      if (held[i] >= 0 && held[i] * p.block >= lim) held[i] = -1;
+      if (held[i] >= 0) add(held[i]);
+    } else {
+      walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, add);
+    }
     if (lane == 0) {
       limits[ti] = lim;
       atomicMax(shared_max, lim);
@@ -212,14 +247,22 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
     if (lane == 0) *shared_tiles = n_tiles;
   }
   __syncthreads();
-  for (int ti = warp; ti < nt; ti += kThreads / 32) {
-    const int lim = limits[ti];
-    walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
-      if (blk * p.block < lim) {
-        const int ord = t.rank[blk >> 5] + __popc(t.bits[blk >> 5] & ((1u << (blk & 31)) - 1u));
-        atomicOr(&t.mask[ord * t.words + (ti >> 5)], 1u << (ti & 31));
-      }
-    });
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int ti = warp + i * (kThreads / 32);
+    if (ti >= nt) break;
+    auto mark = [&](int blk) {
+      const int ord = t.rank[blk >> 5] + __popc(t.bits[blk >> 5] & ((1u << (blk & 31)) - 1u));
+      atomicOr(&t.mask[ord * t.words + (ti >> 5)], 1u << (ti & 31));
+    };
+    if (few) {
+      if (held[i] >= 0) mark(held[i]);
+    } else {
+      const int lim = limits[ti];
+      walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, [&](int blk) {
+        if (blk * p.block < lim) mark(blk);
+      });
+    }
   }
   return *shared_tiles;
 }
@@ -279,21 +322,27 @@ __device__ __forceinline__ void load_key_pair(const CUtensorMap* map, const uint
                     static_cast<int>(row0 + key[h]));
 }
 
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The rows of a row tile (query-major, see above) of a [B, H, Nq, D] bf16
-// tensor into a swizzled 128-row tile; rows without a query as zeros.
-template <int D>
+// tensor into a swizzled 128-row tile; rows without a query as zeros. The copies
+// are in flight when it returns: cp_async_wait_all() before the barrier.
+template <int D, int kThreads>
 __device__ __forceinline__ void load_query_rows(uint8_t* dst, const uint16_t* src, const BlockDims& p, int b, int hk,
-                                                int t0, int tid, int threads) {
-  constexpr int kChunks = D / 8;
-#pragma unroll 4
-  for (int c = tid; c < kRowTile * kChunks; c += threads) {
-    const int r = c / kChunks, ch = c - r * kChunks;
-    const int ti = r / p.G, g = r - ti * p.G;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (ti < p.tpt && t0 + ti < p.Nq)
-      x = *reinterpret_cast<const uint4*>(
-          src + ((static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti) * D + ch * 8);
-    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch * 8, kRowTile)) = x;
+                                                int t0) {
+  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
+  static_assert(kThreads % kChunks == 0, "a thread keeps its columns");
+  const int ch = threadIdx.x % kChunks;
+  const uint32_t to = smem_u32(dst);
+  const uint16_t* from = src + (static_cast<size_t>(b) * p.H + hk * p.G) * p.Nq * D + ch * 8;
+  for (int r = threadIdx.x / kChunks; r < kRowTile; r += kStep) {
+    const int ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
+    const bool there = ti < p.tpt && t0 + ti < p.Nq;
+    cp_async16_or_zero(to + sw128_offset(r, ch * 8, kRowTile),
+                       there ? from + (static_cast<size_t>(g) * p.Nq + t0 + ti) * D : src, there);
   }
 }
 
