@@ -13,9 +13,9 @@ Typical use (all tensors on one CUDA device, bf16 [B, H, N, d]):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 from typing import Optional
@@ -481,16 +481,38 @@ class BlockConfig:
     scale: Optional[float] = None  # default 1/sqrt(d)
 
 
-def _on_device(t: torch.Tensor):
-    """The call's device made current for the launch (nothing when it already is)."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+# The calls below serve single tokens, where the host's own work counts: shapes and
+# workspace sizes are looked up by their numbers, pointers go to ctypes as integers.
+
+
+@functools.lru_cache(maxsize=1024)
+def _bshape(*fields) -> "ctypes.Array":
+    """BlockShape of its thirteen fields, as the pointer that the C calls take."""
+    return ctypes.pointer(BlockShape(*fields))
+
+
+def _dp(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(what: str, t: torch.Tensor, stream, *args):
+    """Calls a C entry point with t's device current, on `stream` or t's device's current one."""
+    L = _lib if _lib is not None else load()
+    dev = t.device
+    if dev.index == torch.cuda.current_device():
+        st = (stream or torch.cuda.current_stream()).cuda_stream
+        status = getattr(L, what)(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            st = (stream or torch.cuda.current_stream()).cuda_stream
+            status = getattr(L, what)(*args, st)
+    if status:
+        _check(status, what)
 
 
 def _need(what: str, dtype, device, shape, t: Optional[torch.Tensor]):
     """A dense tensor of that type, device and shape, or None."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if not t.is_cuda:
         raise SvooError(f"{what} must live on a CUDA device")
@@ -498,40 +520,63 @@ def _need(what: str, dtype, device, shape, t: Optional[torch.Tensor]):
         raise SvooError(f"{what} must be {dtype} on {device}, not {t.dtype} on {t.device}")
     if tuple(t.shape) != tuple(shape):
         raise SvooError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise SvooError(f"{what} must be contiguous")
+    raise SvooError(f"{what} must be contiguous")
+
+
+def _queries(q: torch.Tensor):
+    if q.dim() != 4 or q.dtype is not torch.bfloat16 or not q.is_cuda:
+        raise SvooError("q must be a bf16 [B, H, N, d] tensor on a CUDA device")
+    if not q.is_contiguous():
+        raise SvooError("q must be contiguous")
+    return q.shape
 
 
 def _key_rows(what: str, t: torch.Tensor, device) -> int:
     """Rows from one head to the next of a bf16 [B, Hkv, Nk, d] tensor: contiguous, or the first Nk
     rows of every head of a longer contiguous buffer."""
-    if t.dim() != 4 or not t.is_cuda or t.dtype != torch.bfloat16 or t.device != device:
+    if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.device != device or not t.is_cuda:
         raise SvooError(f"{what} must be a bf16 [B, Hkv, N, d] tensor on {device}")
     B, Hkv, Nk, d = t.shape
     if t.is_contiguous():
         return Nk
-    cap = t.stride(1) // d if Hkv > 1 else t.stride(0) // d
-    if t.stride(3) != 1 or t.stride(2) != d or cap < Nk or (Hkv > 1 and t.stride(1) != cap * d) or \
-            (B > 1 and t.stride(0) != Hkv * cap * d):
+    s0, s1, s2, s3 = t.stride()
+    cap = s1 // d if Hkv > 1 else s0 // (Hkv * d)
+    if s3 != 1 or (s2 != d and Nk > 1) or cap < Nk or (Hkv > 1 and s1 != cap * d) or \
+            (B > 1 and s0 != Hkv * cap * d):
         raise SvooError(f"{what} must be contiguous or the first rows of every head of a contiguous buffer")
     return cap
 
 
-def _block_shape(q, k, v, cfg: BlockConfig, lengths, q_start) -> BlockShape:
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda:
-        raise SvooError("q must be a bf16 [B, H, N, d] tensor on a CUDA device")
-    if not q.is_contiguous():
-        raise SvooError("q must be contiguous")
-    B, H, Nq, d = q.shape
-    cap = _key_rows("k", k, q.device)
-    if v is not None and (v.shape != k.shape or _key_rows("v", v, q.device) != cap):
+def _block_args(q, k, v, cfg: BlockConfig, lengths, q_start):
+    """The fields of a call's BlockShape, after checking its tensors."""
+    B, H, Nq, d = _queries(q)
+    dev = q.device
+    cap = _key_rows("k", k, dev)
+    if v.shape != k.shape or _key_rows("v", v, dev) != cap:
         raise SvooError("k and v must have the same shape and strides")
-    if k.shape[0] != B or k.shape[3] != d:
+    Bk, Hkv, Nk, dk = k.shape
+    if Bk != B or dk != d:
         raise SvooError("q, k and v must agree in batch and head dimension")
-    _need("lengths", torch.int32, q.device, (B,), lengths)
-    Nk = k.shape[2]
-    return BlockShape(B, H, k.shape[1], Nq, Nk, cap, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local,
-                      1 if cfg.causal else 0, Nk - Nq if q_start is None else q_start)
+    _need("lengths", torch.int32, dev, (B,), lengths)
+    return (B, H, Hkv, Nq, Nk, cap, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
+            Nk - Nq if q_start is None else q_start)
+
+
+@functools.lru_cache(maxsize=1024)
+def _ws_bytes(what: str, *args) -> int:
+    """Bytes of a call's workspace (0 where the C side refuses the shape, as the call then does)."""
+    fn = getattr(load(), what)
+    if what == "svoo_cache_evict_workspace_size":
+        return fn(*args)
+    return fn(_bshape(*args[:13]), *args[13:])
+
+
+def _workspace(workspace, device, what: str, *args) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(_ws_bytes(what, *args), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise SvooError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
 
 
 def _block_scale(cfg: Optional[BlockConfig], d: int) -> float:
@@ -545,19 +590,19 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
     hold keys of each sequence are renewed (after a token was appended, last=1)."""
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, N, d] tensor on a CUDA device")
-    cap = _key_rows("k", k, k.device)
+    dev = k.device
+    cap = _key_rows("k", k, dev)
     B, Hkv, Nk, d = k.shape
     nb = -(-Nk // cfg.block) if cfg.block > 0 else 0
-    _need("lengths", torch.int32, k.device, (B,), lengths)
-    _need("pool", torch.float32, k.device, (B, Hkv, nb, d), pool)
+    _need("lengths", torch.int32, dev, (B,), lengths)
     if pool is None:
         if last:
             raise SvooError("last renews blocks of an existing pool: pass it")
-        pool = torch.empty(B, Hkv, nb, d, dtype=torch.float32, device=k.device)
-    sh = BlockShape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0)
-    with _on_device(k):
-        _check(load().svoo_block_pool(ctypes.byref(sh), _ptr(k), _ptr(lengths), last, _ptr(pool),
-                                      _stream(stream)), "svoo_block_pool")
+        pool = torch.empty(B, Hkv, nb, d, dtype=torch.float32, device=dev)
+    else:
+        _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
+    _call("svoo_block_pool", k, stream, _bshape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0),
+          k.data_ptr(), _dp(lengths), last, pool.data_ptr())
     return pool
 
 
@@ -567,25 +612,21 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
 
     n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
     queries are the last Nq of n_keys; -1: the last Nq of each sequence's lengths."""
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
-        raise SvooError("q must be a contiguous bf16 [B, H, N, d] tensor on a CUDA device")
-    B, H, Nq, d = q.shape
+    B, H, Nq, d = _queries(q)
+    dev = q.device
     nb = -(-n_keys // cfg.block) if cfg.block > 0 else 0
     Hkv = pool.shape[1] if pool.dim() == 4 else 0
-    _need("pool", torch.float32, q.device, (B, Hkv, nb, d), pool)
-    _need("lengths", torch.int32, q.device, (B,), lengths)
-    _need("idx", torch.int32, q.device, (B, Hkv, Nq, cfg.n_sel), idx)
+    _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
+    _need("lengths", torch.int32, dev, (B,), lengths)
     if idx is None:
-        idx = torch.empty(B, Hkv, Nq, max(cfg.n_sel, 0), dtype=torch.int32, device=q.device)
-    sh = BlockShape(B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local,
-                    1 if cfg.causal else 0, n_keys - Nq if q_start is None else q_start)
-    L = load()
-    if workspace is None:
-        workspace = torch.empty(L.svoo_block_select_workspace_size(ctypes.byref(sh)), dtype=torch.uint8,
-                                device=q.device)
-    with _on_device(q):
-        _check(L.svoo_block_select(ctypes.byref(sh), _ptr(q), _ptr(pool), _ptr(lengths), _ptr(idx), _ptr(workspace),
-                                   workspace.numel(), _ptr(dev_err), _stream(stream)), "svoo_block_select")
+        idx = torch.empty(B, Hkv, Nq, max(cfg.n_sel, 0), dtype=torch.int32, device=dev)
+    else:
+        _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
+    args = (B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
+            n_keys - Nq if q_start is None else q_start)
+    ws = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
+    _call("svoo_block_select", q, stream, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
+          idx.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _dp(dev_err))
     return idx
 
 
@@ -593,38 +634,35 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
                dev_err=None, stream=None):
     """Attention of every query over the blocks in idx; returns (o, lse). No gradient is recorded
     (block_attention records one)."""
-    sh = _block_shape(q, k, v, cfg, lengths, q_start)
-    _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, sh.Nq, cfg.n_sel), idx)
-    _need("out", torch.bfloat16, q.device, q.shape, out)
+    args = _block_args(q, k, v, cfg, lengths, q_start)
+    B, H, Hkv, Nq, _, _, d = args[:7]
+    dev = q.device
+    _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
+    _need("out", torch.bfloat16, dev, q.shape, out)
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(sh.B, sh.H, sh.Nq, dtype=torch.float32, device=q.device)
-    with _on_device(q):
-        _check(load().svoo_block_attn(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), _ptr(lengths),
-                                      _block_scale(cfg, sh.d), _ptr(out), _ptr(lse), _ptr(dev_err),
-                                      _stream(stream)), "svoo_block_attn")
+    lse = torch.empty(B, H, Nq, dtype=torch.float32, device=dev)
+    _call("svoo_block_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
+          _dp(lengths), _block_scale(cfg, d), out.data_ptr(), lse.data_ptr(), _dp(dev_err))
     return out, lse
 
 
 def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=None,
                         q_start: Optional[int] = None, workspace=None, dev_err=None, stream=None):
     """Gradient of block_attn: (dq, dk, dv), with idx, o and lse as block_attn had or gave them."""
-    sh = _block_shape(q, k, v, cfg, lengths, q_start)
-    _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, sh.Nq, cfg.n_sel), idx)
-    _need("o", torch.bfloat16, q.device, q.shape, o)
-    _need("grad_o", torch.bfloat16, q.device, q.shape, grad_o)
-    _need("lse", torch.float32, q.device, (sh.B, sh.H, sh.Nq), lse)
-    L = load()
-    if workspace is None:
-        workspace = torch.empty(L.svoo_block_attn_backward_workspace_size(ctypes.byref(sh)),
-                                dtype=torch.uint8, device=q.device)
+    args = _block_args(q, k, v, cfg, lengths, q_start)
+    B, H, Hkv, Nq, _, _, d = args[:7]
+    dev = q.device
+    _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
+    _need("o", torch.bfloat16, dev, q.shape, o)
+    _need("grad_o", torch.bfloat16, dev, q.shape, grad_o)
+    _need("lse", torch.float32, dev, (B, H, Nq), lse)
+    ws = _workspace(workspace, dev, "svoo_block_attn_backward_workspace_size", *args)
     dq = torch.empty_like(q)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    with _on_device(q):
-        _check(L.svoo_block_attn_backward(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
-                                          _ptr(grad_o), _ptr(idx), _ptr(lengths), _block_scale(cfg, sh.d),
-                                          _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
-                                          _ptr(dev_err), _stream(stream)), "svoo_block_attn_backward")
+    dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _call("svoo_block_attn_backward", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), _block_scale(cfg, d),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _dp(dev_err))
     return dq, dk, dv
 
 
@@ -652,11 +690,14 @@ def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[i
     blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
     right-padded batch. Differentiable in q, k and v (the selection is a constant of the gradient; the
     gradient's gradient is not offered). Returns (o, dict(idx, lse, pool, dev_err))."""
-    with torch.no_grad():
-        err = _err_buf(dev_err, q.device)
-        pool = block_pool(k, cfg, lengths)
-        idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start, dev_err=err)
-    o, lse = _BlockAttn.apply(q, k, v, idx, cfg, lengths, q_start, err)
+    _block_args(q, k, v, cfg, lengths, q_start)
+    err = _err_buf(dev_err, q.device)
+    pool = block_pool(k, cfg, lengths)
+    idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start, dev_err=err)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        o, lse = _BlockAttn.apply(q, k, v, idx, dataclasses.replace(cfg), lengths, q_start, err)
+    else:
+        o, lse = block_attn(q, k, v, idx, cfg, lengths, q_start, dev_err=err)
     return o, dict(idx=idx, lse=lse, pool=pool, dev_err=err)
 
 
@@ -676,27 +717,26 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
         raise SvooError("idx needs the BlockConfig that it was selected with")
     if idx is not None and weight is not None:
         raise SvooError("weights are summed over whole caches only: idx and weight exclude each other")
-    sh = _block_shape(q, k, v, cfg if cfg is not None else _WHOLE, lengths, 0)
+    args = _block_args(q, k, v, cfg if idx is not None else _WHOLE, lengths, 0)
+    B, H, Hkv, _, Nk, cap, d = args[:7]
+    dev = q.device
     if idx is not None:
-        _need("idx", torch.int32, q.device, (sh.B, sh.Hkv, 1, cfg.n_sel), idx)
-    if weight is not None and sh.cap != sh.Nk:
-        raise SvooError("weights need k and v as whole buffers")
-    _need("weight", torch.float32, q.device, (sh.B, sh.Hkv, sh.Nk), weight)
-    _need("out", torch.bfloat16, q.device, q.shape, out)
-    L = load()
-    if workspace is None:
-        workspace = torch.empty(L.svoo_cache_attn_workspace_size(ctypes.byref(sh), idx is not None, weight is not None),
-                                dtype=torch.uint8, device=q.device)
+        _need("idx", torch.int32, dev, (B, Hkv, 1, cfg.n_sel), idx)
+    if weight is not None:
+        if cap != Nk:
+            raise SvooError("weights need k and v as whole buffers")
+        _need("weight", torch.float32, dev, (B, Hkv, Nk), weight)
+    _need("out", torch.bfloat16, dev, q.shape, out)
+    ws = _workspace(workspace, dev, "svoo_cache_attn_workspace_size", *args, idx is not None, weight is not None)
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(sh.B, sh.H, 1, dtype=torch.float32, device=q.device)
-    with _on_device(q):
-        _check(L.svoo_cache_attn(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(idx),
-                                 _block_scale(cfg, sh.d), _ptr(weight), _ptr(out), _ptr(lse), _ptr(workspace),
-                                 workspace.numel(), _ptr(dev_err), _stream(stream)), "svoo_cache_attn")
+    lse = torch.empty(B, H, 1, dtype=torch.float32, device=dev)
+    _call("svoo_cache_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
+          _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size(), _dp(dev_err))
     return out, lse
 
 
-_WHOLE = BlockConfig()
+_WHOLE = BlockConfig()  # of a call without a selection
 
 
 def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: int = 0, workspace=None,
@@ -707,16 +747,12 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, cap, d] tensor on a CUDA device")
     B, Hkv, cap, d = k.shape
-    _need("k", torch.bfloat16, k.device, (B, Hkv, cap, d), k)
-    _need("v", torch.bfloat16, k.device, (B, Hkv, cap, d), v)
-    _need("weight", torch.float32, k.device, (B, Hkv, cap), weight)
-    _need("pos", torch.int32, k.device, (B, Hkv, cap), pos)
-    _need("lengths", torch.int32, k.device, (B,), lengths)
-    L = load()
-    if workspace is None:
-        workspace = torch.empty(L.svoo_cache_evict_workspace_size(B, Hkv, cap, keep), dtype=torch.uint8,
-                                device=k.device)
-    with _on_device(k):
-        _check(L.svoo_cache_evict(B, Hkv, cap, d, keep, sink, recent, _ptr(k), _ptr(v), _ptr(weight), _ptr(pos),
-                                  _ptr(lengths), _ptr(workspace), workspace.numel(), _stream(stream)),
-               "svoo_cache_evict")
+    dev = k.device
+    for what, t in (("k", k), ("v", v)):
+        _need(what, torch.bfloat16, dev, (B, Hkv, cap, d), t)
+    for what, t, dtype in (("weight", weight, torch.float32), ("pos", pos, torch.int32)):
+        _need(what, dtype, dev, (B, Hkv, cap), t)
+    _need("lengths", torch.int32, dev, (B,), lengths)
+    ws = _workspace(workspace, dev, "svoo_cache_evict_workspace_size", B, Hkv, cap, keep)
+    _call("svoo_cache_evict", k, stream, B, Hkv, cap, d, keep, sink, recent, k.data_ptr(), v.data_ptr(),
+          weight.data_ptr(), pos.data_ptr(), lengths.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())

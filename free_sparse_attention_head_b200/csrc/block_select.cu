@@ -306,16 +306,15 @@ __global__ void __launch_bounds__(kSelThreads)
 //
 // A thread owns a query (= TMEM lane) and streams its scores, 64 blocks a step,
 // through a list of at most kList candidates: a score enters when it is not
-// below the running cut; when the list runs full, the cut rises to just below
-// the m-th best so far (minus the border) and the list is packed. Scores never
-// leave the SM. Two CTAs share an SM, so one streams while the other loads.
+// below the running cut; when a step's would not fit, the cut rises to just
+// below the m-th best so far (minus the border) and the list is packed. Scores
+// never leave the SM. Two CTAs share an SM, so one streams while the other loads.
 // Warps 0-3 stream, 4 loads the means (TMA), 5 issues the products.
 // TMEM: A hi [0, 64), A lo [64, 128), scores [128, 192) and [192, 256).
 
 constexpr int kMmaSelThreads = 192;
 constexpr int kList = 64;         // candidates of a query
-constexpr int kGroup = 16;        // scores between two looks at the list's room
-constexpr int kMaxChosen = 40;    // blocks chosen by score: leaves room for a group and eight ties
+constexpr int kMaxChosen = 48;    // blocks chosen by score: leaves room for six more and ten ties
 constexpr int kMmaMaxBlocks = 6144;  // exact scores of a whole row fit where the lists were
 
 struct MmaSelSmem {
@@ -438,33 +437,51 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
     tmem_relinquish();
   }
   if (steps > 0) {
-    // group sums: coalesced loads, fp32 sums, bf16 parts to shared memory
-    constexpr int kChunks = D / 8;
-    for (int c = tid; c < kRowTile * kChunks; c += kMmaSelThreads) {
-      const int r = c / kChunks, ch = c - r * kChunks;
-      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (r < nt) {
-        const uint16_t* src = qh + static_cast<size_t>(t0 + r) * D + ch * 8;
-#pragma unroll 4
-        for (int g = 0; g < p.G; ++g) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + g * head);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    // group sums: coalesced loads (four rows at a time in flight), fp32 sums,
+    // bf16 parts to shared memory
+    constexpr int kChunks = D / 8, kStep = kMmaSelThreads / kChunks;
+    static_assert(kMmaSelThreads % kChunks == 0, "a thread keeps its columns");
+    const int ch = tid % kChunks;
+    for (int r0 = tid / kChunks; r0 < kRowTile; r0 += 4 * kStep) {
+      float a[4][8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[k][i] = 0.f;
+#pragma unroll 2
+      for (int g = 0; g < p.G; ++g) {
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = r0 + k * kStep;
+          x[k] = r < nt ? *reinterpret_cast<const uint4*>(qh + g * head + static_cast<size_t>(t0 + r) * D + ch * 8)
+                        : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            a[2 * i] += __uint_as_float(w[i] << 16);
-            a[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+            a[k][2 * i] += __uint_as_float(w[i] << 16);
+            a[k][2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
           }
         }
       }
-      uint32_t h[4], l[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
-        l[i] = pack_bf16x2(a[2 * i] - __uint_as_float(h[i] << 16), a[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * kStep;
+        if (r >= kRowTile) break;
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[i] = pack_bf16x2(a[k][2 * i], a[k][2 * i + 1]);
+          l[i] = pack_bf16x2(a[k][2 * i] - __uint_as_float(h[i] << 16),
+                             a[k][2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+        }
+        const uint32_t off = r * D * 2 + ((ch ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(stage + off) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(stage + kHalf + off) = make_uint4(l[0], l[1], l[2], l[3]);
       }
-      const uint32_t off = r * D * 2 + ((ch ^ (r & 7)) << 4);
-      *reinterpret_cast<uint4*>(stage + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(stage + kHalf + off) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
   tc_fence_before();
@@ -556,21 +573,37 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   } else {
     const int lo_c = all || m <= 0 ? 0 : cd.lo, hi_c = all || m <= 0 ? 0 : cd.hi;
     float cut = -3.402823466e38f;  // nothing below it can be among the m best
-    auto prune = [&]() {
-      // a value that m to m + 6 of the list's entries reach
-      const int nmax = warp_max(cnt);
+    float s[kKeyTile];
+    // Raises the cut to just below a value that m to m + 6 of the list's entries
+    // and this step's scores reach, and packs the list. The scores are in
+    // registers and the list's loads go together: a pass costs little more than
+    // its comparisons.
+    auto raise = [&]() {
+      const int nmax = (warp_max(cnt) + 7) & ~7;
       float lo = INFINITY, hi = -INFINITY;
+      int all_n = 0;  // entries and scores not below the cut
+#pragma unroll
+      for (int c = 0; c < kKeyTile; ++c)
+        if (s[c] >= cut) {
+          lo = fminf(lo, s[c]);
+          hi = fmaxf(hi, s[c]);
+          ++all_n;
+        }
+#pragma unroll 8
       for (int i = 0; i < nmax; ++i) {
         const float x = mv[i * 128];
-        if (i < cnt) {
+        if (i < cnt && x >= cut) {
           lo = fminf(lo, x);
           hi = fmaxf(hi, x);
+          ++all_n;
         }
       }
-      bool go = cnt > m + 6;
+      bool go = all_n > m + 6;
       for (int it = 0; it < 32 && __any_sync(0xffffffffu, go); ++it) {
         const float mid = 0.5f * lo + 0.5f * hi;
         int n = 0;
+#pragma unroll
+        for (int c = 0; c < kKeyTile; ++c) n += s[c] >= mid;
 #pragma unroll 8
         for (int i = 0; i < nmax; ++i) n += i < cnt && mv[i * 128] >= mid;
         if (go) {
@@ -583,29 +616,30 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
           }
         }
       }
-      if (cnt > m) cut = fmaxf(cut, lo - e2);
+      if (all_n > m) cut = fmaxf(cut, lo - e2);
       int w = 0;
-      for (int i = 0; i < nmax; ++i) {
-        const float x = mv[i * 128];
-        const uint16_t c = mi[i * 128];
-        if (i < cnt && x >= cut) {
-          mv[w * 128] = x;
-          mi[w * 128] = c;
-          ++w;
+      for (int i0 = 0; i0 < nmax; i0 += 8) {
+        float x[8];
+        uint16_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = mv[(i0 + i) * 128];
+          c[i] = mi[(i0 + i) * 128];
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < cnt && x[i] >= cut) {
+            mv[w * 128] = x[i];
+            mi[w * 128] = c[i];
+            ++w;
+          }
       }
       cnt = w;
-      if (cnt + kGroup > kList) {  // more ties than the list holds
-        hard = true;
-        cnt = 0;
-        cut = INFINITY;
-      }
     };
     for (int j = 0; j < steps; ++j) {
       const int st = j & 1, c0 = j * kKeyTile;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort))) break;
       tc_fence_after();
-      float s[kKeyTile];
       tmem_ld32f(lane_base + 128 + st * 64, s);
       tmem_ld32f(lane_base + 128 + st * 64 + 32, s + 32);
       tmem_wait_ld_f(s);
@@ -618,17 +652,26 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
         for (int c = 0; c < kKeyTile; ++c)
           if (c0 + c < lo_c || c0 + c >= hi_c) s[c] = -INFINITY;
       }
+      int fresh = 0;
 #pragma unroll
-      for (int g = 0; g < kKeyTile / kGroup; ++g) {
-        if (__any_sync(0xffffffffu, cnt + kGroup > kList)) prune();
+      for (int c = 0; c < kKeyTile; ++c) fresh += s[c] >= cut;
+      if (__any_sync(0xffffffffu, cnt + fresh > kList)) {
+        raise();
+        fresh = 0;
 #pragma unroll
-        for (int c = 0; c < kGroup; ++c) {
-          const float x = s[g * kGroup + c];
-          if (x >= cut) {
-            mv[cnt * 128] = x;
-            mi[cnt * 128] = static_cast<uint16_t>(c0 + g * kGroup + c);
-            ++cnt;
-          }
+        for (int c = 0; c < kKeyTile; ++c) fresh += s[c] >= cut;
+        if (cnt + fresh > kList) {  // more ties than the list holds
+          hard = true;
+          cnt = 0;
+          cut = INFINITY;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kKeyTile; ++c) {
+        if (s[c] >= cut) {
+          mv[cnt * 128] = s[c];
+          mi[cnt * 128] = static_cast<uint16_t>(c0 + c);
+          ++cnt;
         }
       }
     }
@@ -641,43 +684,45 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   } else if (warp < 4) {
     // m-th best of the list, and whether the border is clear
     const bool pick = !all && m > 0 && !hard && cnt > m;
-    const int nmax = warp_max(pick ? cnt : 0);
-    float lo = INFINITY, hi = -INFINITY;
-    for (int i = 0; i < nmax; ++i) {
-      const float x = mv[i * 128];
-      if (i < cnt) {
-        lo = fminf(lo, x);
-        hi = fmaxf(hi, x);
+    float tau = INFINITY;  // smallest score taken
+    bool unclear = false;
+    if (__any_sync(0xffffffffu, pick)) {
+      float x[kList];
+#pragma unroll
+      for (int i = 0; i < kList; ++i) x[i] = pick && i < cnt ? mv[i * 128] : -INFINITY;
+      float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kList; ++i) {
+        if (i < cnt) lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
       }
-    }
-    bool go = pick;
-    int n = cnt;
-    for (int it = 0; it < 40 && __any_sync(0xffffffffu, go); ++it) {
-      const float mid = 0.5f * lo + 0.5f * hi;
-      int k = 0;
-#pragma unroll 8
-      for (int i = 0; i < nmax; ++i) k += i < cnt && mv[i * 128] >= mid;
-      if (go) {
-        if (mid <= lo || mid >= hi) go = false;
-        else if (k >= m) {
-          lo = mid;
-          n = k;
-          go = k != m;
-        } else {
-          hi = mid;
+      bool go = pick;
+      int n = cnt;
+      for (int it = 0; it < 40 && __any_sync(0xffffffffu, go); ++it) {
+        const float mid = 0.5f * lo + 0.5f * hi;
+        int k = 0;
+#pragma unroll
+        for (int i = 0; i < kList; ++i) k += x[i] >= mid;
+        if (go) {
+          if (mid <= lo || mid >= hi) go = false;
+          else if (k >= m) {
+            lo = mid;
+            n = k;
+            go = k != m;
+          } else {
+            hi = mid;
+          }
         }
       }
-    }
-    float tau = INFINITY, out = -INFINITY;  // smallest taken, largest left out
-    for (int i = 0; i < nmax; ++i) {
-      const float x = mv[i * 128];
-      if (i < cnt) {
-        if (x >= lo) tau = fminf(tau, x);
-        else out = fmaxf(out, x);
+      float out = -INFINITY;  // largest left out
+#pragma unroll
+      for (int i = 0; i < kList; ++i) {
+        if (x[i] >= lo) tau = fminf(tau, x[i]);
+        else out = fmaxf(out, x[i]);
       }
+      unclear = pick && !(n == m && tau - out > e2);
     }
     float above = pick ? tau : -INFINITY;  // scores from here on are taken
-    const bool unclear = pick && !(n == m && tau - out > e2);
     unsigned todo = __ballot_sync(0xffffffffu, unclear);
     while (todo) {
       // one unclear query at a time, the whole warp: its border in fp64
@@ -685,14 +730,27 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       todo &= todo - 1;
       const float tr = __shfl_sync(0xffffffffu, tau, src), er = __shfl_sync(0xffffffffu, e2, src);
       const int nr = __shfl_sync(0xffffffffu, cnt, src), mr = __shfl_sync(0xffffffffu, m, src);
-      double qd[D / 32];
+      // group sums: eight lanes hold a query, D / 8 dimensions each, four times over
+      constexpr int kDims = D / 8;
+      const int part = lane & 7, who = lane >> 3;
+      double qd[kDims];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        qd[i] = 0.;
-        for (int g = 0; g < p.G; ++g)
-          qd[i] += static_cast<double>(bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + r) * D + i * 32 + lane]));
+      for (int i = 0; i < kDims; ++i) qd[i] = 0.;
+      for (int g = 0; g < p.G; ++g) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(qh + g * head + static_cast<size_t>(t0 + r) * D + part * kDims);
+#pragma unroll
+        for (int c = 0; c < kDims / 8; ++c) {
+          const uint4 x = src[c];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qd[c * 8 + 2 * i] += static_cast<double>(__uint_as_float(w[i] << 16));
+            qd[c * 8 + 2 * i + 1] += static_cast<double>(__uint_as_float(w[i] & 0xffff0000u));
+          }
+        }
       }
-      int sure = 0, near_n = 0;
+      int sure = 0;
       double ex[2] = {0., 0.};
       bool near[2];
 #pragma unroll
@@ -702,17 +760,33 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
         sure += __popc(__ballot_sync(0xffffffffu, x > tr + er));
         near[h] = i < nr && x <= tr + er && x >= tr - er;
         unsigned bal = __ballot_sync(0xffffffffu, near[h]);
-        near_n += __popc(bal);
         while (bal) {
-          const int at = __ffs(bal) - 1;
-          bal &= bal - 1;
-          const float* pc = pool + (static_cast<size_t>(blockIdx.y) * p.nb + li[(h * 32 + at) * 128 + r]) * D + lane;
+          // the next four candidates, one for every eight lanes
+          int at[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            at[k] = bal ? __ffs(bal) - 1 : -1;
+            bal &= bal - 1;
+          }
+          const int mine = at[who] < 0 ? at[0] : at[who];
+          const float4* pc = reinterpret_cast<const float4*>(
+              pool + (static_cast<size_t>(blockIdx.y) * p.nb + li[(h * 32 + mine) * 128 + r]) * D + part * kDims);
           double x64 = 0.;
 #pragma unroll
-          for (int d = 0; d < D / 32; ++d) x64 = fma(qd[d], static_cast<double>(pc[d * 32]), x64);
+          for (int c = 0; c < kDims / 4; ++c) {
+            const float4 v = pc[c];
+            x64 = fma(qd[4 * c], static_cast<double>(v.x), x64);
+            x64 = fma(qd[4 * c + 1], static_cast<double>(v.y), x64);
+            x64 = fma(qd[4 * c + 2], static_cast<double>(v.z), x64);
+            x64 = fma(qd[4 * c + 3], static_cast<double>(v.w), x64);
+          }
 #pragma unroll
-          for (int o = 16; o; o >>= 1) x64 += __shfl_xor_sync(0xffffffffu, x64, o);
-          if (lane == at) ex[h] = x64;
+          for (int o = 4; o; o >>= 1) x64 += __shfl_xor_sync(0xffffffffu, x64, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const double y = __shfl_sync(0xffffffffu, x64, k * 8);
+            if (lane == at[k]) ex[h] = y;
+          }
         }
       }
       const int need = mr - sure;
@@ -742,8 +816,18 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       } else if (!hard) {
         for (; w < cd.lo; ++w) row[w] = w;
         if (m > 0)
-          for (int i = 0; i < cnt; ++i)
-            if (mv[i * 128] >= above && w < p.n_sel) row[w++] = mi[i * 128];
+          for (int i0 = 0; i0 < cnt; i0 += 8) {
+            float x[8];
+            uint16_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              x[i] = mv[(i0 + i) * 128];
+              c[i] = mi[(i0 + i) * 128];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < cnt && x[i] >= above && w < p.n_sel) row[w++] = c[i];
+          }
         for (int c = cd.hi; c < cd.nc && w < p.n_sel; ++c) row[w++] = c;
       }
       for (; w < p.n_sel; ++w) row[w] = -1;
