@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(kSelThreads)
 // below the running cut; when a step's would not fit, the cut rises to just
 // below the m-th best so far (minus the border) and the list is packed. Scores
 // never leave the SM. Two CTAs share an SM, so one streams while the other loads.
+// (A first pass over the products for the cut alone, from the maxima of groups of
+// blocks, was no faster: 520 against 502 us at 65536 queries of 1024 blocks.)
 // Warps 0-3 stream, 4 loads the means (TMA), 5 issues the products.
 // TMEM: A hi [0, 64), A lo [64, 128), scores [128, 192) and [192, 256).
 
@@ -336,7 +338,7 @@ __host__ __device__ constexpr size_t sel_area_bytes() {  // the stages; at other
 }
 template <int D>
 constexpr size_t mma_sel_smem() {
-  return sel_area_bytes<D>() + static_cast<size_t>(kList) * 128 * 6 + sizeof(MmaSelSmem);
+  return sel_area_bytes<D>() + static_cast<size_t>(kList + 1) * 128 * 6 + sizeof(MmaSelSmem);
 }
 static_assert(2 * (mma_sel_smem<128>() + 1024) <= 233472, "two CTAs on an SM");
 
@@ -376,6 +378,28 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// how many of N values in registers reach x
+template <int N>
+__device__ __forceinline__ int reach(const float (&s)[N], float x) {
+  int n[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < N; ++c) n[c & 3] += s[c] >= x;
+  return (n[0] + n[1]) + (n[2] + n[3]);
+}
+
+// A search's next probe in [lo, hi): n_lo values reach lo, n_hi reach hi, about
+// `want` are to reach the probe. By the counts and by halves in turn.
+__device__ __forceinline__ float probe_at(float lo, float hi, int n_lo, int n_hi, int want, int it) {
+  float f = 0.5f;
+  if (!(it & 1)) f = fminf(fmaxf(__fdividef(n_lo - want - 0.5f, static_cast<float>(n_lo - n_hi)), 0.1f), 0.9f);
+  return lo + f * (hi - lo);
+}
+
+template <int N>
+struct Width {
+  static constexpr int value = N;
+};
+
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
 template <int D>
@@ -388,9 +412,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   constexpr int kHalf = kRowTile * D * 2;     // group sums, one part
   extern __shared__ __align__(1024) uint8_t sel_smem[];
   uint8_t* stage = sel_smem;
-  float* lv = reinterpret_cast<float*>(sel_smem + sel_area_bytes<D>());  // [kList][128]
-  uint16_t* li = reinterpret_cast<uint16_t*>(lv + kList * 128);
-  MmaSelSmem* S = reinterpret_cast<MmaSelSmem*>(li + kList * 128);
+  float* lv = reinterpret_cast<float*>(sel_smem + sel_area_bytes<D>());  // [kList + 1][128], the last is scrap
+  uint16_t* li = reinterpret_cast<uint16_t*>(lv + (kList + 1) * 128);
+  MmaSelSmem* S = reinterpret_cast<MmaSelSmem*>(li + (kList + 1) * 128);
   int32_t* ids = reinterpret_cast<int32_t*>(sel_smem);  // [128][n_sel], once the products are done
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -536,13 +560,13 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       tma_prefetch_desc(&pmap);
       const int row0 = blockIdx.y * nbp, lo_row = p.B * p.Hkv * nbp;
       for (int j = 0; j < steps; ++j) {
-        const int st = j & 1;
+        const int st = j & 1, c0 = j * kKeyTile;
         if (j >= 2 && !mbar_wait(smem_u32(&S->empty[st]), ((j - 2) >> 1) & 1, abort)) break;
         const uint32_t bar = smem_u32(&S->full[st]), dst = smem_u32(stage) + st * 2 * kTile;
         mbar_arrive_expect_tx(bar, 2 * kTile);
         for (int s = 0; s < kSub; ++s) {
-          tma_load_2d(&pmap, dst + s * kKeyTile * 128, bar, s * 64, row0 + j * kKeyTile);
-          tma_load_2d(&pmap, dst + kTile + s * kKeyTile * 128, bar, s * 64, lo_row + row0 + j * kKeyTile);
+          tma_load_2d(&pmap, dst + s * kKeyTile * 128, bar, s * 64, row0 + c0);
+          tma_load_2d(&pmap, dst + kTile + s * kKeyTile * 128, bar, s * 64, lo_row + row0 + c0);
         }
         armed = j;
       }
@@ -575,48 +599,48 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
     float cut = -3.402823466e38f;  // nothing below it can be among the m best
     float s[kKeyTile];
     // Raises the cut to just below a value that m to m + 6 of the list's entries
-    // and this step's scores reach, and packs the list. The scores are in
-    // registers and the list's loads go together: a pass costs little more than
-    // its comparisons.
+    // and this step's scores reach, and packs the list.
     auto raise = [&]() {
       const int nmax = (warp_max(cnt) + 7) & ~7;
       float lo = INFINITY, hi = -INFINITY;
-      int all_n = 0;  // entries and scores not below the cut
 #pragma unroll
-      for (int c = 0; c < kKeyTile; ++c)
-        if (s[c] >= cut) {
-          lo = fminf(lo, s[c]);
-          hi = fmaxf(hi, s[c]);
-          ++all_n;
-        }
+      for (int c = 0; c < kKeyTile; ++c) {
+        if (s[c] >= cut) lo = fminf(lo, s[c]);
+        hi = fmaxf(hi, s[c]);
+      }
 #pragma unroll 8
       for (int i = 0; i < nmax; ++i) {
         const float x = mv[i * 128];
         if (i < cnt && x >= cut) {
           lo = fminf(lo, x);
           hi = fmaxf(hi, x);
-          ++all_n;
         }
       }
-      bool go = all_n > m + 6;
-      for (int it = 0; it < 32 && __any_sync(0xffffffffu, go); ++it) {
-        const float mid = 0.5f * lo + 0.5f * hi;
-        int n = 0;
-#pragma unroll
-        for (int c = 0; c < kKeyTile; ++c) n += s[c] >= mid;
+      auto both = [&](float x) {
+        int n[4] = {reach(s, x), 0, 0, 0};
 #pragma unroll 8
-        for (int i = 0; i < nmax; ++i) n += i < cnt && mv[i * 128] >= mid;
+        for (int i = 0; i < nmax; ++i) n[i & 3] += i < cnt && mv[i * 128] >= x;
+        return (n[0] + n[1]) + (n[2] + n[3]);
+      };
+      int n_lo = both(lo), n_hi = 1;
+      const bool some = n_lo > m;
+      bool go = n_lo > m + 6;
+      for (int it = 0; it < 32 && __any_sync(0xffffffffu, go); ++it) {
+        const float mid = probe_at(lo, hi, n_lo, n_hi, m + 3, it);
+        const int n = both(mid);
         if (go) {
-          if (mid <= lo || mid >= hi) go = false;
+          if (mid <= lo || mid >= hi || hi - lo < e2) go = false;
           else if (n >= m) {
             lo = mid;
+            n_lo = n;
             go = n > m + 6;
           } else {
             hi = mid;
+            n_hi = n;
           }
         }
       }
-      if (all_n > m) cut = fmaxf(cut, lo - e2);
+      if (some) cut = fmaxf(cut, lo - e2);
       int w = 0;
       for (int i0 = 0; i0 < nmax; i0 += 8) {
         float x[8];
@@ -627,18 +651,18 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
           c[i] = mi[(i0 + i) * 128];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < cnt && x[i] >= cut) {
-            mv[w * 128] = x[i];
-            mi[w * 128] = c[i];
-            ++w;
-          }
+        for (int i = 0; i < 8; ++i) {  // w <= i0 + i: nothing unread is written over
+          mv[w * 128] = x[i];
+          mi[w * 128] = c[i];
+          w += i0 + i < cnt && x[i] >= cut;
+        }
       }
       cnt = w;
     };
-    for (int j = 0; j < steps; ++j) {
-      const int st = j & 1, c0 = j * kKeyTile;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort))) break;
+    // the next 64 scores into registers; what is not to be chosen at -inf
+    auto next = [&](int j, int c0) {
+      const int st = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[st]), (j >> 1) & 1, abort))) return false;
       tc_fence_after();
       tmem_ld32f(lane_base + 128 + st * 64, s);
       tmem_ld32f(lane_base + 128 + st * 64 + 32, s + 32);
@@ -652,26 +676,29 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
         for (int c = 0; c < kKeyTile; ++c)
           if (c0 + c < lo_c || c0 + c >= hi_c) s[c] = -INFINITY;
       }
-      int fresh = 0;
-#pragma unroll
-      for (int c = 0; c < kKeyTile; ++c) fresh += s[c] >= cut;
-      if (__any_sync(0xffffffffu, cnt + fresh > kList)) {
+      return true;
+    };
+    for (int j = 0; j < steps && next(j, j * kKeyTile); ++j) {
+      // the first step's cut from its own scores alone: most of them need not be listed
+      if ((j == 0 && steps > 1) || __any_sync(0xffffffffu, cnt + reach(s, cut) > kList)) {
         raise();
-        fresh = 0;
-#pragma unroll
-        for (int c = 0; c < kKeyTile; ++c) fresh += s[c] >= cut;
-        if (cnt + fresh > kList) {  // more ties than the list holds
+        if (cnt + reach(s, cut) > kList) {  // more ties than the list holds
           hard = true;
           cnt = 0;
           cut = INFINITY;
         }
       }
 #pragma unroll
-      for (int c = 0; c < kKeyTile; ++c) {
-        if (s[c] >= cut) {
+      for (int g = 0; g < kKeyTile / 8; ++g) {
+        float top = fmaxf(s[g * 8], s[g * 8 + 1]);
+#pragma unroll
+        for (int c = 2; c < 8; c += 2) top = fmax3(top, s[g * 8 + c], s[g * 8 + c + 1]);
+        if (!__any_sync(0xffffffffu, top >= cut)) continue;
+#pragma unroll
+        for (int c = g * 8; c < g * 8 + 8; ++c) {  // written in any case, kept when the count moves
           mv[cnt * 128] = s[c];
-          mi[cnt * 128] = static_cast<uint16_t>(c0 + c);
-          ++cnt;
+          mi[cnt * 128] = static_cast<uint16_t>(j * kKeyTile + c);
+          cnt += s[c] >= cut;
         }
       }
     }
@@ -684,51 +711,62 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   } else if (warp < 4) {
     // m-th best of the list, and whether the border is clear
     const bool pick = !all && m > 0 && !hard && cnt > m;
-    float tau = INFINITY;  // smallest score taken
+    float above = -INFINITY;           // scores from here on are taken
+    float edge_lo = 0.f, edge_hi = 0.f;  // of an unclear border
     bool unclear = false;
-    if (__any_sync(0xffffffffu, pick)) {
-      float x[kList];
+    auto border = [&](auto width) {
+      constexpr int N = decltype(width)::value;
+      float x[N];
 #pragma unroll
-      for (int i = 0; i < kList; ++i) x[i] = pick && i < cnt ? mv[i * 128] : -INFINITY;
+      for (int i = 0; i < N; ++i) x[i] = pick && i < cnt ? mv[i * 128] : -INFINITY;
       float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kList; ++i) {
+      for (int i = 0; i < N; ++i) {
         if (i < cnt) lo = fminf(lo, x[i]);
         hi = fmaxf(hi, x[i]);
       }
+      // the m-th best lies in [lo, hi]: n_lo >= m values reach lo, fewer reach
+      // hi, unless all the best are equal to it
       bool go = pick;
-      int n = cnt;
+      int n_lo = cnt, n_hi = 1;
       for (int it = 0; it < 40 && __any_sync(0xffffffffu, go); ++it) {
-        const float mid = 0.5f * lo + 0.5f * hi;
-        int k = 0;
-#pragma unroll
-        for (int i = 0; i < kList; ++i) k += x[i] >= mid;
+        const float mid = probe_at(lo, hi, n_lo, n_hi, m, it);
+        const int n = reach(x, mid);
         if (go) {
-          if (mid <= lo || mid >= hi) go = false;
-          else if (k >= m) {
+          if (mid <= lo || mid >= hi || hi - lo < e2) go = false;  // as near as the border test asks for
+          else if (n >= m) {
             lo = mid;
-            n = k;
-            go = k != m;
+            n_lo = n;
+            go = n != m;
           } else {
             hi = mid;
+            n_hi = n;
           }
         }
       }
-      float out = -INFINITY;  // largest left out
+      float in = INFINITY, out = -INFINITY;  // smallest taken, largest left out
 #pragma unroll
-      for (int i = 0; i < kList; ++i) {
-        if (x[i] >= lo) tau = fminf(tau, x[i]);
+      for (int i = 0; i < N; ++i) {
+        if (x[i] >= lo) in = fminf(in, x[i]);
         else out = fmaxf(out, x[i]);
       }
-      unclear = pick && !(n == m && tau - out > e2);
-    }
-    float above = pick ? tau : -INFINITY;  // scores from here on are taken
+      if (pick) {
+        above = in;
+        unclear = !(n_lo == m && in - out > e2);
+        if (n_lo == m) lo = hi = in;
+        edge_lo = lo - e2;
+        edge_hi = hi + e2;
+      }
+    };
+    const int longest = warp_max(pick ? cnt : 0);
+    if (longest > 32) border(Width<kList>());
+    else if (longest > 0) border(Width<32>());
     unsigned todo = __ballot_sync(0xffffffffu, unclear);
     while (todo) {
       // one unclear query at a time, the whole warp: its border in fp64
       const int src = __ffs(todo) - 1, r = (warp << 5) + src;
       todo &= todo - 1;
-      const float tr = __shfl_sync(0xffffffffu, tau, src), er = __shfl_sync(0xffffffffu, e2, src);
+      const float el = __shfl_sync(0xffffffffu, edge_lo, src), eh = __shfl_sync(0xffffffffu, edge_hi, src);
       const int nr = __shfl_sync(0xffffffffu, cnt, src), mr = __shfl_sync(0xffffffffu, m, src);
       // group sums: eight lanes hold a query, D / 8 dimensions each, four times over
       constexpr int kDims = D / 8;
@@ -757,8 +795,8 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       for (int h = 0; h < 2; ++h) {
         const int i = h * 32 + lane;
         const float x = i < nr ? lv[i * 128 + r] : -INFINITY;
-        sure += __popc(__ballot_sync(0xffffffffu, x > tr + er));
-        near[h] = i < nr && x <= tr + er && x >= tr - er;
+        sure += __popc(__ballot_sync(0xffffffffu, x > eh));
+        near[h] = i < nr && x <= eh && x >= el;
         unsigned bal = __ballot_sync(0xffffffffu, near[h]);
         while (bal) {
           // the next four candidates, one for every eight lanes
@@ -805,7 +843,7 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (near[h]) lv[(h * 32 + lane) * 128 + r] = rank[h] < need ? INFINITY : -INFINITY;
-      if (lane == src) above = tr + er;
+      if (lane == src) above = nextafterf(eh, INFINITY);  // INF marks the near ones that are taken
       __syncwarp();
     }
     if (tid < nt) {
