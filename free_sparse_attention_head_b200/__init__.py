@@ -497,15 +497,14 @@ def _dp(t: Optional[torch.Tensor]):
 
 def _call(what: str, t: torch.Tensor, stream, *args):
     """Calls a C entry point with t's device current, on `stream` or t's device's current one."""
-    L = _lib if _lib is not None else load()
-    dev = t.device
-    if dev.index == torch.cuda.current_device():
-        st = (stream or torch.cuda.current_stream()).cuda_stream
-        status = getattr(L, what)(*args, st)
+    fn = getattr(_lib if _lib is not None else load(), what)
+    dev = t.device.index
+    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, st)
     else:
         with torch.cuda.device(dev):
-            st = (stream or torch.cuda.current_stream()).cuda_stream
-            status = getattr(L, what)(*args, st)
+            status = fn(*args, st)
     if status:
         _check(status, what)
 

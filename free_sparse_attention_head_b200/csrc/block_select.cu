@@ -63,13 +63,21 @@ __global__ void __launch_bounds__(128)
 constexpr int kSelThreads = 256;
 constexpr int kAmb = 64;  // border candidates kept with their exact scores
 
-// unsigned keys in the order of the floats
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+// how many of N values in registers reach x
+template <int N>
+__device__ __forceinline__ int reach(const float (&s)[N], float x) {
+  int n[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < N; ++c) n[c & 3] += s[c] >= x;
+  return (n[0] + n[1]) + (n[2] + n[3]);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+
+// A search's next probe in [lo, hi): n_lo values reach lo, n_hi reach hi, about
+// `want` are to reach the probe. By the counts and by halves in turn.
+__device__ __forceinline__ float probe_at(float lo, float hi, int n_lo, int n_hi, int want, int it) {
+  float f = 0.5f;
+  if (!(it & 1)) f = fminf(fmaxf(__fdividef(n_lo - want - 0.5f, static_cast<float>(n_lo - n_hi)), 0.1f), 0.9f);
+  return lo + f * (hi - lo);
 }
 
 struct SelWarp {
@@ -119,6 +127,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const int t = i / D, d = i - t * D;
     float a = 0.f;
     if (t < nt)
+#pragma unroll 8
       for (int g = 0; g < p.G; ++g) a += bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + t) * D + d]);
     qs[i] = a;
   }
@@ -132,28 +141,55 @@ __global__ void __launch_bounds__(kSelThreads)
   __syncthreads();
   if (most > p.n_sel) {
     float big = 0.f;
-    for (int c0 = warp * 32; c0 < nmax; c0 += kSelThreads) {
-      const int c = c0 + lane;
-      const float4* row = reinterpret_cast<const float4*>(pl + static_cast<size_t>(min(c, nmax - 1)) * D);
-      float acc[TQ], n2 = 0.f;
+    if (TQ == 1) {
+      // one query: a warp reads whole rows (128 / D of them at a time, eight
+      // loads in flight) and sums across lanes
+      constexpr int kLanes = D / 4, kRows = 32 / kLanes;
+      const int part = lane % kLanes, sub = lane / kLanes;
+      const float4 y = *reinterpret_cast<const float4*>(qs + part * 4);
+      for (int c0 = warp * kRows * 8; c0 < nmax; c0 += (kSelThreads / 32) * kRows * 8) {
+        float4 x[8];
 #pragma unroll
-      for (int t = 0; t < TQ; ++t) acc[t] = 0.f;
-#pragma unroll 2
-      for (int d = 0; d < D / 4; ++d) {
-        const float4 x = row[d];
-        n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, n2))));
+        for (int i = 0; i < 8; ++i) {
+          const int c = min(c0 + i * kRows + sub, nmax - 1);
+          x[i] = *reinterpret_cast<const float4*>(pl + static_cast<size_t>(c) * D + part * 4);
+        }
 #pragma unroll
-        for (int t = 0; t < TQ; ++t) {
-          const float4 y = *reinterpret_cast<const float4*>(qs + t * D + d * 4);
-          acc[t] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[t]))));
+        for (int i = 0; i < 8; ++i) {
+          // largest partial norm of each lane; their sum bounds every row's
+          big = fmaxf(big, fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, fmaf(x[i].z, x[i].z, x[i].w * x[i].w))));
+          float a = fmaf(x[i].x, y.x, fmaf(x[i].y, y.y, fmaf(x[i].z, y.z, x[i].w * y.w)));
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          const int c = c0 + i * kRows + sub;
+          if (part == 0 && c < nmax) sc[c] = a;
         }
       }
-      big = fmaxf(big, n2);
-      if (c < nmax) {
 #pragma unroll
-        for (int t = 0; t < TQ; ++t) sc[t * pitch + c] = acc[t];
+      for (int o = kLanes / 2; o; o >>= 1) big += __shfl_xor_sync(0xffffffffu, big, o);
+    } else
+      for (int c0 = warp * 32; c0 < nmax; c0 += kSelThreads) {
+        const int c = c0 + lane;
+        const float4* row = reinterpret_cast<const float4*>(pl + static_cast<size_t>(min(c, nmax - 1)) * D);
+        float acc[TQ], n2 = 0.f;
+  #pragma unroll
+        for (int t = 0; t < TQ; ++t) acc[t] = 0.f;
+  #pragma unroll 2
+        for (int d = 0; d < D / 4; ++d) {
+          const float4 x = row[d];
+          n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, n2))));
+  #pragma unroll
+          for (int t = 0; t < TQ; ++t) {
+            const float4 y = *reinterpret_cast<const float4*>(qs + t * D + d * 4);
+            acc[t] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[t]))));
+          }
+        }
+        big = fmaxf(big, n2);
+        if (c < nmax) {
+  #pragma unroll
+          for (int t = 0; t < TQ; ++t) sc[t * pitch + c] = acc[t];
+        }
       }
-    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     if (lane == 0) atomicMax(&pool_norm2, __float_as_int(big));
@@ -169,40 +205,40 @@ __global__ void __launch_bounds__(kSelThreads)
     float cut = INFINITY;   // scores above it are taken
     bool incl = false;      // ... and those equal to it
     if (!all && m > 0) {
-      // m-th largest score: bisection over the ordered keys
-      uint32_t lo = 0xffffffffu, hi = 0;
-      for (int c = cd.lo + lane; c < cd.hi; c += 32) {
-        const uint32_t k = order_key(s[c]);
-        lo = min(lo, k);
-        hi = max(hi, k);
+      // the m-th largest score, between `lo`, which n_lo >= m scores reach, and
+      // `hi`, which fewer do; up to 32 a lane in registers
+      constexpr int kHeld = 32;
+      const bool few = cd.hi - cd.lo <= 32 * kHeld;
+      float held[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int c = cd.lo + i * 32 + lane;
+        held[i] = few && c < cd.hi ? s[c] : -INFINITY;
       }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+      auto count = [&](float x) {
         int n = 0;
-        for (int c = cd.lo + lane; c < cd.hi; c += 32) n += order_key(s[c]) >= mid;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (n >= m) lo = mid;
-        else hi = mid - 1;
-        if (n == m) break;
-      }
-      // smallest score taken, largest left out, how many are taken
-      uint32_t in = 0xffffffffu, outk = 0;
-      int n = 0;
-      for (int c = cd.lo + lane; c < cd.hi; c += 32) {
-        const uint32_t k = order_key(s[c]);
-        if (k >= lo) {
-          in = min(in, k);
-          ++n;
+        if (few) {
+          if (cd.hi - cd.lo <= 128) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n += held[i] >= x;
+          } else {
+            n = reach(held, x);
+          }
         } else {
-          outk = max(outk, k);
+          for (int c = cd.lo + lane; c < cd.hi; c += 32) n += s[c] >= x;
         }
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+      };
+      float lo = INFINITY, hi = -INFINITY;
+      for (int c = cd.lo + lane; c < cd.hi; c += 32) {
+        lo = fminf(lo, s[c]);
+        hi = fmaxf(hi, s[c]);
       }
-      in = __reduce_min_sync(0xffffffffu, in);
-      outk = __reduce_max_sync(0xffffffffu, outk);
-      n = __reduce_add_sync(0xffffffffu, n);
-      const float tau = key_value(in);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
       float q2 = 0.f;
       for (int d = lane; d < D; d += 32) q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
 #pragma unroll
@@ -210,12 +246,38 @@ __global__ void __launch_bounds__(kSelThreads)
       // |fp32 score - score| <= (D + G + 2) 2^-24 sum |q_d pool_d| <= (D + G + 2) 2^-24 |q||pool|,
       // and the norms themselves are good to far better than the 1.5 spent on them
       const float e2 = 3.f * (D + p.G + 2) * 5.9604645e-8f * sqrtf(q2) * sqrtf(__int_as_float(pool_norm2));
-      if (n == m && tau - key_value(outk) > e2) {
-        cut = tau;
+      int n = cd.hi - cd.lo, n_hi = 1;
+      for (int it = 0; it < 48 && n != m; ++it) {
+        const float mid = probe_at(lo, hi, n, n_hi, m, it);
+        if (mid <= lo || mid >= hi || hi - lo < e2) break;
+        const int k = count(mid);
+        if (k >= m) {
+          lo = mid;
+          n = k;
+        } else {
+          hi = mid;
+          n_hi = k;
+        }
+      }
+      // smallest score taken, largest left out
+      float in = INFINITY, out_s = -INFINITY;
+      for (int c = cd.lo + lane; c < cd.hi; c += 32) {
+        if (s[c] >= lo) in = fminf(in, s[c]);
+        else out_s = fmaxf(out_s, s[c]);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        in = fminf(in, __shfl_xor_sync(0xffffffffu, in, o));
+        out_s = fmaxf(out_s, __shfl_xor_sync(0xffffffffu, out_s, o));
+      }
+      if (n == m && in - out_s > e2) {
+        cut = in;
         incl = true;
       } else {
         // border: scored again in fp64, the best `need` of them are taken
-        cut = tau + e2;
+        if (n == m) lo = hi = in;
+        const float edge = lo - e2;
+        cut = hi + e2;
         int sure = 0, na = 0;
         double qd[D / 32];
 #pragma unroll
@@ -237,7 +299,7 @@ __global__ void __launch_bounds__(kSelThreads)
           const int c = c0 + lane;
           const float x = c < cd.hi ? s[c] : 0.f;
           sure += __popc(__ballot_sync(0xffffffffu, c < cd.hi && x > cut));
-          const unsigned near = __ballot_sync(0xffffffffu, c < cd.hi && x <= cut && x >= tau - e2);
+          const unsigned near = __ballot_sync(0xffffffffu, c < cd.hi && x <= cut && x >= edge);
           const int at = na + __popc(near & ((1u << lane) - 1u));
           if (((near >> lane) & 1u) && at < kAmb) amb[warp].blk[at] = c;
           na += __popc(near);
@@ -267,7 +329,7 @@ __global__ void __launch_bounds__(kSelThreads)
             int at = -1;
             for (int c = cd.lo; c < cd.hi; ++c) {
               const float x = s[c];
-              if (!(x <= cut && x >= tau - e2)) continue;
+              if (!(x <= cut && x >= edge)) continue;
               const double y = exact(c);
               if (at < 0 || y > best) {
                 best = y;
@@ -376,23 +438,6 @@ __global__ void __launch_bounds__(256)
     for (int w = 1; w < 8; ++w) big = fmaxf(big, best[w]);
     norms[static_cast<size_t>(bh) * gridDim.x + blockIdx.x] = big;
   }
-}
-
-// how many of N values in registers reach x
-template <int N>
-__device__ __forceinline__ int reach(const float (&s)[N], float x) {
-  int n[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int c = 0; c < N; ++c) n[c & 3] += s[c] >= x;
-  return (n[0] + n[1]) + (n[2] + n[3]);
-}
-
-// A search's next probe in [lo, hi): n_lo values reach lo, n_hi reach hi, about
-// `want` are to reach the probe. By the counts and by halves in turn.
-__device__ __forceinline__ float probe_at(float lo, float hi, int n_lo, int n_hi, int want, int it) {
-  float f = 0.5f;
-  if (!(it & 1)) f = fminf(fmaxf(__fdividef(n_lo - want - 0.5f, static_cast<float>(n_lo - n_hi)), 0.1f), 0.9f);
-  return lo + f * (hi - lo);
 }
 
 template <int N>

@@ -301,61 +301,81 @@ __global__ void __launch_bounds__(kCacheThreads)
 
 // Grid (1 + chunks of 1024 slots where weights are kept, B * Hkv). Block 0
 // joins the runs of the group's heads (when there are several), the others add
-// the slots' weights.
+// the slots' weights. Dynamic shared memory: a factor per (head, run).
 template <int D>
 __global__ void __launch_bounds__(256)
     cache_join_kernel(BlockDims p, int runs, const int32_t* __restrict__ lengths, const float* __restrict__ part_o,
                       const float2* __restrict__ part_ml, const float* __restrict__ scores, uint16_t* __restrict__ o,
                       float* __restrict__ lse, float* __restrict__ weight) {
-  __shared__ float lse2[kRowTile], top[kRowTile];
+  extern __shared__ float factor[];
+  __shared__ float lse2[kRowTile];
   const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh - b * p.Hkv;
   const size_t row0 = static_cast<size_t>(b) * p.H + hk * p.G, rows = static_cast<size_t>(p.B) * p.H;
-  const int tid = threadIdx.x;
-  for (int g = tid; g < p.G; g += 256) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int g = warp; g < p.G; g += 8) {
+    float l2;
     if (runs > 1) {
+      // lanes over the runs (at most 256: eight a lane)
+      float2 v[8];
       float mm = -INFINITY, ll = 0.f;
-      for (int x = 0; x < runs; ++x) mm = fmaxf(mm, part_ml[x * rows + row0 + g].x);
-      for (int x = 0; x < runs; ++x) {
-        const float2 v = part_ml[x * rows + row0 + g];
-        if (v.y > 0.f) ll = fmaf(v.y, ex2_approx(v.x - mm), ll);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = i * 32 + lane;
+        v[i] = x < runs ? part_ml[x * rows + row0 + g] : make_float2(-INFINITY, 0.f);
+        mm = fmaxf(mm, v[i].x);
       }
-      top[g] = mm;
-      lse2[g] = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+#pragma unroll
+      for (int s = 16; s; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (v[i].y > 0.f) ll = fmaf(v[i].y, ex2_approx(v[i].x - mm), ll);
+#pragma unroll
+      for (int s = 16; s; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
+      l2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+      if (blockIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 32 + lane < runs) factor[g * runs + i * 32 + lane] = v[i].y > 0.f ? ex2_approx(v[i].x - l2) : 0.f;
+      }
     } else {
-      lse2[g] = lse[row0 + g] * 1.4426950408889634f;
+      l2 = lse[row0 + g] * 1.4426950408889634f;
     }
+    if (lane == 0) lse2[g] = l2;
   }
   __syncthreads();
   if (blockIdx.x == 0) {
     if (runs == 1) return;
     for (int i = tid; i < p.G * (D / 2); i += 256) {
       const int g = i / (D / 2), c = (i - g * (D / 2)) * 2;
+      const float* f = factor + g * runs;
+      const float* src = part_o + (row0 + g) * D + c;
       float a = 0.f, e = 0.f;
-      const float l2 = lse2[g];
+#pragma unroll 8
       for (int x = 0; x < runs; ++x) {
-        const float2 ml = part_ml[x * rows + row0 + g];
-        if (!(ml.y > 0.f)) continue;
-        const float f = ex2_approx(ml.x - l2);
-        const float2 v = *reinterpret_cast<const float2*>(part_o + (x * rows + row0 + g) * D + c);
-        a = fmaf(v.x, f, a);
-        e = fmaf(v.y, f, e);
+        const float2 v = *reinterpret_cast<const float2*>(src + x * rows * D);
+        a = fmaf(v.x, f[x], a);
+        e = fmaf(v.y, f[x], e);
       }
       *reinterpret_cast<uint32_t*>(o + (row0 + g) * D + c) = pack_bf16x2(a, e);
-      if (c == 0) lse[row0 + g] = l2 * 0.6931471805599453f;
+      if (c == 0) lse[row0 + g] = lse2[g] * 0.6931471805599453f;
     }
     return;
   }
   const int len = seq_len(p, lengths, b);
-  const int k0 = (blockIdx.x - 1) * 1024;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = k0 + i * 256 + tid;
-    if (key >= len) break;
-    float a = 0.f;
+  const int k0 = (blockIdx.x - 1) * 1024 + tid;
+  if (k0 - tid >= len) return;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int g = 0; g < p.G; ++g) a += ex2_approx(scores[(row0 + g) * p.cap + key] - lse2[g]);
-    weight[static_cast<size_t>(bh) * p.cap + key] += a;
+  for (int g = 0; g < p.G; ++g) {
+    const float* src = scores + (row0 + g) * p.cap;
+    const float l2 = lse2[g];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k0 + i * 256 < len) a[i] += ex2_approx(src[k0 + i * 256] - l2);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (k0 + i * 256 < len) weight[static_cast<size_t>(bh) * p.cap + k0 + i * 256] += a[i];
 }
 
 // Runs per (sequence, key head): enough CTAs to fill the card four times over
@@ -408,8 +428,12 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
   cache_attn_kernel<D><<<dim3(c.runs, p.B * p.Hkv, (p.G + kHeadRows - 1) / kHeadRows), kCacheThreads, smem, st>>>(
       km, vm, p, static_cast<const uint16_t*>(q), idx, lengths, scale_log2, weight ? c.scores : nullptr, c.part_o,
       c.part_ml, static_cast<uint16_t*>(o), lse, dev_err);
+  const size_t factors = c.runs > 1 ? static_cast<size_t>(p.G) * c.runs * 4 : 0;
+  if (factors > 48 * 1024 && cudaFuncSetAttribute(cache_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  static_cast<int>(factors)) != cudaSuccess)
+    return SVOO_ERR_CUDA;
   if (c.runs > 1 || weight)
-    cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, 0, st>>>(
+    cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, factors, st>>>(
         p, c.runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight);
   return launch_status();
 }
@@ -456,7 +480,9 @@ __device__ __forceinline__ int evict_exclusive(int x, int* warp_sums, int* all) 
 // One CTA per (sequence, key head). Finds the keep-th largest key by radix
 // selection (four passes of 8 bits), then walks the slots in order: equal keys
 // stay from the lowest slot up; evicted slots below `keep` are holes, kept ones
-// from `keep` on are sources. moves: the i-th hole and the i-th source.
+// from `keep` on are sources. moves: the i-th hole and the i-th source. R keys a
+// thread stay in registers; R = 0 reads the weights anew in every pass.
+template <int R>
 __global__ void __launch_bounds__(kEvictThreads)
     evict_select_kernel(EvictDims p, const float* __restrict__ weight, const int32_t* __restrict__ pos,
                         const int32_t* __restrict__ lengths, int m_cap, int2* __restrict__ moves,
@@ -472,22 +498,53 @@ __global__ void __launch_bounds__(kEvictThreads)
   const float* w = weight + static_cast<size_t>(bh) * p.cap;
   const int32_t* ps = pos + static_cast<size_t>(bh) * p.cap;
   if (tid == 0) newest_s = -1;
-  __syncthreads();
+  if (tid < 256) hist[tid] = 0;
+  uint32_t held[R ? R : 1];
+  int place[R ? R : 1];
   int newest = -1;
-  for (int i = tid; i < len; i += kEvictThreads) newest = max(newest, ps[i]);
+  if (R) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * kEvictThreads + tid;
+      held[r] = i < len ? __float_as_uint(w[i]) : 0u;
+      place[r] = i < len ? ps[i] : -1;
+      newest = max(newest, place[r]);
+    }
+  } else {
+    for (int i = tid; i < len; i += kEvictThreads) newest = max(newest, ps[i]);
+  }
+  __syncthreads();
   newest = __reduce_max_sync(0xffffffffu, newest);
   if ((tid & 31) == 0) atomicMax(&newest_s, newest);
   __syncthreads();
   newest = newest_s;
+  if (R) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) held[r] = evict_key(__uint_as_float(held[r]), place[r], p.sink, newest, p.recent);
+  }
+  const int rounds = (len + kEvictThreads - 1) / kEvictThreads;
+  // f(slot, key) for every slot, a round of threads at a time
+  auto each = [&](auto f) {
+    if (R) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rounds) f(r * kEvictThreads + tid, held[r]);
+    } else {
+      for (int r = 0; r < rounds; ++r) {
+        const int i = r * kEvictThreads + tid;
+        f(i, i < len ? evict_key(w[i], ps[i], p.sink, newest, p.recent) : 0u);
+      }
+    }
+  };
   uint32_t prefix = 0, mask = 0;
   int want = p.keep;  // the want-th largest of those that match the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < len; i += kEvictThreads) {
-      const uint32_t k = evict_key(w[i], ps[i], p.sink, newest, p.recent);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-    }
+    each([&](int i, uint32_t k) {
+      // weights share their leading bits: one addition per digit and warp
+      const bool in = i < len && (k & mask) == prefix;
+      const unsigned same = __match_any_sync(0xffffffffu, in ? (k >> shift) & 255u : 256u);
+      if (in && (same & ((1u << (tid & 31)) - 1u)) == 0) atomicAdd(&hist[(k >> shift) & 255], __popc(same));
+    });
     __syncthreads();
     if (tid < 32) {
       // from the top: lane l holds digits 255 - 8 l ... 248 - 8 l
@@ -495,6 +552,7 @@ __global__ void __launch_bounds__(kEvictThreads)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         c[i] = hist[255 - tid * 8 - i];
+        hist[255 - tid * 8 - i] = 0;
         s += c[i];
       }
       int inc = s;
@@ -519,13 +577,10 @@ __global__ void __launch_bounds__(kEvictThreads)
     prefix |= static_cast<uint32_t>(digit_s) << shift;
     mask |= 255u << shift;
     want = left_s;
-    __syncthreads();
   }
   // kept: keys above `prefix`, and the first `want` equal to it
   int equal = 0, holes = 0, srcs = 0;
-  for (int i0 = 0; i0 < len; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < len ? evict_key(w[i], ps[i], p.sink, newest, p.recent) : 0;
+  each([&](int i, uint32_t k) {
     int all;
     const int before = equal + evict_exclusive(i < len && k == prefix, sums, &all);
     equal += all;
@@ -538,30 +593,50 @@ __global__ void __launch_bounds__(kEvictThreads)
     if (src) moves[static_cast<size_t>(bh) * m_cap + srcs + (at >> 16)].y = i;
     holes += both & 0xffff;
     srcs += both >> 16;
-  }
+  });
   if (tid == 0) n_moves[bh] = srcs;
 }
 
-// Grid (chunks, B * Hkv): one warp per move (both rows, the weight, the
-// position). Sources lie at or behind `keep`, holes before it: no order needed.
+// Grid (chunks, B * Hkv): the lanes of a move carry both its rows, 16 bytes
+// each, four moves in flight; weight and position with them. Sources lie at or
+// behind `keep`, holes before it: no order needed.
 template <int D>
 __global__ void __launch_bounds__(256)
     evict_move_kernel(EvictDims p, int m_cap, const int2* __restrict__ moves, const int32_t* __restrict__ n_moves,
                       uint16_t* __restrict__ k, uint16_t* __restrict__ v, float* __restrict__ weight,
                       int32_t* __restrict__ pos, int32_t* __restrict__ lengths) {
-  const int bh = blockIdx.y, lane = threadIdx.x & 31;
-  const int n = n_moves[bh];
   constexpr int kLanes = D / 8;  // 16-byte pieces of a row
+  constexpr int kSide = 256 / (2 * kLanes);  // moves side by side in a CTA
+  constexpr int kDeep = 4;
+  const int bh = blockIdx.y, n = n_moves[bh];
+  const int in = threadIdx.x % (2 * kLanes), side = threadIdx.x / (2 * kLanes);
   const size_t base = static_cast<size_t>(bh) * p.cap;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
-    const int2 mv = moves[static_cast<size_t>(bh) * m_cap + i];
-    if (lane < 2 * kLanes) {
-      uint16_t* x = lane < kLanes ? k : v;
-      const int c = (lane % kLanes) * 8;
-      *reinterpret_cast<uint4*>(x + (base + mv.x) * D + c) = *reinterpret_cast<const uint4*>(x + (base + mv.y) * D + c);
+  uint16_t* x = (in < kLanes ? k : v) + base * D + (in % kLanes) * 8;
+  const int2* mine = moves + static_cast<size_t>(bh) * m_cap;
+  for (int i0 = blockIdx.x * kSide * kDeep + side; i0 < n; i0 += gridDim.x * kSide * kDeep) {
+    int2 mv[kDeep];
+    uint4 row[kDeep];
+    float w[kDeep];
+    int32_t ps[kDeep];
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      const int i = i0 + j * kSide;
+      mv[j] = i < n ? mine[i] : make_int2(-1, -1);
     }
-    if (lane == 0) weight[base + mv.x] = weight[base + mv.y];
-    if (lane == 1) pos[base + mv.x] = pos[base + mv.y];
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      if (mv[j].y < 0) continue;
+      row[j] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(mv[j].y) * D);
+      if (in == 0) w[j] = weight[base + mv[j].y];
+      if (in == 1) ps[j] = pos[base + mv[j].y];
+    }
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) {
+      if (mv[j].y < 0) continue;
+      *reinterpret_cast<uint4*>(x + static_cast<size_t>(mv[j].x) * D) = row[j];
+      if (in == 0) weight[base + mv[j].x] = w[j];
+      if (in == 1) pos[base + mv[j].x] = ps[j];
+    }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && bh % p.Hkv == 0) {
     const int b = bh / p.Hkv;
@@ -631,9 +706,16 @@ extern "C" svoo_status svoo_cache_evict(int B, int Hkv, int cap, int d, int keep
   int32_t* n_moves = static_cast<int32_t*>(workspace);
   int2* moves = reinterpret_cast<int2*>(static_cast<char*>(workspace) + (static_cast<size_t>(rows) * 4 + 255) / 256 * 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<rows, kEvictThreads, 0, st>>>(p, weight, pos, lengths, m_cap, moves, n_moves);
-  int chunks = (m_cap + 63) / 64;
-  if (chunks > 64) chunks = 64;
+  if (cap <= 4 * kEvictThreads)
+    evict_select_kernel<4><<<rows, kEvictThreads, 0, st>>>(p, weight, pos, lengths, m_cap, moves, n_moves);
+  else if (cap <= 16 * kEvictThreads)
+    evict_select_kernel<16><<<rows, kEvictThreads, 0, st>>>(p, weight, pos, lengths, m_cap, moves, n_moves);
+  else
+    evict_select_kernel<0><<<rows, kEvictThreads, 0, st>>>(p, weight, pos, lengths, m_cap, moves, n_moves);
+  // 32 moves (64 at d = 64) a CTA and turn; the moves are not known here, their bound is
+  const int turn = 4 * 256 / (2 * (d / 8));
+  int chunks = (m_cap + turn - 1) / turn;
+  if (chunks > 32) chunks = 32;
   if (d == 128)
     evict_move_kernel<128><<<dim3(chunks, rows), 256, 0, st>>>(p, m_cap, moves, n_moves, static_cast<uint16_t*>(k),
                                                                static_cast<uint16_t*>(v), weight, pos, lengths);
