@@ -455,26 +455,23 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int sink, int ne
   return (u & 0x7fffffffu) > 0x7f800000u ? 0u : min(k, 0xfffffffeu);
 }
 
-__device__ __forceinline__ int evict_exclusive(int x, int* warp_sums, int* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = x;
+// Sums before each warp of a round, in place: n counts (one per warp and round,
+// in slot order) by the first warp. Returns nothing until the caller's barrier.
+__device__ __forceinline__ void evict_scan(int* counts, int n) {
+  const int lane = threadIdx.x;  // of the first warp
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int x = i0 + lane < n ? counts[i0 + lane] : 0;
+    int inc = x;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (i0 + lane < n) counts[i0 + lane] = base + inc - x;
+    base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kEvictThreads / 32; ++w) {
-    const int y = warp_sums[w];
-    if (w < warp) before += y;
-    sum += y;
-  }
-  *all = sum;
-  __syncthreads();
-  return inc - x + before;
+  if (lane == 0) counts[n] = base;
 }
 
 // One CTA per (sequence, key head). Finds the keep-th largest key by radix
@@ -487,7 +484,9 @@ __global__ void __launch_bounds__(kEvictThreads)
     evict_select_kernel(EvictDims p, const float* __restrict__ weight, const int32_t* __restrict__ pos,
                         const int32_t* __restrict__ lengths, int m_cap, int2* __restrict__ moves,
                         int32_t* __restrict__ n_moves) {
-  __shared__ int hist[256], sums[32];
+  constexpr int kCounts = (R ? R : 1) * (kEvictThreads / 32);
+  __shared__ int hist[4][256];  // four, since weights share their leading bits
+  __shared__ int counts[2][kCounts + 1];
   __shared__ int newest_s, digit_s, left_s;
   const int bh = blockIdx.x, b = bh / p.Hkv, tid = threadIdx.x;
   const int len = max(0, min(p.cap, lengths[b]));
@@ -498,7 +497,9 @@ __global__ void __launch_bounds__(kEvictThreads)
   const float* w = weight + static_cast<size_t>(bh) * p.cap;
   const int32_t* ps = pos + static_cast<size_t>(bh) * p.cap;
   if (tid == 0) newest_s = -1;
-  if (tid < 256) hist[tid] = 0;
+  hist[tid >> 8][tid & 255] = 0;
+  static_assert(kEvictThreads == 4 * 256, "one thread per counter");
+  const int warp = tid >> 5, lane = tid & 31;
   uint32_t held[R ? R : 1];
   int place[R ? R : 1];
   int newest = -1;
@@ -523,27 +524,24 @@ __global__ void __launch_bounds__(kEvictThreads)
     for (int r = 0; r < R; ++r) held[r] = evict_key(__uint_as_float(held[r]), place[r], p.sink, newest, p.recent);
   }
   const int rounds = (len + kEvictThreads - 1) / kEvictThreads;
-  // f(slot, key) for every slot, a round of threads at a time
+  // f(round, slot, key) for every slot, a round of threads at a time
   auto each = [&](auto f) {
     if (R) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (r < rounds) f(r * kEvictThreads + tid, held[r]);
+        if (r < rounds) f(r, r * kEvictThreads + tid, held[r]);
     } else {
       for (int r = 0; r < rounds; ++r) {
         const int i = r * kEvictThreads + tid;
-        f(i, i < len ? evict_key(w[i], ps[i], p.sink, newest, p.recent) : 0u);
+        f(r, i, i < len ? evict_key(w[i], ps[i], p.sink, newest, p.recent) : 0u);
       }
     }
   };
   uint32_t prefix = 0, mask = 0;
   int want = p.keep;  // the want-th largest of those that match the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    each([&](int i, uint32_t k) {
-      // weights share their leading bits: one addition per digit and warp
-      const bool in = i < len && (k & mask) == prefix;
-      const unsigned same = __match_any_sync(0xffffffffu, in ? (k >> shift) & 255u : 256u);
-      if (in && (same & ((1u << (tid & 31)) - 1u)) == 0) atomicAdd(&hist[(k >> shift) & 255], __popc(same));
+    each([&](int r, int i, uint32_t k) {
+      if (i < len && (k & mask) == prefix) atomicAdd(&hist[warp & 3][(k >> shift) & 255], 1);
     });
     __syncthreads();
     if (tid < 32) {
@@ -551,8 +549,12 @@ __global__ void __launch_bounds__(kEvictThreads)
       int c[8], s = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - tid * 8 - i];
-        hist[255 - tid * 8 - i] = 0;
+        c[i] = 0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          c[i] += hist[h][255 - tid * 8 - i];
+          hist[h][255 - tid * 8 - i] = 0;
+        }
         s += c[i];
       }
       int inc = s;
@@ -578,23 +580,92 @@ __global__ void __launch_bounds__(kEvictThreads)
     mask |= 255u << shift;
     want = left_s;
   }
-  // kept: keys above `prefix`, and the first `want` equal to it
-  int equal = 0, holes = 0, srcs = 0;
-  each([&](int i, uint32_t k) {
-    int all;
-    const int before = equal + evict_exclusive(i < len && k == prefix, sums, &all);
-    equal += all;
-    const bool keep = i < len && (k > prefix || (k == prefix && before < want));
-    const bool hole = i < len && i < p.keep && !keep, src = keep && i >= p.keep;
-    // both lists have at most m_cap entries; one scan carries the two counts
-    int both;
-    const int at = evict_exclusive((hole ? 1 : 0) | (src ? 1 << 16 : 0), sums, &both);
-    if (hole) moves[static_cast<size_t>(bh) * m_cap + holes + (at & 0xffff)].x = i;
-    if (src) moves[static_cast<size_t>(bh) * m_cap + srcs + (at >> 16)].y = i;
-    holes += both & 0xffff;
-    srcs += both >> 16;
-  });
-  if (tid == 0) n_moves[bh] = srcs;
+  // Kept: keys above `prefix`, and the first `want` equal to it. A slot's place
+  // among its like: ballots within a warp, sums over the warps before it. Both
+  // lists of moves have at most m_cap entries.
+  const unsigned below = (1u << lane) - 1u;
+  constexpr int kWarps = kEvictThreads / 32;
+  int2* out = moves + static_cast<size_t>(bh) * m_cap;
+  auto kept = [&](int i, uint32_t k, int equal_before, unsigned eq) {
+    return i < len && (k > prefix || (k == prefix && equal_before + __popc(eq & below) < want));
+  };
+  if (R) {
+    each([&](int r, int i, uint32_t k) {
+      const unsigned eq = __ballot_sync(0xffffffffu, i < len && k == prefix);
+      if (lane == 0) counts[0][r * kWarps + warp] = __popc(eq);
+    });
+    __syncthreads();
+    if (warp == 0) evict_scan(counts[0], rounds * kWarps);
+    __syncthreads();
+    unsigned keeps[R ? R : 1];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * kEvictThreads + tid;
+      const unsigned eq = __ballot_sync(0xffffffffu, r < rounds && i < len && held[r] == prefix);
+      keeps[r] = __ballot_sync(0xffffffffu, r < rounds && kept(i, held[r], r < rounds ? counts[0][r * kWarps + warp] : 0, eq));
+    }
+    __syncthreads();
+    // holes lie below `keep`, sources from there on: one count per warp for both
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * kEvictThreads + tid;
+      const bool keep = (keeps[r] >> lane) & 1u;
+      const unsigned hole = __ballot_sync(0xffffffffu, i < p.keep && i < len && !keep);
+      const unsigned src = __ballot_sync(0xffffffffu, i >= p.keep && keep);
+      if (lane == 0 && r < rounds) {
+        counts[0][r * kWarps + warp] = __popc(hole);
+        counts[1][r * kWarps + warp] = __popc(src);
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      evict_scan(counts[0], rounds * kWarps);
+      evict_scan(counts[1], rounds * kWarps);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * kEvictThreads + tid;
+      const bool keep = (keeps[r] >> lane) & 1u;
+      const unsigned hole = __ballot_sync(0xffffffffu, i < p.keep && i < len && !keep);
+      const unsigned src = __ballot_sync(0xffffffffu, i >= p.keep && keep);
+      if (r < rounds) {
+        if ((hole >> lane) & 1u) out[counts[0][r * kWarps + warp] + __popc(hole & below)].x = i;
+        if ((src >> lane) & 1u) out[counts[1][r * kWarps + warp] + __popc(src & below)].y = i;
+      }
+    }
+    if (tid == 0) n_moves[bh] = counts[1][rounds * kWarps];
+  } else {
+    int equal = 0, holes = 0, srcs = 0;
+    each([&](int r, int i, uint32_t k) {
+      const unsigned eq = __ballot_sync(0xffffffffu, i < len && k == prefix);
+      if (lane == 0) counts[0][warp] = __popc(eq);
+      __syncthreads();
+      if (warp == 0) evict_scan(counts[0], kWarps);
+      __syncthreads();
+      const bool keep = kept(i, k, equal + counts[0][warp], eq);
+      equal += counts[0][kWarps];
+      __syncthreads();
+      const unsigned hole = __ballot_sync(0xffffffffu, i < p.keep && i < len && !keep);
+      const unsigned src = __ballot_sync(0xffffffffu, i >= p.keep && keep);
+      if (lane == 0) {
+        counts[0][warp] = __popc(hole);
+        counts[1][warp] = __popc(src);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        evict_scan(counts[0], kWarps);
+        evict_scan(counts[1], kWarps);
+      }
+      __syncthreads();
+      if ((hole >> lane) & 1u) out[holes + counts[0][warp] + __popc(hole & below)].x = i;
+      if ((src >> lane) & 1u) out[srcs + counts[1][warp] + __popc(src & below)].y = i;
+      holes += counts[0][kWarps];
+      srcs += counts[1][kWarps];
+      __syncthreads();
+    });
+    if (tid == 0) n_moves[bh] = srcs;
+  }
 }
 
 // Grid (chunks, B * Hkv): the lanes of a move carry both its rows, 16 bytes

@@ -89,6 +89,9 @@ EVICTIONS = [
     (2, 1, 2100, 64, 2000, 4, 1996, [2100, 2050], "random"),
     (1, 4, 500, 64, 250, 1, 9, [500], "zeros"),
     (1, 1, 300, 64, 77, 2, 3, [300], "nan"),
+    (1, 2, 5000, 64, 2500, 4, 100, [4999], "random"),
+    (2, 1, 17000, 64, 16000, 4, 100, [17000, 16500], "random"),
+    (1, 1, 17000, 64, 3000, 0, 10, [16999], "ties"),
 ]
 
 
