@@ -570,12 +570,17 @@ def _ws_bytes(what: str, *args) -> int:
     return fn(_bshape(*args[:13]), *args[13:])
 
 
-def _workspace(workspace, device, what: str, *args) -> torch.Tensor:
+def _workspace(workspace, device, what: str, *args):
+    """(tensor to keep alive, address, bytes) of a call's workspace."""
     if workspace is None:
-        return torch.empty(_ws_bytes(what, *args), dtype=torch.uint8, device=device)
+        n = _ws_bytes(what, *args)
+        if n == 0:
+            return None, None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), n
     if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise SvooError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _block_scale(cfg: Optional[BlockConfig], d: int) -> float:
@@ -623,9 +628,9 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
         _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
     args = (B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
             n_keys - Nq if q_start is None else q_start)
-    ws = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
+    ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
     _call("svoo_block_select", q, stream, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
-          idx.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _dp(dev_err))
+          idx.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return idx
 
 
@@ -655,13 +660,13 @@ def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=
     _need("o", torch.bfloat16, dev, q.shape, o)
     _need("grad_o", torch.bfloat16, dev, q.shape, grad_o)
     _need("lse", torch.float32, dev, (B, H, Nq), lse)
-    ws = _workspace(workspace, dev, "svoo_block_attn_backward_workspace_size", *args)
+    ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_backward_workspace_size", *args)
     dq = torch.empty_like(q)
     dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
     dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
     _call("svoo_block_attn_backward", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), _block_scale(cfg, d),
-          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _dp(dev_err))
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return dq, dk, dv
 
 
@@ -726,12 +731,12 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
             raise SvooError("weights need k and v as whole buffers")
         _need("weight", torch.float32, dev, (B, Hkv, Nk), weight)
     _need("out", torch.bfloat16, dev, q.shape, out)
-    ws = _workspace(workspace, dev, "svoo_cache_attn_workspace_size", *args, idx is not None, weight is not None)
+    ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_attn_workspace_size", *args, idx is not None, weight is not None)
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(B, H, 1, dtype=torch.float32, device=dev)
     _call("svoo_cache_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
-          _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-          ws.numel() * ws.element_size(), _dp(dev_err))
+          _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws_at, ws_n,
+          _dp(dev_err))
     return out, lse
 
 
@@ -752,6 +757,6 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
     for what, t, dtype in (("weight", weight, torch.float32), ("pos", pos, torch.int32)):
         _need(what, dtype, dev, (B, Hkv, cap), t)
     _need("lengths", torch.int32, dev, (B,), lengths)
-    ws = _workspace(workspace, dev, "svoo_cache_evict_workspace_size", B, Hkv, cap, keep)
+    ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_evict_workspace_size", B, Hkv, cap, keep)
     _call("svoo_cache_evict", k, stream, B, Hkv, cap, d, keep, sink, recent, k.data_ptr(), v.data_ptr(),
-          weight.data_ptr(), pos.data_ptr(), lengths.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          weight.data_ptr(), pos.data_ptr(), lengths.data_ptr(), ws_at, ws_n)

@@ -813,12 +813,14 @@ static_assert(dkv_tile_bytes<128>() + sizeof(DkvSmem) <= kMaxSmem, "dk, dv: shar
 
 // ------------------------------------------------------------------ host side
 
-// Rows of one piece: an eighth of an SM's share of all rows, so that a block
-// which every query keeps does not leave one SM with the last word, and at
-// least 32 tiles, below which a piece's own start and its part's bytes show.
+// Rows of one piece: a quarter of an SM's share of all rows, so that a block
+// which every query keeps does not leave one SM with the last word, and at least
+// 32 tiles, below which a piece's own start and its part's bytes show. (An eighth
+// cut most of the lists of ordinary length too: the parts' sum alone took 78 us
+// of 2000 at 16384 tokens.)
 inline int piece_rows(const BlockDims& p) {
   const long long rows = static_cast<long long>(p.B) * p.Hkv * p.Nq * p.n_sel * p.nsub * p.G;
-  long long piece = rows / (148 * 8);
+  long long piece = rows / (148 * 4);
   piece = (piece + kRowTile - 1) / kRowTile * kRowTile;
   if (piece < 32 * kRowTile) piece = 32 * kRowTile;
   return static_cast<int>(piece < (1 << 28) ? piece : (1 << 28));
@@ -838,7 +840,8 @@ GradPlan grad_plan(const BlockDims& p, int d, void* ws) {
   const long long BHk = static_cast<long long>(p.B) * p.Hkv;
   const long long rows = BHk * p.Nq * p.n_sel * p.nsub * p.G;  // over all key tiles, at most
   g.ktiles = (p.Nk + kKeyTile - 1) / kKeyTile;
-  g.chunk = p.nb > 256 ? (p.nb + 31) / 32 * 32 : 256;  // the counts stay below one per key
+  // one warp a chunk: many of them, while the counts stay below four per query
+  g.chunk = p.nb > 256 ? (p.nb / 4 + 31) / 32 * 32 : 64;
   g.nchunk = (p.Nq + g.chunk - 1) / g.chunk;
   g.piece = piece_rows(p);
   g.max_items = BHk * g.ktiles + rows / g.piece;

@@ -1082,18 +1082,18 @@ extern "C" svoo_status svoo_block_pool(const svoo_block_shape* shape, const void
 
 extern "C" size_t svoo_block_select_workspace_size(const svoo_block_shape* shape) {
   if (!block_shape_ok(shape)) return 0;
-  const size_t n = select_plan(block_dims(shape), shape->d, nullptr).bytes;
-  return n ? n : 256;
+  return select_plan(block_dims(shape), shape->d, nullptr).bytes;
 }
 
 extern "C" svoo_status svoo_block_select(const svoo_block_shape* shape, const void* q, const float* pool,
                                          const int32_t* lengths, int32_t* idx, void* workspace, size_t workspace_bytes,
                                          int32_t* dev_err, void* stream) {
-  if (!block_shape_ok(shape) || !q || !pool || !idx || !workspace) return SVOO_ERR_INVALID_ARG;
+  if (!block_shape_ok(shape) || !q || !pool || !idx) return SVOO_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
-  if (workspace_bytes < select_plan(p, shape->d, nullptr).bytes) return SVOO_ERR_WORKSPACE;
+  const size_t need = select_plan(p, shape->d, nullptr).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SVOO_ERR_WORKSPACE;
   if (shape->Nq == 0) return SVOO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (mma_select(p)) {

@@ -732,23 +732,22 @@ using namespace svoo;
 
 extern "C" size_t svoo_cache_attn_workspace_size(const svoo_block_shape* shape, int selected, int weights) {
   if (!block_shape_ok(shape) || shape->Nq != 1) return 0;
-  const size_t n = cache_plan(block_dims(shape), shape->d, selected != 0, weights != 0, nullptr).bytes;
-  return n ? n : 256;
+  return cache_plan(block_dims(shape), shape->d, selected != 0, weights != 0, nullptr).bytes;
 }
 
 extern "C" svoo_status svoo_cache_attn(const svoo_block_shape* shape, const void* q, const void* k, const void* v,
                                        const int32_t* lengths, const int32_t* idx, float scale, float* weight, void* o,
                                        float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_err,
                                        void* stream) {
-  if (!block_shape_ok(shape) || shape->Nq != 1 || !q || !k || !v || !o || !lse || !workspace || !scale_ok(scale))
+  if (!block_shape_ok(shape) || shape->Nq != 1 || !q || !k || !v || !o || !lse || !scale_ok(scale))
     return SVOO_ERR_INVALID_ARG;
   if (idx && weight) return SVOO_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(lengths, 4) || !aligned(idx, 4) || !aligned(weight, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
-  if (workspace_bytes < cache_plan(p, shape->d, idx != nullptr, weight != nullptr, nullptr).bytes)
-    return SVOO_ERR_WORKSPACE;
+  const size_t need = cache_plan(p, shape->d, idx != nullptr, weight != nullptr, nullptr).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SVOO_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (shape->d == 128)
     return launch_cache_attn<128>(p, q, k, v, lengths, idx, scale, weight, o, lse, workspace, dev_err, st);

@@ -337,8 +337,9 @@ svoo_status svoo_block_pool(const svoo_block_shape *shape, const void *k, const 
  *   score(t, c) = (sum over the group's heads of q[t]) . pool[c],
  * equal scores to the lower block; decided as in fp64. Causal: the blocks up to
  * the query's own, which is always kept and never scored. A query outside its
- * sequence selects nothing. The workspace (256-byte aligned) must not be shared
- * by calls that overlap on the GPU. */
+ * sequence selects nothing. The workspace (256-byte aligned; a call of few
+ * queries needs none, 0 bytes) must not be shared by calls that overlap on the
+ * GPU. */
 size_t svoo_block_select_workspace_size(const svoo_block_shape *shape);
 svoo_status svoo_block_select(const svoo_block_shape *shape, const void *q, const float *pool,
                               const int32_t *lengths, int32_t *idx, void *workspace,
@@ -376,7 +377,8 @@ svoo_status svoo_block_attn_backward(const svoo_block_shape *shape, const void *
  *  group's heads of the slot's softmax weight, for every valid slot. idx and
  *  weight together are SVOO_ERR_UNSUPPORTED.
  * Workspace: svoo_cache_attn_workspace_size(shape, idx != NULL, weight != NULL)
- * bytes, 256-byte aligned, not shared by calls that overlap on the GPU. */
+ * bytes (may be 0), 256-byte aligned, not shared by calls that overlap on the
+ * GPU. */
 size_t svoo_cache_attn_workspace_size(const svoo_block_shape *shape, int selected, int weights);
 svoo_status svoo_cache_attn(const svoo_block_shape *shape, const void *q, const void *k,
                             const void *v, const int32_t *lengths, const int32_t *idx, float scale,
