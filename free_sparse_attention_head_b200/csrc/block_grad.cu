@@ -7,9 +7,8 @@
 // P is computed again from lse in both kernels rather than kept: two products
 // of 64 keys cost less than its bytes.
 //
-//   row_delta_kernel     delta, one warp per row
-//   block_dq_kernel      dq: row tiles against the union of their blocks, as the
-//                        forward kernel walks it
+//   block_dq_kernel      delta, and dq: row tiles against the union of their
+//                        blocks, as the forward kernel walks it
 //   sel_hist / sel_scan / sel_items / sel_fill
 //                        for every block the list of the queries that selected
 //                        it, in a fixed order (no atomics decide a place)
@@ -24,31 +23,6 @@
 namespace svoo {
 
 namespace {
-
-// ------------------------------------------------------------------ delta
-
-// one warp per row of [rows, D]; D / 32 elements per lane
-template <int D>
-__global__ void __launch_bounds__(256)
-    row_delta_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ go, size_t rows,
-                     float* __restrict__ delta) {
-  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  constexpr int kE = D / 32;
-  float a = 0.f;
-  const uint32_t* po = reinterpret_cast<const uint32_t*>(o + row * D + lane * kE);
-  const uint32_t* pg = reinterpret_cast<const uint32_t*>(go + row * D + lane * kE);
-#pragma unroll
-  for (int i = 0; i < kE / 2; ++i) {
-    const uint32_t x = po[i], y = pg[i];
-    a = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), a);
-    a = fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), a);
-  }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) a += __shfl_xor_sync(0xffffffffu, a, s);
-  if (lane == 0) delta[row] = a;
-}
 
 // ------------------------------------------------------------------ dq
 
@@ -80,8 +54,8 @@ template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
     block_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
                     int cap, int v_stages, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
-                    const uint16_t* __restrict__ v, const uint16_t* __restrict__ go, const float* __restrict__ lse,
-                    const float* __restrict__ delta, const int32_t* __restrict__ idx,
+                    const uint16_t* __restrict__ v, const uint16_t* __restrict__ go, const uint16_t* __restrict__ o,
+                    const float* __restrict__ lse, float* __restrict__ delta, const int32_t* __restrict__ idx,
                     const int32_t* __restrict__ lengths, float scale, float scale_log2, uint16_t* __restrict__ dq,
                     int* __restrict__ err) {
   constexpr int kSub = D / 64;
@@ -219,7 +193,26 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const bool live = ti < nt;
     const int lim = live ? S->limit[ti] : 0;
     const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
-    const float lse2 = lse[row] * 1.4426950408889634f, dl = delta[row];
+    const float lse2 = lse[row] * 1.4426950408889634f;
+    // delta, from dO as it lies in shared memory, under the first products
+    float dl = 0.f;
+    {
+      const uint4* po = reinterpret_cast<const uint4*>(o + row * D);
+      uint4 x[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) x[c] = po[c];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 y = *reinterpret_cast<const uint4*>(g_s + sw128_offset(r, c * 8, kRowTile));
+        const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dl = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), dl);
+          dl = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), dl);
+        }
+      }
+      if (live && h == 0) delta[row] = dl;
+    }
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t* my_word = tl.mask + (live ? ti >> 5 : 0);
     auto visible = [&](int j) {  // keys of this thread's tile in step j that the row sees
@@ -378,20 +371,32 @@ __global__ void __launch_bounds__(32)
     for (int i = lane; i < p.nb; i += 32) h[i] = cnt[i];
 }
 
-// per block: running sums of the chunks' counts (in place) and the total
+// per block: running sums of the chunks' counts (in place) and the total; a CTA
+// takes 32 blocks, its eight warps an eighth of the chunks each
 __global__ void __launch_bounds__(256)
     sel_scan_kernel(BlockDims p, int nchunk, int32_t* __restrict__ hist, int32_t* __restrict__ total) {
-  const int blk = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y;
-  if (blk >= p.nb) return;
-  int32_t* h = hist + static_cast<size_t>(bh) * nchunk * p.nb + blk;
+  __shared__ int part[8][32];
+  const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5, blk = blockIdx.x * 32 + lane, bh = blockIdx.y;
+  const int per = (nchunk + 7) / 8, c0 = min(nchunk, seg * per), c1 = min(nchunk, c0 + per);
+  const bool there = blk < p.nb;
+  int32_t* h = hist + static_cast<size_t>(bh) * nchunk * p.nb + (there ? blk : 0);
   int a = 0;
+  if (there) {
 #pragma unroll 8
-  for (int c = 0; c < nchunk; ++c) {
+    for (int c = c0; c < c1; ++c) a += h[static_cast<size_t>(c) * p.nb];
+  }
+  part[seg][lane] = a;
+  __syncthreads();
+  a = 0;
+  for (int s = 0; s < seg; ++s) a += part[s][lane];
+  if (!there) return;
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c) {
     const int x = h[static_cast<size_t>(c) * p.nb];
     h[static_cast<size_t>(c) * p.nb] = a;
     a += x;
   }
-  total[static_cast<size_t>(bh) * p.nb + blk] = a;
+  if (seg == 7) total[static_cast<size_t>(bh) * p.nb + blk] = a;
 }
 
 // Exclusive sums over a block of 1024 threads, each with its own value.
@@ -784,7 +789,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   }
 }
 
-// adds the parts of the key tiles whose list was cut, in order
+// adds the parts of the key tiles whose list was cut, in order; grid.y eighths of
+// a tile's dv and dk
 template <int D>
 __global__ void __launch_bounds__(256)
     block_dkv_sum_kernel(BlockDims p, int ktiles, const int4* __restrict__ items, const int32_t* __restrict__ counts,
@@ -795,17 +801,21 @@ __global__ void __launch_bounds__(256)
   const int bh = item.x / ktiles, key0 = (item.x - bh * ktiles) * kKeyTile;
   const int nkeys = min(kKeyTile, p.Nk - key0);
   const float* src = parts + static_cast<size_t>(item.w) * 2 * kKeyTile * D;
-  for (int i = threadIdx.x * 2; i < 2 * kKeyTile * D; i += 512) {
-    float a = 0.f, b = 0.f;
+  constexpr int kAll = 2 * kKeyTile * D;
+  for (int i = (blockIdx.y * 256 + threadIdx.x) * 4; i < kAll; i += 8 * 256 * 4) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int c = 0; c < item.z; ++c) {
-      const float2 x = *reinterpret_cast<const float2*>(src + static_cast<size_t>(c) * 2 * kKeyTile * D + i);
-      a += x.x;
-      b += x.y;
+      const float4 x = *reinterpret_cast<const float4*>(src + static_cast<size_t>(c) * kAll + i);
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
     }
     const int which = i / (kKeyTile * D), rest = i - which * kKeyTile * D, key = rest / D;
     if (key < nkeys)
-      *reinterpret_cast<uint32_t*>((which ? dk : dv) + (static_cast<size_t>(bh) * p.Nk + key0) * D + rest) =
-          pack_bf16x2(a, b);
+      *reinterpret_cast<uint2*>((which ? dk : dv) + (static_cast<size_t>(bh) * p.Nk + key0) * D + rest) =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
 }
 
@@ -866,7 +876,6 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
                               cudaStream_t st) {
   const GradPlan g = grad_plan(p, D, ws);
   const int BHk = p.B * p.Hkv;
-  const size_t rows = static_cast<size_t>(p.B) * p.H * p.Nq;
   const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
                  *vp = static_cast<const uint16_t*>(v), *gp = static_cast<const uint16_t*>(go);
   CUtensorMap km, vm;
@@ -891,24 +900,23 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (p.Nq > 0) {
-    row_delta_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(static_cast<const uint16_t*>(o), gp,
-                                                                               rows, g.delta);
     sel_walk_kernel<false><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                       nullptr, nullptr);
   }
-  sel_scan_kernel<<<dim3((p.nb + 255) / 256, BHk), 256, 0, st>>>(p, g.nchunk, g.hist, g.total);
+  sel_scan_kernel<<<dim3((p.nb + 31) / 32, BHk), 256, 0, st>>>(p, g.nchunk, g.hist, g.total);
   sel_items_kernel<<<1, 1024, 0, st>>>(p, g.ktiles, g.piece, g.total, g.start, g.items, g.counts);
   if (p.Nq > 0) {
     sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        km, vm, p, static_cast<int>(union_cap(p)), v_stages, qp, kp, vp, gp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+        km, vm, p, static_cast<int>(union_cap(p)), v_stages, qp, kp, vp, gp, static_cast<const uint16_t*>(o), lse, g.delta, idx,
+        lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
       p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,
       scale_log2, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv), g.parts, dev_err);
   if (g.max_slots > 0)
-    block_dkv_sum_kernel<D><<<static_cast<unsigned>(g.max_items), 256, 0, st>>>(
+    block_dkv_sum_kernel<D><<<dim3(static_cast<unsigned>(g.max_items), 8), 256, 0, st>>>(
         p, g.ktiles, g.items, g.counts, g.parts, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv));
   return launch_status();
 }
