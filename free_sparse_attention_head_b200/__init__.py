@@ -85,7 +85,8 @@ _SIGS = {
     "svoo_block_pool": (_I, [_BP, _P, _P, _I, _P, _P]),
     "svoo_block_select_workspace_size": (_SZ, [_BP]),
     "svoo_block_select": (_I, [_BP, _P, _P, _P, _P, _P, _SZ, _P, _P]),
-    "svoo_block_attn": (_I, [_BP, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P]),
+    "svoo_block_attn_workspace_size": (_SZ, [_BP]),
+    "svoo_block_attn": (_I, [_BP, _P, _P, _P, _P, _P, _F, _P, _P, _P, _SZ, _P, _P]),
     "svoo_block_attn_backward_workspace_size": (_SZ, [_BP]),
     "svoo_block_attn_backward": (_I, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _SZ, _P, _P]),
     "svoo_cache_attn_workspace_size": (_SZ, [_BP, _I, _I]),
@@ -635,7 +636,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
 
 
 def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[int] = None, out=None,
-               dev_err=None, stream=None):
+               workspace=None, dev_err=None, stream=None):
     """Attention of every query over the blocks in idx; returns (o, lse). No gradient is recorded
     (block_attention records one)."""
     args = _block_args(q, k, v, cfg, lengths, q_start)
@@ -645,8 +646,9 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
     _need("out", torch.bfloat16, dev, q.shape, out)
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(B, H, Nq, dtype=torch.float32, device=dev)
+    ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
     _call("svoo_block_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-          _dp(lengths), _block_scale(cfg, d), out.data_ptr(), lse.data_ptr(), _dp(dev_err))
+          _dp(lengths), _block_scale(cfg, d), out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return out, lse
 
 

@@ -12,6 +12,9 @@
 // rows that compute for nothing: neighbouring queries mostly agree, and in the
 // worst case the union is what dense attention would read.
 //
+// Where there are few row tiles, a tile's list is shared out to several CTAs
+// (grid.z), whose parts block_join_kernel puts together.
+//
 // Two CTAs share an SM (256 tensor-memory columns and half of the shared
 // memory each), so one's softmax runs beside the other's products.
 // Warps: 0-3 softmax (thread r = row r = TMEM lane r), 4 key/value producer
@@ -26,6 +29,7 @@ namespace svoo {
 namespace {
 
 constexpr int kFwdThreads = 192;
+constexpr int kMaxShares = 16;  // CTAs that share a row tile's list
 // The running maximum stays until it is outgrown by 2^32: P (bf16, fp32's range)
 // and its sums lose nothing by being large, at most 2^52 here, and the rescaling
 // that a smaller bound (2^8) asked for stalled most steps on the last product.
@@ -52,7 +56,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                       BlockDims p, int cap, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
                       const uint16_t* __restrict__ v, const int32_t* __restrict__ idx,
                       const int32_t* __restrict__ lengths, float scale_log2, uint16_t* __restrict__ o,
-                      float* __restrict__ lse, int* __restrict__ err) {
+                      float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
+                      int* __restrict__ err) {
   constexpr int kSub = D / 64;
   constexpr int kKvBytes = kKeyTile * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint8_t* k_s = q_s + kRowTile * D * 2;  // 2 stages
   uint8_t* v_s = k_s + 2 * kKvBytes;      // 2 stages
   FwdSmem* S = reinterpret_cast<FwdSmem*>(v_s + 2 * kKvBytes);
-  const TileList tl = tile_list(p, cap, S + 1);
+  TileList tl = tile_list(p, cap, S + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
@@ -90,7 +95,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
-  const int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
+  int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
+  if (gridDim.z > 1) {  // this CTA's share of the list
+    const int per = (tiles + gridDim.z - 1) / gridDim.z, first = min(tiles, static_cast<int>(blockIdx.z) * per);
+    tl.list += first;
+    tiles = min(per, tiles - first);
+  }
   cp_async_wait_all();
   fence_proxy_async_smem();
   tc_fence_before();
@@ -291,6 +301,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tc_fence_after();
       const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti;
       const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool part = gridDim.z > 1;
+      const size_t at = blockIdx.z * (static_cast<size_t>(p.B) * p.H * p.Nq) + row;  // of a part
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t x[32];
@@ -298,21 +310,30 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_ld32(lane_base + 128 + c0 * 32, x);
           tmem_wait_ld_regs(x);
         }
-        if (live) {
+        if (!live) continue;
+        if (part) {
+          if (l > 0.f) {
 #pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) {
-            uint4 pk = make_uint4(0, 0, 0, 0);
-            if (l > 0.f) {
-              pk.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * inv, __uint_as_float(x[c8 * 8 + 1]) * inv);
-              pk.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * inv, __uint_as_float(x[c8 * 8 + 3]) * inv);
-              pk.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * inv, __uint_as_float(x[c8 * 8 + 5]) * inv);
-              pk.w = pack_bf16x2(__uint_as_float(x[c8 * 8 + 6]) * inv, __uint_as_float(x[c8 * 8 + 7]) * inv);
-            }
-            reinterpret_cast<uint4*>(o + row * D + c0 * 32)[c8] = pk;
+            for (int c4 = 0; c4 < 8; ++c4)
+              *reinterpret_cast<uint4*>(part_o + at * D + c0 * 32 + c4 * 4) =
+                  make_uint4(x[c4 * 4], x[c4 * 4 + 1], x[c4 * 4 + 2], x[c4 * 4 + 3]);
           }
+          continue;
+        }
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) {
+          uint4 pk = make_uint4(0, 0, 0, 0);
+          if (l > 0.f) {
+            pk.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * inv, __uint_as_float(x[c8 * 8 + 1]) * inv);
+            pk.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * inv, __uint_as_float(x[c8 * 8 + 3]) * inv);
+            pk.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * inv, __uint_as_float(x[c8 * 8 + 5]) * inv);
+            pk.w = pack_bf16x2(__uint_as_float(x[c8 * 8 + 6]) * inv, __uint_as_float(x[c8 * 8 + 7]) * inv);
+          }
+          reinterpret_cast<uint4*>(o + row * D + c0 * 32)[c8] = pk;
         }
       }
-      if (live) lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (live && part) part_ml[at] = make_float2(m, l);
+      if (live && !part) lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
   tc_fence_before();
@@ -333,10 +354,80 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   }
 }
 
+// One warp per row of [B*H*Nq, D]: o = sum of the shares' parts, each at its own
+// maximum. A share that the row had nothing in (l = 0) wrote no part.
+template <int D>
+__global__ void __launch_bounds__(256)
+    block_join_kernel(size_t rows, int shares, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                      uint16_t* __restrict__ o, float* __restrict__ lse) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  constexpr int kE = D / 32;
+  float2 ml[kMaxShares];
+  float top = -INFINITY, l = 0.f, acc[kE];
+#pragma unroll
+  for (int z = 0; z < kMaxShares; ++z) {
+    ml[z] = z < shares ? part_ml[z * rows + row] : make_float2(-INFINITY, 0.f);
+    if (ml[z].y > 0.f) top = fmaxf(top, ml[z].x);
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int z = 0; z < kMaxShares; ++z) {
+    if (!(ml[z].y > 0.f)) continue;
+    const float f = ex2_approx(ml[z].x - top);
+    l = fmaf(ml[z].y, f, l);
+    const float2* src = reinterpret_cast<const float2*>(part_o + (z * rows + row) * D + lane * kE);
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) {
+      const float2 x = src[e];
+      acc[2 * e] = fmaf(x.x, f, acc[2 * e]);
+      acc[2 * e + 1] = fmaf(x.y, f, acc[2 * e + 1]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kE);
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Shares of a row tile's list: as many as bring two CTAs to every SM, while a
+// share may have four key tiles or more (the lists' lengths are not known here,
+// their bound is).
+inline int block_shares(const BlockDims& p) {
+  const long long ctas = static_cast<long long>((p.Nq + p.tpt - 1) / p.tpt) * p.B * p.Hkv;
+  if (ctas == 0) return 1;
+  const long long longest = static_cast<long long>(union_cap(p)) * p.nsub;
+  long long z = 2 * 148 / ctas;
+  if (z > longest / 4) z = longest / 4;
+  if (z > kMaxShares) z = kMaxShares;
+  return z < 1 ? 1 : static_cast<int>(z);
+}
+
+struct FwdPlan {
+  int shares;
+  float* part_o;
+  float2* part_ml;
+  size_t bytes;
+};
+FwdPlan fwd_plan(const BlockDims& p, int d, void* ws) {
+  FwdPlan f;
+  f.shares = block_shares(p);
+  const size_t rows = f.shares > 1 ? static_cast<size_t>(f.shares) * p.B * p.H * p.Nq : 0;
+  Carver c(ws);
+  f.part_o = c.take<float>(rows * d);
+  f.part_ml = c.take<float2>(rows);
+  f.bytes = (c.used + 255) / 256 * 256;
+  return f;
+}
+
 template <int D>
 svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, const void* v, const int32_t* idx,
-                              const int32_t* lengths, float scale, void* o, float* lse, int32_t* dev_err,
+                              const int32_t* lengths, float scale, void* o, float* lse, void* ws, int32_t* dev_err,
                               cudaStream_t st) {
+  const FwdPlan f = fwd_plan(p, D, ws);
   CUtensorMap km, vm;
   const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.cap;
   if (encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
@@ -347,9 +438,15 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv), kFwdThreads, smem, st>>>(
-      km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-      idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, dev_err);
+  block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares), kFwdThreads, smem, st>>>(
+      km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+      static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml,
+      dev_err);
+  if (f.shares > 1) {
+    const size_t qrows = static_cast<size_t>(p.B) * p.H * p.Nq;
+    block_join_kernel<D><<<static_cast<unsigned>((qrows + 7) / 8), 256, 0, st>>>(qrows, f.shares, f.part_o, f.part_ml,
+                                                                                static_cast<uint16_t*>(o), lse);
+  }
   return launch_status();
 }
 
@@ -359,16 +456,23 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
 
 using namespace svoo;
 
+extern "C" size_t svoo_block_attn_workspace_size(const svoo_block_shape* shape) {
+  if (!block_shape_ok(shape)) return 0;
+  return fwd_plan(block_dims(shape), shape->d, nullptr).bytes;
+}
+
 extern "C" svoo_status svoo_block_attn(const svoo_block_shape* shape, const void* q, const void* k, const void* v,
                                        const int32_t* idx, const int32_t* lengths, float scale, void* o, float* lse,
-                                       int32_t* dev_err, void* stream) {
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
   if (!block_shape_ok(shape) || !q || !k || !v || !idx || !o || !lse || !scale_ok(scale)) return SVOO_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(idx, 4) ||
-      !aligned(lse, 4))
+      !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
-  if (shape->Nq == 0) return SVOO_OK;
   const BlockDims p = block_dims(shape);
+  const size_t need = fwd_plan(p, shape->d, nullptr).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SVOO_ERR_WORKSPACE;
+  if (shape->Nq == 0) return SVOO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (shape->d == 128) return launch_block_attn<128>(p, q, k, v, idx, lengths, scale, o, lse, dev_err, st);
-  return launch_block_attn<64>(p, q, k, v, idx, lengths, scale, o, lse, dev_err, st);
+  if (shape->d == 128) return launch_block_attn<128>(p, q, k, v, idx, lengths, scale, o, lse, workspace, dev_err, st);
+  return launch_block_attn<64>(p, q, k, v, idx, lengths, scale, o, lse, workspace, dev_err, st);
 }

@@ -825,14 +825,14 @@ static_assert(dkv_tile_bytes<128>() + sizeof(DkvSmem) <= kMaxSmem, "dk, dv: shar
 
 // Rows of one piece: a quarter of an SM's share of all rows, so that a block
 // which every query keeps does not leave one SM with the last word, and at least
-// 32 tiles, below which a piece's own start and its part's bytes show. (An eighth
+// 8 tiles, below which a piece's own start and its part's bytes show. (An eighth
 // cut most of the lists of ordinary length too: the parts' sum alone took 78 us
 // of 2000 at 16384 tokens.)
 inline int piece_rows(const BlockDims& p) {
   const long long rows = static_cast<long long>(p.B) * p.Hkv * p.Nq * p.n_sel * p.nsub * p.G;
   long long piece = rows / (148 * 4);
   piece = (piece + kRowTile - 1) / kRowTile * kRowTile;
-  if (piece < 32 * kRowTile) piece = 32 * kRowTile;
+  if (piece < 8 * kRowTile) piece = 8 * kRowTile;
   return static_cast<int>(piece < (1 << 28) ? piece : (1 << 28));
 }
 

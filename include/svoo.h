@@ -351,10 +351,13 @@ svoo_status svoo_block_select(const svoo_block_shape *shape, const void *q, cons
  * first entry that is out of range or not above the one before it, and an entry
  * other than -1 there sets bit 4 in dev_err. A query without keys gets o = 0,
  * lse = -inf. sink and local are not used. fp32 softmax and sums; P is rounded
- * to bf16 for the second product. */
+ * to bf16 for the second product. The workspace (256-byte aligned; 0 bytes where
+ * there are many queries) must not be shared by calls that overlap on the GPU. */
+size_t svoo_block_attn_workspace_size(const svoo_block_shape *shape);
 svoo_status svoo_block_attn(const svoo_block_shape *shape, const void *q, const void *k,
                             const void *v, const int32_t *idx, const int32_t *lengths, float scale,
-                            void *o, float *lse, int32_t *dev_err, void *stream);
+                            void *o, float *lse, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_err, void *stream);
 
 /* Gradient of svoo_block_attn with respect to q, k and v (the selection is a
  * constant): dq bf16 [B][H][Nq][d]; dk, dv bf16 [B][Hkv][Nk][d], contiguous
