@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  load_query_rows<D, kFwdThreads>(q_s, q, p, b, hk, t0);
+  load_query_rows<D, kFwdThreads>(q_s, q, p, b, hk, t0, len);
   if (warp == 5) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 256);
@@ -464,14 +464,15 @@ extern "C" size_t svoo_block_attn_workspace_size(const svoo_block_shape* shape) 
 extern "C" svoo_status svoo_block_attn(const svoo_block_shape* shape, const void* q, const void* k, const void* v,
                                        const int32_t* idx, const int32_t* lengths, float scale, void* o, float* lse,
                                        void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
-  if (!block_shape_ok(shape) || !q || !k || !v || !idx || !o || !lse || !scale_ok(scale)) return SVOO_ERR_INVALID_ARG;
+  if (!block_shape_ok(shape) || !scale_ok(scale)) return SVOO_ERR_INVALID_ARG;
+  if (shape->Nq == 0) return SVOO_OK;  // empty tensors have no address
+  if (!q || !k || !v || !idx || !o || !lse) return SVOO_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(idx, 4) ||
       !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const size_t need = fwd_plan(p, shape->d, nullptr).bytes;
   if (need > 0 && (!workspace || workspace_bytes < need)) return SVOO_ERR_WORKSPACE;
-  if (shape->Nq == 0) return SVOO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (shape->d == 128) return launch_block_attn<128>(p, q, k, v, idx, lengths, scale, o, lse, workspace, dev_err, st);
   return launch_block_attn<64>(p, q, k, v, idx, lengths, scale, o, lse, workspace, dev_err, st);

@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  load_query_rows<D, kDqThreads>(q_s, q, p, b, hk, t0);
-  load_query_rows<D, kDqThreads>(g_s, go, p, b, hk, t0);
+  load_query_rows<D, kDqThreads>(q_s, q, p, b, hk, t0, len);
+  load_query_rows<D, kDqThreads>(g_s, go, p, b, hk, t0, len);
   if (warp == 9) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 512);
@@ -937,9 +937,9 @@ extern "C" svoo_status svoo_block_attn_backward(const svoo_block_shape* shape, c
                                                 const int32_t* idx, const int32_t* lengths, float scale, void* dq,
                                                 void* dk, void* dv, void* workspace, size_t workspace_bytes,
                                                 int32_t* dev_err, void* stream) {
-  if (!block_shape_ok(shape) || !q || !k || !v || !o || !lse || !grad_o || !idx || !dq || !dk || !dv || !workspace ||
-      !scale_ok(scale))
-    return SVOO_ERR_INVALID_ARG;
+  if (!block_shape_ok(shape) || !k || !v || !dk || !dv || !workspace || !scale_ok(scale)) return SVOO_ERR_INVALID_ARG;
+  // tensors without queries are empty and have no address; dk and dv are then zeros
+  if (shape->Nq > 0 && (!q || !o || !lse || !grad_o || !idx || !dq)) return SVOO_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, o, grad_o, static_cast<const void*>(dq), static_cast<const void*>(dk),
                         static_cast<const void*>(dv)})
     if (!aligned(x, 16)) return SVOO_ERR_INVALID_ARG;

@@ -1088,13 +1088,14 @@ extern "C" size_t svoo_block_select_workspace_size(const svoo_block_shape* shape
 extern "C" svoo_status svoo_block_select(const svoo_block_shape* shape, const void* q, const float* pool,
                                          const int32_t* lengths, int32_t* idx, void* workspace, size_t workspace_bytes,
                                          int32_t* dev_err, void* stream) {
-  if (!block_shape_ok(shape) || !q || !pool || !idx) return SVOO_ERR_INVALID_ARG;
+  if (!block_shape_ok(shape)) return SVOO_ERR_INVALID_ARG;
+  if (shape->Nq == 0) return SVOO_OK;  // empty tensors have no address
+  if (!q || !pool || !idx) return SVOO_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const size_t need = select_plan(p, shape->d, nullptr).bytes;
   if (need > 0 && (!workspace || workspace_bytes < need)) return SVOO_ERR_WORKSPACE;
-  if (shape->Nq == 0) return SVOO_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (mma_select(p)) {
     if (shape->d == 128) return launch_mma_select<128>(p, q, pool, lengths, idx, workspace, dev_err, st);
