@@ -26,34 +26,38 @@ namespace {
 
 // ------------------------------------------------------------------ dq
 
-// Row tiles and steps of two 64-key tiles as in the forward kernel; P needs no
+// Row tiles as in the forward kernel, in steps of two 64-key tiles; P needs no
 // maximum here, so the two tiles of a step are two groups of warps that never
-// meet. One CTA per SM: S alternates between two buffers, so S(j+1) is computed
-// under dS(j); dP has one, whose next product goes ahead of dQ(j).
+// meet. One CTA per SM. Q and dO are the products' first operand from tensor
+// memory: from shared memory, each product would read its 32 KB anew, and the
+// step was bound by shared memory's bandwidth (2400 cycles, for 1540 of the
+// tensor core). dS goes over dP, so that S(j+1) can follow as soon as S(j) has
+// been read, under the work on dS(j); dQ(j) and dP(j+1) follow that.
 // Warps: 0-3, 4-7 dS of a step's first / second tile (thread = row), 8 key and
 // value producer, 9 MMA issuer.
-// TMEM: S [0,128) and [128,256), dS over the first half of each tile's scores;
-// dP [256,384); dQ [384,384+D).
+// TMEM: S [0,128); dP [128,256), dS over the first half of each tile's part;
+// dQ [256,256+D); Q [384,384+D/2), dO [448,448+D/2).
 
 constexpr int kDqThreads = 320;
 constexpr int kDqPair = 2 * kKeyTile;
-
-constexpr int kDqK = 3;  // stages of K: dQ(j-1) may still read one while S(j+1) needs the next but one
+constexpr int kDqK = 3;  // stages of K: dQ(j) still reads one while S(j+1) reads the next
+constexpr int kDqV = 2;  // stages of V, where Q and dO pass through first
 
 struct DqSmem {
-  uint64_t k_full[kDqK], k_empty[kDqK], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, ds_full, mma_final;
+  uint64_t k_full[kDqK], k_empty[kDqK], v_full[kDqV], v_empty[kDqV];
+  uint64_t s_full, s_read, dp_full, ds_full, mma_final;
   uint32_t tmem_base;
   int abort;
   int max_limit;
   int tiles;
   int limit[kRowTile];
+  float delta[kRowTile];
 };
 
 template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
     block_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
-                    int cap, int v_stages, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                    int cap, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
                     const uint16_t* __restrict__ v, const uint16_t* __restrict__ go, const uint16_t* __restrict__ o,
                     const float* __restrict__ lse, float* __restrict__ delta, const int32_t* __restrict__ idx,
                     const int32_t* __restrict__ lengths, float scale, float scale_log2, uint16_t* __restrict__ dq,
@@ -68,11 +72,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (threadIdx.x == 0) report_error(err, kErrBadPlan);
     return;
   }
-  uint8_t* q_s = smem_raw;
-  uint8_t* g_s = q_s + kRowBytes;
-  uint8_t* k_s = g_s + kRowBytes;
+  uint8_t* k_s = smem_raw;
   uint8_t* v_s = k_s + kDqK * kPairBytes;
-  DqSmem* S = reinterpret_cast<DqSmem*>(v_s + v_stages * kPairBytes);
+  static_assert(kDqV * kPairBytes == 2 * kRowBytes, "Q and dO where V goes later");
+  uint8_t* q_s = v_s;
+  uint8_t* g_s = q_s + kRowBytes;
+  DqSmem* S = reinterpret_cast<DqSmem*>(v_s + kDqV * kPairBytes);
   const TileList tl = tile_list(p, cap, S + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -89,13 +94,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       mbar_init(smem_u32(&S->k_full[s]), 1);
       mbar_init(smem_u32(&S->k_empty[s]), 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kDqV; ++s) {
       mbar_init(smem_u32(&S->v_full[s]), 1);
       mbar_init(smem_u32(&S->v_empty[s]), 1);
-      mbar_init(smem_u32(&S->s_full[s]), 1);
     }
+    mbar_init(smem_u32(&S->s_full), 1);
+    mbar_init(smem_u32(&S->s_read), 8);   // one arrival per dS warp
     mbar_init(smem_u32(&S->dp_full), 1);
-    mbar_init(smem_u32(&S->ds_full), 8);  // one arrival per dS warp
+    mbar_init(smem_u32(&S->ds_full), 8);
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
@@ -116,7 +122,49 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
-  const uint32_t q_u = smem_u32(q_s), g_u = smem_u32(g_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
+  const uint32_t k_u = smem_u32(k_s), v_u = smem_u32(v_s);
+  if (warp < 8) {
+    // group 0 moves its row of Q to tensor memory, group 1 its row of dO, and
+    // takes delta from it on the way
+    const int h = warp >> 2, r = tid & 127, ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
+    const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 384 + h * 64;
+    const uint8_t* from = h ? g_s : q_s;
+    const bool live = ti < nt;
+    const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
+    const uint4* po = reinterpret_cast<const uint4*>(o + row * D);
+    float dl = 0.f;
+#pragma unroll
+    for (int c4 = 0; c4 < D / 32; ++c4) {
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(from + sw128_offset(r, (c4 * 4 + i) * 8, kRowTile));
+        x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+      }
+      tmem_st16(to + c4 * 16, x);
+      if (h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 y = po[c4 * 4 + i];
+          const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k2 = 0; k2 < 4; ++k2) {
+            dl = fmaf(__uint_as_float(x[4 * i + k2] << 16), __uint_as_float(ys[k2] << 16), dl);
+            dl = fmaf(__uint_as_float(x[4 * i + k2] & 0xffff0000u), __uint_as_float(ys[k2] & 0xffff0000u), dl);
+          }
+        }
+      }
+    }
+    if (h) {
+      S->delta[r] = dl;
+      if (live) delta[row] = dl;
+    }
+    tmem_wait_st();
+  }
+  fence_proxy_async_smem();  // the rows' place goes to the TMA
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   int k_armed = -1, v_armed = -1;
 
   if (warp == 8) {
@@ -132,13 +180,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       tma_prefetch_desc(&vmap);
     }
     for (int j = 0; j < steps; ++j) {
-      const int ks = j % kDqK, vs = j % v_stages;
+      const int ks = j % kDqK, vs = j % kDqV;
       const int key[2] = {static_cast<int>(tl.list[2 * j] & 0xffffu) * kKeyTile,
                           2 * j + 1 < tiles ? static_cast<int>(tl.list[2 * j + 1] & 0xffffu) * kKeyTile : -1};
       if (j >= kDqK && !warp_wait(smem_u32(&S->k_empty[ks]), (j / kDqK - 1) & 1)) break;
       load_key_pair<D>(&kmap, k, k_s + ks * kPairBytes, smem_u32(&S->k_full[ks]), row0, len, key);
       k_armed = j;
-      if (j >= v_stages && !warp_wait(smem_u32(&S->v_empty[vs]), (j / v_stages - 1) & 1)) break;
+      if (j >= kDqV && !warp_wait(smem_u32(&S->v_empty[vs]), (j / kDqV - 1) & 1)) break;
       load_key_pair<D>(&vmap, v, v_s + vs * kPairBytes, smem_u32(&S->v_full[vs]), row0, len, key);
       v_armed = j;
     }
@@ -147,24 +195,24 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kDqPair, false, false);
       const uint32_t idesc_q = idesc_bf16_f32(kRowTile, D, false, true);
-      auto rows_by_keys = [&](uint32_t d, uint32_t a_u, uint32_t b_u) {
+      auto rows_by_keys = [&](uint32_t d, uint32_t a_tmem, uint32_t b_u) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16(d, sw128_desc(a_u + (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, 16, 1024),
-                   sw128_desc(b_u + (kk >> 2) * kDqPair * 128 + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+          umma_f16_a_tmem(d, a_tmem + kk * 8, sw128_desc(b_u + (kk >> 2) * kDqPair * 128 + (kk & 3) * 32, 16, 1024),
+                          idesc_s, kk > 0 ? 1u : 0u);
       };
-      auto issue_s = [&](int j) -> bool {  // over dS(j-2), whose product is ahead in the queue
+      auto issue_s = [&](int j) -> bool {  // S(j-1) has been read
         if (!mbar_wait(smem_u32(&S->k_full[j % kDqK]), (j / kDqK) & 1, abort)) return false;
         tc_fence_after();
-        rows_by_keys(tmem + (j & 1) * 128, q_u, k_u + (j % kDqK) * kPairBytes);
-        umma_commit(smem_u32(&S->s_full[j & 1]));
+        rows_by_keys(tmem, tmem + 384, k_u + (j % kDqK) * kPairBytes);
+        umma_commit(smem_u32(&S->s_full));
         return true;
       };
-      auto issue_dp = [&](int j) -> bool {  // dP(j-1) has been read
-        const int vs = j % v_stages;
-        if (!mbar_wait(smem_u32(&S->v_full[vs]), (j / v_stages) & 1, abort)) return false;
+      auto issue_dp = [&](int j) -> bool {  // over dS(j-1), whose product is ahead in the queue
+        const int vs = j % kDqV;
+        if (!mbar_wait(smem_u32(&S->v_full[vs]), (j / kDqV) & 1, abort)) return false;
         tc_fence_after();
-        rows_by_keys(tmem + 256, g_u, v_u + vs * kPairBytes);
+        rows_by_keys(tmem + 128, tmem + 448, v_u + vs * kPairBytes);
         umma_commit(smem_u32(&S->dp_full));
         umma_commit(smem_u32(&S->v_empty[vs]));
         return true;
@@ -172,16 +220,16 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       bool ok = steps > 0 && issue_s(0) && issue_dp(0);
       for (int j = 0; j < steps && ok; ++j) {
         const bool more = j + 1 < steps;
-        if (more && !issue_s(j + 1)) break;
+        if (more && (!mbar_wait(smem_u32(&S->s_read), j & 1, abort) || !issue_s(j + 1))) break;
         if (!mbar_wait(smem_u32(&S->ds_full), j & 1, abort)) break;
         tc_fence_after();
-        if (more && !issue_dp(j + 1)) break;
         const uint32_t kt = k_u + (j % kDqK) * kPairBytes;
 #pragma unroll
         for (int kk = 0; kk < kDqPair / 16; ++kk)
-          umma_f16_a_tmem(tmem + 384, tmem + (j & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+          umma_f16_a_tmem(tmem + 256, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                           sw128_desc(kt + kk * 16 * 128, kDqPair * 128, 1024), idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(smem_u32(&S->k_empty[j % kDqK]));
+        if (more && !issue_dp(j + 1)) break;
       }
       umma_commit(smem_u32(&S->mma_final));
       mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
@@ -194,25 +242,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int lim = live ? S->limit[ti] : 0;
     const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
     const float lse2 = lse[row] * 1.4426950408889634f;
-    // delta, from dO as it lies in shared memory, under the first products
-    float dl = 0.f;
-    {
-      const uint4* po = reinterpret_cast<const uint4*>(o + row * D);
-      uint4 x[D / 8];
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) x[c] = po[c];
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 y = *reinterpret_cast<const uint4*>(g_s + sw128_offset(r, c * 8, kRowTile));
-        const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dl = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), dl);
-          dl = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), dl);
-        }
-      }
-      if (live && h == 0) delta[row] = dl;
-    }
+    const float dl = S->delta[r];
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t* my_word = tl.mask + (live ? ti >> 5 : 0);
     auto visible = [&](int j) {  // keys of this thread's tile in step j that the row sees
@@ -227,22 +257,27 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int j = 0; j < steps; ++j) {
       const bool some = __any_sync(0xffffffffu, nv > 0);
       const bool whole = __all_sync(0xffffffffu, nv == kKeyTile || nv == 0);
-      const uint32_t s_col = lane_base + (j & 1) * 128 + h * kKeyTile;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full[j & 1]), (j >> 1) & 1, abort));
+      const uint32_t s_col = lane_base + h * kKeyTile, p_col = s_col + 128;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort));
       if (!ok) break;
       tc_fence_after();
       float s[kKeyTile];
       if (some) {
-        // P = 2^(s - lse); a row that does not take part: 2^(s - inf) = 0
         tmem_ld32f(s_col, s);
         tmem_ld32f(s_col + 32, s + 32);
         tmem_wait_ld_f(s);
         tmem_wait_ld_f(s + 32);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->s_read));
+      if (some) {
         if (!whole) {  // the row's own limit falls into this tile
 #pragma unroll
           for (int c = 0; c < kKeyTile; ++c)
             if (c >= nv) s[c] = -INFINITY;
         }
+        // P = 2^(s - lse); a row that does not take part: 2^(s - inf) = 0
         const float nl = nv > 0 ? -lse2 : -INFINITY;
         const uint64_t nl2 = f2pack(nl, nl);
 #pragma unroll
@@ -261,7 +296,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) {
           float x[32];
-          tmem_ld32f(lane_base + 256 + h * kKeyTile + q4 * 32, x);
+          tmem_ld32f(p_col + q4 * 32, x);
           tmem_wait_ld_f(x);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -276,7 +311,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }
-      tmem_st32(s_col, pk);  // over scores that this warp alone has read
+      tmem_st32(p_col, pk);  // over dP that this warp alone has read
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -291,7 +326,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const int col = h * (D / 2) + c0 * 32;
         uint32_t x[32];
         if (steps > 0) {
-          tmem_ld32(lane_base + 384 + col, x);
+          tmem_ld32(lane_base + 256 + col, x);
           tmem_wait_ld_regs(x);
         }
         if (live) {
@@ -317,8 +352,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (warp == 8 && lane == 0) {  // copies still in flight land before the shared memory goes away
       for (int j = max(0, k_armed - kDqK + 1); j <= k_armed; ++j)
         mbar_wait_cleanup(smem_u32(&S->k_full[j % kDqK]), (j / kDqK) & 1);
-      for (int j = max(0, v_armed - v_stages + 1); j <= v_armed; ++j)
-        mbar_wait_cleanup(smem_u32(&S->v_full[j % v_stages]), (j / v_stages) & 1);
+      for (int j = max(0, v_armed - kDqV + 1); j <= v_armed; ++j)
+        mbar_wait_cleanup(smem_u32(&S->v_full[j % kDqV]), (j / kDqV) & 1);
     }
     __syncthreads();
   }
@@ -883,10 +918,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  // two stages of V where the list of tiles leaves the room
-  size_t dq_smem = static_cast<size_t>(2 * kRowTile + (kDqK + 2) * kDqPair) * D * 2 + sizeof(DqSmem) + tile_list_bytes(p);
-  const int v_stages = dq_smem <= kMaxSmem ? 2 : 1;
-  if (v_stages == 1) dq_smem -= static_cast<size_t>(kDqPair) * D * 2;
+  const size_t dq_smem = static_cast<size_t>(kDqK + kDqV) * kDqPair * D * 2 + sizeof(DqSmem) + tile_list_bytes(p);
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
   const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
   if (cudaFuncSetAttribute(block_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -909,7 +941,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
     sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        km, vm, p, static_cast<int>(union_cap(p)), v_stages, qp, kp, vp, gp, static_cast<const uint16_t*>(o), lse, g.delta, idx,
+        km, vm, p, static_cast<int>(union_cap(p)), qp, kp, vp, gp, static_cast<const uint16_t*>(o), lse, g.delta, idx,
         lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
