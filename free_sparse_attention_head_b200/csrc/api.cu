@@ -7,10 +7,9 @@
 
 namespace svoo {
 
-CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
-                         uint32_t box_rows, uint32_t box_cols) {
-  // looked up once; a function-local static is initialised exactly once even
-  // when several host threads make their first call at the same time
+// cuTensorMapEncodeTiled, looked up once; a function-local static is initialised
+// exactly once even when several host threads make their first call at the same time
+static PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -19,6 +18,12 @@ CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
       return nullptr;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }();
+  return fn;
+}
+
+CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                         uint32_t box_rows, uint32_t box_cols) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
@@ -27,6 +32,19 @@ CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_token_major(CUtensorMap* map, const void* base, uint64_t B, uint64_t H, uint64_t N, uint64_t cols,
+                            uint32_t heads, uint32_t tokens) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t dims[4] = {cols, H, N, B};
+  const cuuint64_t strides[3] = {N * cols * 2, cols * 2, H * N * cols * 2};
+  const cuuint32_t box[4] = {64, heads, tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace svoo

@@ -45,7 +45,7 @@ constexpr int kDqV = 2;  // stages of V, where Q and dO pass through first
 
 struct DqSmem {
   uint64_t k_full[kDqK], k_empty[kDqK], v_full[kDqV], v_empty[kDqV];
-  uint64_t s_full, s_read, dp_full, ds_full, mma_final;
+  uint64_t q_full, s_full, s_read, dp_full, ds_full, mma_final;
   uint32_t tmem_base;
   int abort;
   int max_limit;
@@ -56,10 +56,10 @@ struct DqSmem {
 
 template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
-    block_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
-                    int cap, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
-                    const uint16_t* __restrict__ v, const uint16_t* __restrict__ go, const uint16_t* __restrict__ o,
-                    const float* __restrict__ lse, float* __restrict__ delta, const int32_t* __restrict__ idx,
+    block_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
+                    const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, BlockDims p, int cap, const uint16_t* __restrict__ k,
+                    const uint16_t* __restrict__ v, const float* __restrict__ lse, float* __restrict__ delta, const int32_t* __restrict__ idx,
                     const int32_t* __restrict__ lengths, float scale, float scale_log2, uint16_t* __restrict__ dq,
                     int* __restrict__ err) {
   constexpr int kSub = D / 64;
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   static_assert(kDqV * kPairBytes == 2 * kRowBytes, "Q and dO where V goes later");
   uint8_t* q_s = v_s;
   uint8_t* g_s = q_s + kRowBytes;
+  uint8_t* o_s = k_s;  // and o, for delta, where K goes later
   DqSmem* S = reinterpret_cast<DqSmem*>(v_s + kDqV * kPairBytes);
   const TileList tl = tile_list(p, cap, S + 1);
 
@@ -102,19 +103,21 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(smem_u32(&S->s_read), 8);   // one arrival per dS warp
     mbar_init(smem_u32(&S->dp_full), 1);
     mbar_init(smem_u32(&S->ds_full), 8);
+    mbar_init(smem_u32(&S->q_full), 1);
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
+    const uint32_t bar = smem_u32(&S->q_full);
+    mbar_arrive_expect_tx(bar, 3 * p.tpt * p.G * D * 2);
+    load_query_rows<D>(&qmap, q_s, bar, hk * p.G, t0, b);
+    load_query_rows<D>(&gmap, g_s, bar, hk * p.G, t0, b);
+    load_query_rows<D>(&omap, o_s, bar, hk * p.G, t0, b);
   }
-  load_query_rows<D, kDqThreads>(q_s, q, p, b, hk, t0, len);
-  load_query_rows<D, kDqThreads>(g_s, go, p, b, hk, t0, len);
   if (warp == 9) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 512);
     tmem_relinquish();
   }
   const int tiles = make_tile_list<kDqThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
-  cp_async_wait_all();
-  fence_proxy_async_smem();
   const int steps = (tiles + 1) / 2;
   tc_fence_before();
   __syncthreads();
@@ -123,41 +126,38 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t k_u = smem_u32(k_s), v_u = smem_u32(v_s);
-  if (warp < 8) {
+  const bool loaded = mbar_wait(smem_u32(&S->q_full), 0, abort);
+  __syncwarp();
+  if (warp < 8 && loaded) {
     // group 0 moves its row of Q to tensor memory, group 1 its row of dO, and
     // takes delta from it on the way
     const int h = warp >> 2, r = tid & 127, ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
     const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 384 + h * 64;
     const uint8_t* from = h ? g_s : q_s;
-    const bool live = ti < nt;
-    const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + (live ? g : 0)) * p.Nq + t0 + (live ? ti : 0);
-    const uint4* po = reinterpret_cast<const uint4*>(o + row * D);
     float dl = 0.f;
 #pragma unroll
     for (int c4 = 0; c4 < D / 32; ++c4) {
       uint32_t x[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 y = *reinterpret_cast<const uint4*>(from + sw128_offset(r, (c4 * 4 + i) * 8, kRowTile));
+        const uint32_t at = sw128_offset(r, (c4 * 4 + i) * 8, kRowTile);
+        const uint4 y = *reinterpret_cast<const uint4*>(from + at);
         x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
-      }
-      tmem_st16(to + c4 * 16, x);
-      if (h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 y = po[c4 * 4 + i];
-          const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+        if (h) {
+          const uint4 z = *reinterpret_cast<const uint4*>(o_s + at);
+          const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
           for (int k2 = 0; k2 < 4; ++k2) {
-            dl = fmaf(__uint_as_float(x[4 * i + k2] << 16), __uint_as_float(ys[k2] << 16), dl);
-            dl = fmaf(__uint_as_float(x[4 * i + k2] & 0xffff0000u), __uint_as_float(ys[k2] & 0xffff0000u), dl);
+            dl = fmaf(__uint_as_float(x[4 * i + k2] << 16), __uint_as_float(zs[k2] << 16), dl);
+            dl = fmaf(__uint_as_float(x[4 * i + k2] & 0xffff0000u), __uint_as_float(zs[k2] & 0xffff0000u), dl);
           }
         }
       }
+      tmem_st16(to + c4 * 16, x);
     }
     if (h) {
       S->delta[r] = dl;
-      if (live) delta[row] = dl;
+      if (ti < nt) delta[(static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti] = dl;
     }
     tmem_wait_st();
   }
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
           for (int c8 = 0; c8 < 4; ++c8) {
             uint4 w = make_uint4(0, 0, 0, 0);
-            if (steps > 0) {
+            if (steps > 0 && lim > 0) {  // a query outside its sequence may hold anything
               w.x = pack_bf16x2(__uint_as_float(x[c8 * 8 + 0]) * scale, __uint_as_float(x[c8 * 8 + 1]) * scale);
               w.y = pack_bf16x2(__uint_as_float(x[c8 * 8 + 2]) * scale, __uint_as_float(x[c8 * 8 + 3]) * scale);
               w.z = pack_bf16x2(__uint_as_float(x[c8 * 8 + 4]) * scale, __uint_as_float(x[c8 * 8 + 5]) * scale);
@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         mbar_wait_cleanup(smem_u32(&S->k_full[j % kDqK]), (j / kDqK) & 1);
       for (int j = max(0, v_armed - kDqV + 1); j <= v_armed; ++j)
         mbar_wait_cleanup(smem_u32(&S->v_full[j % kDqV]), (j / kDqV) & 1);
+      mbar_wait_cleanup(smem_u32(&S->q_full), 0);
     }
     __syncthreads();
   }
@@ -522,6 +523,11 @@ constexpr size_t dkv_tile_bytes() {
   return 2 * static_cast<size_t>(kKeyTile) * D * 2 + 4 * static_cast<size_t>(kRowTile) * D * 2 +
          4 * static_cast<size_t>(kRowTile) * kKeyTile * 2;
 }
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // barrier of the four loader warps, with a vote
 __device__ __forceinline__ bool loaders_agree(bool ok) {
@@ -913,8 +919,12 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   const int BHk = p.B * p.Hkv;
   const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
                  *vp = static_cast<const uint16_t*>(v), *gp = static_cast<const uint16_t*>(go);
-  CUtensorMap km, vm;
+  CUtensorMap qm, gm, om, km, vm;
   const uint64_t krows = static_cast<uint64_t>(BHk) * p.cap;
+  if (p.Nq > 0 && (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
+                   encode_token_major(&gm, go, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
+                   encode_token_major(&om, o, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS))
+    return SVOO_ERR_CUDA;
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
@@ -941,8 +951,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
     sel_walk_kernel<true><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        km, vm, p, static_cast<int>(union_cap(p)), qp, kp, vp, gp, static_cast<const uint16_t*>(o), lse, g.delta, idx,
-        lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+        qm, gm, om, km, vm, p, static_cast<int>(union_cap(p)), kp, vp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
       p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,

@@ -193,10 +193,11 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
   }
   __syncthreads();
   bool bad = false;
+  int most = 0;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int ti = warp + i * (kThreads / 32);
-    if (ti >= nt) break;
+    if (ti >= nt) continue;
     const int lim = query_limit(p, len, t0 + ti);
     auto add = [&](int blk) {
       if (blk * p.block < lim) atomicOr(&t.bits[blk >> 5], 1u << (blk & 31));
@@ -208,11 +209,10 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
     } else {
       walk_slots(slots + static_cast<size_t>(ti) * p.n_sel, p.n_sel, p.nb, &bad, add);
     }
-    if (lane == 0) {
-      limits[ti] = lim;
-      atomicMax(shared_max, lim);
-    }
+    if (lane == 0) limits[ti] = lim;
+    most = max(most, lim);
   }
+  if (lane == 0) atomicMax(shared_max, most);
   if (bad && lane == 0) report_error(err, kErrBadPlan);
   __syncthreads();
   const int tiles = (*shared_max + kKeyTile - 1) / kKeyTile;
@@ -250,7 +250,7 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int ti = warp + i * (kThreads / 32);
-    if (ti >= nt) break;
+    if (ti >= nt) continue;
     auto mark = [&](int blk) {
       const int ord = t.rank[blk >> 5] + __popc(t.bits[blk >> 5] & ((1u << (blk & 31)) - 1u));
       atomicOr(&t.mask[ord * t.words + (ti >> 5)], 1u << (ti & 31));
@@ -327,24 +327,21 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The rows of a row tile (query-major, see above) of a [B, H, Nq, D] bf16
-// tensor into a swizzled 128-row tile; rows without a query, and those of
-// queries outside their sequence (which may hold anything), as zeros. The copies
-// are in flight when it returns: cp_async_wait_all() before the barrier.
-template <int D, int kThreads>
-__device__ __forceinline__ void load_query_rows(uint8_t* dst, const uint16_t* src, const BlockDims& p, int b, int hk,
-                                                int t0, int len) {
-  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
-  static_assert(kThreads % kChunks == 0, "a thread keeps its columns");
-  const int ch = threadIdx.x % kChunks;
-  const uint32_t to = smem_u32(dst);
-  const uint16_t* from = src + (static_cast<size_t>(b) * p.H + hk * p.G) * p.Nq * D + ch * 8;
-  for (int r = threadIdx.x / kChunks; r < kRowTile; r += kStep) {
-    const int ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
-    const bool there = ti < p.tpt && t0 + ti < p.Nq && query_limit(p, len, t0 + ti) > 0;
-    cp_async16_or_zero(to + sw128_offset(r, ch * 8, kRowTile),
-                       there ? from + (static_cast<size_t>(g) * p.Nq + t0 + ti) * D : src, there);
-  }
+// One thread: the rows of a row tile (query-major, see above) of a [B, H, Nq, D]
+// bf16 tensor (mapped by encode_token_major) into a swizzled 128-row tile,
+// completing on `bar`, which expects tpt * G * D * 2 bytes of it. Queries behind
+// the last arrive as zeros; rows from tpt * G on keep what was there, and rows of
+// queries outside their sequence may hold anything: a row's products reach that
+// row alone, and what such rows yield is not written.
+template <int D>
+__device__ __forceinline__ void load_query_rows(const CUtensorMap* map, uint8_t* dst, uint32_t bar, int head0, int t0,
+                                                int b) {
+  for (int s = 0; s < D / 64; ++s)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst) + s * kRowTile * 128),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(s * 64), "r"(head0), "r"(t0), "r"(b)
+        : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, A read from tensor memory.

@@ -59,6 +59,12 @@ struct Carver {
 CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows, uint32_t box_cols);
 
+// Map of a bf16 [B, H, N, cols] tensor as (cols, head, token, sequence) with a box
+// of 64 columns of `heads` heads of `tokens` tokens: one load brings a row tile
+// with its rows ordered by token, then head.
+CUresult encode_token_major(CUtensorMap* map, const void* base, uint64_t B, uint64_t H, uint64_t N, uint64_t cols,
+                            uint32_t heads, uint32_t tokens);
+
 inline svoo_status launch_status() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SVOO_OK : SVOO_ERR_CUDA;
