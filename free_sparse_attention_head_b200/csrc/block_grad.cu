@@ -524,11 +524,6 @@ constexpr size_t dkv_tile_bytes() {
          4 * static_cast<size_t>(kRowTile) * kKeyTile * 2;
 }
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // barrier of the four loader warps, with a vote
 __device__ __forceinline__ bool loaders_agree(bool ok) {
   uint32_t r;
