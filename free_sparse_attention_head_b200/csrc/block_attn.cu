@@ -36,7 +36,7 @@ constexpr int kMaxShares = 16;  // CTAs that share a row tile's list
 constexpr float kFwdRescaleLog2 = 32.0f;
 
 struct FwdSmem {
-  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
+  uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2];
   uint64_t s_full[2], p_full[2], mma_final;
   uint32_t tmem_base;
   int abort;
@@ -52,9 +52,9 @@ constexpr size_t fwd_tile_bytes() {
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 2)
-    block_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      BlockDims p, int cap, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
-                      const uint16_t* __restrict__ v, const int32_t* __restrict__ idx,
+    block_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, BlockDims p, int cap,
+                      const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const int32_t* __restrict__ idx,
                       const int32_t* __restrict__ lengths, float scale_log2, uint16_t* __restrict__ o,
                       float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
                       int* __restrict__ err) {
@@ -86,18 +86,18 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       mbar_init(smem_u32(&S->s_full[s]), 1);
       mbar_init(smem_u32(&S->p_full[s]), 4);
     }
+    mbar_init(smem_u32(&S->q_full), 1);
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
+    mbar_arrive_expect_tx(smem_u32(&S->q_full), p.tpt * p.G * D * 2);
+    load_query_rows<D>(&qmap, q_s, smem_u32(&S->q_full), hk * p.G, t0, b);
   }
-  copy_query_rows<D, kFwdThreads>(q_s, q, p, b, hk, t0, len);
   if (warp == 5) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
   int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
-  cp_async_wait_all();
-  fence_proxy_async_smem();
   if (gridDim.z > 1) {  // this CTA's share of the list
     const int per = (tiles + gridDim.z - 1) / gridDim.z, first = min(tiles, static_cast<int>(blockIdx.z) * per);
     tl.list += first;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         umma_commit(smem_u32(&S->k_empty[st]));
         return true;
       };
-      bool ok = tiles > 0 && issue_s(0);
+      bool ok = mbar_wait(smem_u32(&S->q_full), 0, abort) && tiles > 0 && issue_s(0);
       for (int j = 0; j < tiles && ok; ++j) {
         const int st = j & 1;
         // S(j+1) goes where P(j-1) was: its product is ahead in the queue
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         mbar_wait_cleanup(smem_u32(&S->k_full[j & 1]), (j >> 1) & 1);
       for (int j = max(0, v_armed - 1); j <= v_armed; ++j)
         mbar_wait_cleanup(smem_u32(&S->v_full[j & 1]), (j >> 1) & 1);
+      mbar_wait_cleanup(smem_u32(&S->q_full), 0);
     }
     __syncthreads();
   }
@@ -428,9 +429,10 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
                               const int32_t* lengths, float scale, void* o, float* lse, void* ws, int32_t* dev_err,
                               cudaStream_t st) {
   const FwdPlan f = fwd_plan(p, D, ws);
-  CUtensorMap km, vm;
+  CUtensorMap qm, km, vm;
   const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.cap;
-  if (encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
+  if (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
+      encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
   const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + tile_list_bytes(p);
@@ -439,8 +441,7 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares), kFwdThreads, smem, st>>>(
-      km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
-      static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml,
+      qm, km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml,
       dev_err);
   if (f.shares > 1) {
     const size_t qrows = static_cast<size_t>(p.B) * p.H * p.Nq;

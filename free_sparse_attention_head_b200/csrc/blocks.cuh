@@ -197,7 +197,7 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int ti = warp + i * (kThreads / 32);
-    if (ti >= nt) continue;
+    if (ti >= nt) break;
     const int lim = query_limit(p, len, t0 + ti);
     auto add = [&](int blk) {
       if (blk * p.block < lim) atomicOr(&t.bits[blk >> 5], 1u << (blk & 31));
@@ -250,7 +250,7 @@ __device__ __forceinline__ int make_tile_list(const BlockDims& p, const TileList
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int ti = warp + i * (kThreads / 32);
-    if (ti >= nt) continue;
+    if (ti >= nt) break;
     auto mark = [&](int blk) {
       const int ord = t.rank[blk >> 5] + __popc(t.bits[blk >> 5] & ((1u << (blk & 31)) - 1u));
       atomicOr(&t.mask[ord * t.words + (ti >> 5)], 1u << (ti & 31));
@@ -326,29 +326,6 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// The rows of a row tile (query-major, see above) of a [B, H, Nq, D] bf16
-// tensor into a swizzled 128-row tile; rows without a query, and those of
-// queries outside their sequence (which may hold anything), as zeros. The copies
-// are in flight when it returns: cp_async_wait_all() before the barrier. (Two
-// CTAs share an SM in the forward kernel, and one's copies run under the other's
-// products; by TMA its 128-byte rows took 3 % longer in all. The dq kernel, alone
-// on its SM, gained 6 % from the TMA.)
-template <int D, int kThreads>
-__device__ __forceinline__ void copy_query_rows(uint8_t* dst, const uint16_t* src, const BlockDims& p, int b, int hk,
-                                                int t0, int len) {
-  constexpr int kChunks = D / 8, kStep = kThreads / kChunks;
-  static_assert(kThreads % kChunks == 0, "a thread keeps its columns");
-  const int ch = threadIdx.x % kChunks;
-  const uint32_t to = smem_u32(dst);
-  const uint16_t* from = src + (static_cast<size_t>(b) * p.H + hk * p.G) * p.Nq * D + ch * 8;
-  for (int r = threadIdx.x / kChunks; r < kRowTile; r += kStep) {
-    const int ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
-    const bool there = ti < p.tpt && t0 + ti < p.Nq && query_limit(p, len, t0 + ti) > 0;
-    cp_async16_or_zero(to + sw128_offset(r, ch * 8, kRowTile),
-                       there ? from + (static_cast<size_t>(g) * p.Nq + t0 + ti) * D : src, there);
-  }
-}
 
 // One thread: the rows of a row tile (query-major, see above) of a [B, H, Nq, D]
 // bf16 tensor (mapped by encode_token_major) into a swizzled 128-row tile,
