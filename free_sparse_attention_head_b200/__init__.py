@@ -644,11 +644,16 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
     dev = q.device
     _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
     _need("out", torch.bfloat16, dev, q.shape, out)
+    return _run_attn(args, _block_scale(cfg, d), q, k, v, idx, lengths, out, workspace, dev_err, stream)
+
+
+def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err, stream=None):
+    dev = q.device
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(B, H, Nq, dtype=torch.float32, device=dev)
+    lse = torch.empty(args[0], args[1], args[3], dtype=torch.float32, device=dev)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
     _call("svoo_block_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-          _dp(lengths), _block_scale(cfg, d), out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _dp(dev_err))
+          _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return out, lse
 
 
@@ -662,32 +667,38 @@ def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=
     _need("o", torch.bfloat16, dev, q.shape, o)
     _need("grad_o", torch.bfloat16, dev, q.shape, grad_o)
     _need("lse", torch.float32, dev, (B, H, Nq), lse)
+    return _run_attn_backward(args, _block_scale(cfg, d), q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err,
+                              stream)
+
+
+def _run_attn_backward(args, scale, q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err, stream=None):
+    dev = q.device
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_backward_workspace_size", *args)
     dq = torch.empty_like(q)
     dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
     dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
     _call("svoo_block_attn_backward", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), _block_scale(cfg, d),
+          o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), scale,
           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return dq, dk, dv
 
 
 class _BlockAttn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, idx, cfg, lengths, q_start, dev_err):
-        o, lse = block_attn(q, k, v, idx, cfg, lengths, q_start, dev_err=dev_err)
-        ctx.save_for_backward(q, k, v, idx, lengths, o, lse, dev_err)
-        ctx.args = (cfg, q_start)
+    def forward(ctx, q, k, v, idx, args, scale, lengths, dev_err):
+        o, lse = _run_attn(args, scale, q, k, v, idx, lengths, None, None, dev_err)
+        ctx.save_for_backward(q, k, v, idx, lengths, o, lse)
+        ctx.args = (args, scale, dev_err)    # an error word may be cleared between the two passes
         ctx.mark_non_differentiable(lse)
         return o, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_o, _):
-        q, k, v, idx, lengths, o, lse, dev_err = ctx.saved_tensors
-        cfg, q_start = ctx.args
-        dq, dk, dv = block_attn_backward(q, k, v, o, lse, grad_o.contiguous(), idx, cfg, lengths, q_start,
-                                         dev_err=dev_err)
+        q, k, v, idx, lengths, o, lse = ctx.saved_tensors
+        args, scale, dev_err = ctx.args
+        _need("the incoming gradient", torch.bfloat16, q.device, q.shape, grad_o := grad_o.contiguous())
+        dq, dk, dv = _run_attn_backward(args, scale, q, k, v, o, lse, grad_o, idx, lengths, None, dev_err)
         return dq, dk, dv, None, None, None, None, None
 
 
@@ -696,14 +707,15 @@ def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[i
     blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
     right-padded batch. Differentiable in q, k and v (the selection is a constant of the gradient; the
     gradient's gradient is not offered). Returns (o, dict(idx, lse, pool, dev_err))."""
-    _block_args(q, k, v, cfg, lengths, q_start)
+    args = _block_args(q, k, v, cfg, lengths, q_start)
+    scale = _block_scale(cfg, args[6])
     err = _err_buf(dev_err, q.device)
     pool = block_pool(k, cfg, lengths)
-    idx = block_select(q, pool, cfg, k.shape[2], lengths, q_start, dev_err=err)
+    idx = block_select(q, pool, cfg, args[4], lengths, q_start, dev_err=err)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        o, lse = _BlockAttn.apply(q, k, v, idx, dataclasses.replace(cfg), lengths, q_start, err)
+        o, lse = _BlockAttn.apply(q, k, v, idx, args, scale, lengths, err)
     else:
-        o, lse = block_attn(q, k, v, idx, cfg, lengths, q_start, dev_err=err)
+        o, lse = _run_attn(args, scale, q, k, v, idx, lengths, None, None, err)
     return o, dict(idx=idx, lse=lse, pool=pool, dev_err=err)
 
 
