@@ -33,9 +33,13 @@ namespace {
 // step was bound by shared memory's bandwidth (2400 cycles, for 1540 of the
 // tensor core). dS goes over dP, so that S(j+1) can follow as soon as S(j) has
 // been read, under the work on dS(j); dQ(j) and dP(j+1) follow that.
+// dS goes into its product as two bf16 parts, 16 bits of it: rows of dS sum to
+// zero, so that one part's rounding is as large in dq as that of the output
+// (relative to the formula in 64 bits 2.9e-3 in all, with two parts 2.2e-3,
+// for 632 -> 784 us at 16,384 tokens with 16/4 heads).
 // Warps: 0-3, 4-7 dS of a step's first / second tile (thread = row), 8 key and
 // value producer, 9 MMA issuer.
-// TMEM: S [0,128); dP [128,256), dS over the first half of each tile's part;
+// TMEM: S [0,128); dP [128,256), the parts of dS over each tile's half of it;
 // dQ [256,256+D); Q [384,384+D/2), dO [448,448+D/2).
 
 constexpr int kDqThreads = 320;
@@ -225,9 +229,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tc_fence_after();
         const uint32_t kt = k_u + (j % kDqK) * kPairBytes;
 #pragma unroll
-        for (int kk = 0; kk < kDqPair / 16; ++kk)
-          umma_f16_a_tmem(tmem + 256, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                          sw128_desc(kt + kk * 16 * 128, kDqPair * 128, 1024), idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 2 * kDqPair / 16; ++kk) {
+          const int part = kk & 1, key = kk >> 1;  // 16 keys
+          umma_f16_a_tmem(tmem + 256, tmem + 128 + (key >> 2) * 64 + part * 32 + (key & 3) * 8,
+                          sw128_desc(kt + key * 16 * 128, kDqPair * 128, 1024), idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
+        }
         umma_commit(smem_u32(&S->k_empty[j % kDqK]));
         if (more && !issue_dp(j + 1)) break;
       }
@@ -290,9 +296,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->dp_full), j & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      uint32_t pk[32];
+      uint32_t pk[32], lo[32];
       if (some) {
-        // dS = P (dP - delta)
+        // dS = P (dP - delta), as two bf16 parts
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) {
           float x[32];
@@ -304,14 +310,17 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             f2unpack(f2mul(f2pack(s[q4 * 32 + 2 * c], s[q4 * 32 + 2 * c + 1]),
                            f2add(f2pack(x[2 * c], x[2 * c + 1]), nd2)),
                      e0, e1);
-            pk[q4 * 16 + c] = pack_bf16x2(e0, e1);
+            const uint32_t hi = pack_bf16x2(e0, e1);
+            pk[q4 * 16 + c] = hi;
+            lo[q4 * 16 + c] = pack_bf16x2(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
           }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        for (int c = 0; c < 32; ++c) pk[c] = lo[c] = 0u;
       }
       tmem_st32(p_col, pk);  // over dP that this warp alone has read
+      tmem_st32(p_col + 32, lo);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
