@@ -23,7 +23,7 @@ STALL_LIB = os.path.join(HERE, "libsvoo_stall.so")
 SOURCES = ["api.cu", "cluster.cu", "mask.cu", "permute.cu", "attn.cu", "psa.cu",
            "block_select.cu", "block_attn.cu", "block_grad.cu", "cache.cu"]
 STALL_SOURCES = ["cluster.cu", "attn.cu"]  # the kernels with pipeline waits
-HEADERS = ["common.cuh", "internal.h", "blocks.cuh"]
+HEADERS = ["common.cuh", "internal.h", "blocks.cuh", "block_lists.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC_FLAGS = [

@@ -22,7 +22,7 @@
 // behind it), 5 MMA issuer, which runs S(j+1) ahead of the softmax of tile j.
 // TMEM: S [0,64) and [64,128) alternating, P over the S that it came from,
 // O [128,128+D).
-#include "blocks.cuh"
+#include "block_lists.cuh"
 
 namespace svoo {
 
@@ -394,6 +394,355 @@ __global__ void __launch_bounds__(256)
   if (lane == 0) lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// ------------------------------------------------------------------ by key blocks
+
+// The other way round, for calls whose unions would be nearly all blocks: a CTA
+// keeps 128 keys of one block and their values in shared memory and runs through
+// the block's list, 128 gathered rows at a time, so that no row works for
+// nothing. What a row gets from those keys (a part: O at its own maximum m, and
+// m, l) goes to memory in 32 bits; block_parts_kernel adds a row's parts. The
+// parts' bytes bound it (D * 4 per row and 128 keys, written and read), so the
+// way pays only where a block has 128 keys or more.
+// Two CTAs share an SM, each with one row tile in work: one's softmax and
+// stores run beside the other's loads and products.
+// Warps: 0-3 softmax (thread = row), 4-7 row gather, 8 MMA issuer.
+// TMEM: S [0,128), P over its first half, O [128,128+D).
+
+constexpr int kListThreads = 288;
+constexpr int kListKeys = 2 * kKeyTile;
+
+struct ListSmem {
+  uint64_t full, q_free, s_full, p_full, o_full, mma_final;
+  uint32_t tmem_base;
+  int abort;
+  int row[kRowTile];      // gather: the rows of the tile being loaded
+  int part[2][kRowTile];  // a row's part, -1: none of these keys are the row's
+  uint8_t nv[2][kRowTile];  // keys that the row sees
+};
+
+template <int D>
+constexpr size_t list_tile_bytes() {
+  return static_cast<size_t>(2 * kListKeys + kRowTile) * D * 2;
+}
+
+__device__ __forceinline__ void st_global_f32x8(float* at, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// Dimensions as the lists' kernels take them here: a key tile is 128 keys.
+inline BlockDims list_dims(BlockDims p) {
+  p.nsub = p.block / kListKeys;
+  return p;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kListThreads, 2)
+    block_list_kernel(BlockDims p, int ktiles, int piece, const uint16_t* __restrict__ q,
+                      const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
+                      const int32_t* __restrict__ lengths, const int32_t* __restrict__ total,
+                      const int32_t* __restrict__ start, const int32_t* __restrict__ list,
+                      const int4* __restrict__ items, const int32_t* __restrict__ counts, float scale_log2,
+                      float* __restrict__ part_o, float2* __restrict__ part_ml, int* __restrict__ err) {
+  constexpr int kKvBytes = kListKeys * D * 2;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* k_s = base;
+  uint8_t* v_s = k_s + kKvBytes;
+  uint8_t* q_s = v_s + kKvBytes;
+  ListSmem* S = reinterpret_cast<ListSmem*>(q_s + kRowTile * D * 2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= counts[0]) return;
+  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  const int4 item = items[blockIdx.x];
+  const int bh = item.x / ktiles, kt = item.x - bh * ktiles, key0 = kt * kListKeys;
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int len = seq_len(p, lengths, b);
+  const size_t at = static_cast<size_t>(bh) * p.nb + kt / p.nsub;
+  const int32_t* toks = list + static_cast<size_t>(bh) * p.Nq * p.n_sel + start[at];
+  const long long all_rows = static_cast<long long>(total[at]) * p.G;
+  const long long row0 = static_cast<long long>(item.y) * piece;
+  const int rows = static_cast<int>(min(static_cast<long long>(piece), all_rows - row0));
+  const int nj = (max(rows, 0) + kRowTile - 1) / kRowTile;
+  if (nj == 0) return;
+
+  if (tid == 0) {
+    S->abort = 0;
+    mbar_init(smem_u32(&S->full), 128);
+    mbar_init(smem_u32(&S->q_free), 1);
+    mbar_init(smem_u32(&S->s_full), 1);
+    mbar_init(smem_u32(&S->p_full), 4);
+    mbar_init(smem_u32(&S->o_full), 1);
+    mbar_init(smem_u32(&S->mma_final), 1);
+    fence_mbar_init();
+  }
+  const size_t krow = static_cast<size_t>(bh) * p.cap + key0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_key_rows<D, kListKeys>(k_s + h * kKeyTile * 128, k, krow + h * kKeyTile, len - key0 - h * kKeyTile, tid,
+                                kListThreads);
+    load_key_rows<D, kListKeys>(v_s + h * kKeyTile * 128, v, krow + h * kKeyTile, len - key0 - h * kKeyTile, tid,
+                                kListThreads);
+  }
+  fence_proxy_async_smem();
+  if (warp == 8) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&S->tmem_base), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  volatile int* abort = &S->abort;
+
+  if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- row gather
+    const int t = tid - 128;  // one row's list entry per thread
+    constexpr int kChunks = D / 8;
+    const int ch = t % kChunks, r0 = t / kChunks;
+    const uint32_t q_dst = smem_u32(q_s);
+    const int per_row = p.n_sel * p.nsub;
+    int row = -1, part = -1, nv = 0;
+    auto entry = [&](int j) {  // this thread's row in tile j, -1 behind the last
+      const int f = j * kRowTile + t;
+      return f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
+    };
+    auto scalars = [&](int j, int e) {
+      row = part = -1;
+      nv = 0;
+      if (e >= 0) {
+        const int tok = e & 0xffffff, g = static_cast<int>((row0 + j * kRowTile + t) % p.G);
+        row = (b * p.H + hk * p.G + g) * p.Nq + tok;
+        nv = max(0, min(kListKeys, query_limit(p, len, tok) - key0));
+        if (nv > 0) part = row * per_row + (e >> 24) * p.nsub + kt % p.nsub;
+      }
+    };
+    scalars(0, entry(0));
+    int next = entry(1);
+    for (int j = 0; j < nj; ++j) {
+      // S(j-1) is done with the rows; it came after the softmax of tile j-2,
+      // which was the last to read this tile's place in part[] and nv[]
+      const bool free = j < 1 || mbar_wait(smem_u32(&S->q_free), (j - 1) & 1, abort);
+      S->row[t] = row;
+      if (!loaders_agree(free)) break;  // all four warps go on or leave together
+#pragma unroll 4
+      for (int r = r0; r < kRowTile; r += 128 / kChunks) {
+        const int src = S->row[r];
+        cp_async16_or_zero(q_dst + sw128_offset(r, ch * 8, kRowTile),
+                           q + static_cast<size_t>(src < 0 ? 0 : src) * D + ch * 8, src >= 0);
+      }
+      S->part[j & 1][t] = part;
+      S->nv[j & 1][t] = static_cast<uint8_t>(nv);
+      scalars(j + 1, next);
+      next = entry(j + 2);
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&S->full));  // this thread's part of row tile j is in
+      loaders_agree(true);  // S->row is free again
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kListKeys, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(kRowTile, D, false, true);
+      const uint32_t k_u = smem_u32(k_s), v_u = smem_u32(v_s), q_u = smem_u32(q_s);
+      for (int j = 0; j < nj; ++j) {
+        if (!mbar_wait(smem_u32(&S->full), j & 1, abort)) break;
+        tc_fence_after();
+        // over P(j-1), whose product is ahead in the queue
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16(tmem, sw128_desc(q_u + (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, 16, 1024),
+                   sw128_desc(k_u + (kk >> 2) * kListKeys * 128 + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&S->s_full));
+        umma_commit(smem_u32(&S->q_free));
+        if (!mbar_wait(smem_u32(&S->p_full), j & 1, abort)) break;  // and O(j-1) has been read
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kListKeys / 16; ++kk)
+          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(v_u + kk * 16 * 128, kListKeys * 128, 1024), idesc_o,
+                          kk > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&S->o_full));
+      }
+      umma_commit(smem_u32(&S->mma_final));
+      mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int r = tid;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint64_t sc2 = f2pack(scale_log2, scale_log2);
+    for (int j = 0; j < nj; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort))) break;
+      tc_fence_after();
+      // they came with the row's tile, which S was computed from
+      const int part = S->part[j & 1][r], nv = S->nv[j & 1][r];
+      const bool whole = __all_sync(0xffffffffu, nv == kListKeys || nv == 0);
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        float s[32];
+        tmem_ld32f(lane_base + h * 32, s);
+        tmem_wait_ld_f(s);
+        if (!whole) {  // a row's own limit falls into these keys
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c >= nv) s[c] = -INFINITY;
+        }
+        float m2[2] = {fmaxf(m, s[0]), s[1]};
+#pragma unroll
+        for (int c = 2; c < 32; c += 4) {
+          m2[0] = fmax3(m2[0], s[c], s[c + 1]);
+          if (c + 2 < 32) m2[1] = fmax3(m2[1], s[c + 2], s[c + 3]);
+        }
+        m = fmaxf(m2[0], m2[1]);
+      }
+      m = nv > 0 ? m * scale_log2 : -INFINITY;
+      const float nm = nv > 0 ? -m : -INFINITY;  // a row without keys here: 2^(s - inf) = 0
+      const uint64_t nm2 = f2pack(nm, nm);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {  // P(h) goes where S(h / 2) was
+        float s[32];
+        tmem_ld32f(lane_base + h * 32, s);
+        tmem_wait_ld_f(s);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c >= nv) s[c] = -INFINITY;
+        }
+        uint32_t pk[16];
+        uint64_t sum2 = 0ull;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x0, x1;
+          f2unpack(f2fma(f2pack(s[2 * c], s[2 * c + 1]), sc2, nm2), x0, x1);
+          x0 = ex2_approx(x0);
+          x1 = ex2_approx(x1);
+          pk[c] = pack_bf16x2(x0, x1);  // for the second product; l sums them in 32 bits
+          sum2 = f2add(f2pack(x0, x1), sum2);
+        }
+        tmem_st16(lane_base + h * 16, pk);
+        float a0, a1;
+        f2unpack(sum2, a0, a1);
+        l += a0 + a1;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->p_full));
+      if (part >= 0) part_ml[part] = make_float2(m, l);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->o_full), j & 1, abort))) break;
+      tc_fence_after();
+      float* to = part_o + static_cast<size_t>(part < 0 ? 0 : part) * D;
+#pragma unroll
+      for (int c0 = 0; c0 < D / 32; ++c0) {
+        uint32_t x[32];
+        tmem_ld32(lane_base + 128 + c0 * 32, x);
+        tmem_wait_ld_regs(x);
+        if (part >= 0) {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8) st_global_f32x8(to + c0 * 32 + c8 * 8, x + c8 * 8);
+        }
+      }
+      tc_fence_before();  // O is free with p_full of the next tile
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort) report_error(err, kErrTimeoutAttn);
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// One warp per row of [B*H*Nq, D], a lane per part: o = sum of the row's parts,
+// each at its own maximum. The parts that exist are those of the list's walk:
+// the counted slots' key tiles below the row's limit.
+template <int D>
+__global__ void __launch_bounds__(256)
+    block_parts_kernel(BlockDims p, const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths,
+                       const float* __restrict__ part_o, const float2* __restrict__ part_ml, uint16_t* __restrict__ o,
+                       float* __restrict__ lse, int* __restrict__ err) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<size_t>(p.B) * p.H * p.Nq) return;
+  constexpr int kE = D / 32, kDeep = 8;
+  const int t = static_cast<int>(row % p.Nq), head = static_cast<int>(row / p.Nq);
+  const int b = head / p.H, hk = (head - b * p.H) / p.G;
+  const int lim = query_limit(p, seq_len(p, lengths, b), t);
+  bool bad = false;
+  const size_t mine = (static_cast<size_t>(b) * p.Hkv + hk) * p.Nq + t;
+  const int held = counted_slot(lane < p.n_sel ? idx[mine * p.n_sel + lane] : -1, p.nb, &bad);
+  if (bad && lane == 0) report_error(err, kErrBadPlan);
+  const int parts = p.n_sel * p.nsub;
+  const int blk = __shfl_sync(0xffffffffu, held, (lane / p.nsub) & 31);
+  const bool there = lane < parts && blk >= 0 && (blk * p.nsub + lane % p.nsub) * kListKeys < lim;
+  const float2 ml = there ? part_ml[row * parts + lane] : make_float2(-INFINITY, 0.f);
+  float top = ml.x;
+#pragma unroll
+  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  const float f = there ? ex2_approx(ml.x - top) : 0.f;
+  float l = ml.y * f;
+#pragma unroll
+  for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  float acc[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  const float* src = part_o + row * parts * D + lane * kE;
+  const unsigned all = __ballot_sync(0xffffffffu, there);
+  for (int i0 = 0; i0 < parts; i0 += kDeep) {
+    float x[kDeep][kE];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        float2 y = make_float2(0.f, 0.f);
+        if (i0 + i < parts && ((all >> (i0 + i)) & 1u))
+          y = *reinterpret_cast<const float2*>(src + static_cast<size_t>(i0 + i) * D + e);
+        x[i][e] = y.x;
+        x[i][e + 1] = y.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+      if (i0 + i < parts)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = fmaf(x[i][e], fi, acc[e]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kE);
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host side
+
+// Whether a call goes by key blocks. The union of a row tile's selections costs
+// about 0.9 ns per row and block of 128 keys (d = 128) in it, the other way
+// about 3 ns per row and *selected* block, so the union has to be five times a
+// selection and more; and it is near that only where the tile holds queries
+// enough to name each block four times over (neighbouring queries agree). Lists
+// and launches cost some 40 us: small calls keep to the union. The parts' place
+// stays below 4 GB.
+inline bool by_blocks(const BlockDims& p) {
+  if (p.block % kListKeys || p.n_sel * (p.block / kListKeys) > 32 || p.Nq >= 1 << 24) return false;
+  const long long parts = static_cast<long long>(p.B) * p.H * p.Nq * p.n_sel * (p.block / kListKeys);
+  if (parts < 1 << 18 || parts > 1 << 23) return false;
+  long long seen = p.nb;  // blocks before the middle query
+  if (p.causal) {
+    const long long middle = (p.q_start >= 0 ? p.q_start : p.Nk - p.Nq) + p.Nq / 2;
+    if (middle / p.block + 1 < seen) seen = middle / p.block + 1;
+  }
+  return seen >= 5LL * p.n_sel && static_cast<long long>(p.tpt) * p.n_sel >= 4 * seen;
+}
+
 // Shares of a row tile's list: as many as bring two CTAs to every SM, while a
 // share may have four key tiles or more (the lists' lengths are not known here,
 // their bound is).
@@ -407,21 +756,79 @@ inline int block_shares(const BlockDims& p) {
   return z < 1 ? 1 : static_cast<int>(z);
 }
 
+// Rows of one piece of a list: an eighth of an SM's share of all, two CTAs an SM.
+inline int list_piece(const BlockDims& p) {
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Nq * p.n_sel * p.nsub;
+  long long piece = (rows / (148 * 8) + kRowTile - 1) / kRowTile * kRowTile;
+  return static_cast<int>(piece < 8 * kRowTile ? 8 * kRowTile : piece);
+}
+
 struct FwdPlan {
+  bool by_blocks;
   int shares;
+  int ktiles, chunk, nchunk, piece;
+  long long max_items;
+  int32_t *hist, *total, *start, *list, *counts;
+  int4* items;
   float* part_o;
   float2* part_ml;
   size_t bytes;
 };
 FwdPlan fwd_plan(const BlockDims& p, int d, void* ws) {
-  FwdPlan f;
-  f.shares = block_shares(p);
-  const size_t rows = f.shares > 1 ? static_cast<size_t>(f.shares) * p.B * p.H * p.Nq : 0;
+  FwdPlan f = {};
+  f.by_blocks = by_blocks(p);
+  f.shares = f.by_blocks ? 1 : block_shares(p);
   Carver c(ws);
-  f.part_o = c.take<float>(rows * d);
-  f.part_ml = c.take<float2>(rows);
+  size_t parts = f.shares > 1 ? static_cast<size_t>(f.shares) * p.B * p.H * p.Nq : 0;
+  if (f.by_blocks) {
+    const BlockDims lp = list_dims(p);
+    const size_t BHk = static_cast<size_t>(p.B) * p.Hkv;
+    parts = static_cast<size_t>(p.B) * p.H * p.Nq * p.n_sel * lp.nsub;
+    f.ktiles = (p.Nk + kListKeys - 1) / kListKeys;
+    f.chunk = sel_chunk(p);
+    f.nchunk = (p.Nq + f.chunk - 1) / f.chunk;
+    f.piece = list_piece(lp);
+    f.max_items = static_cast<long long>(BHk * f.ktiles + parts / f.piece);
+    f.hist = c.take<int32_t>(BHk * f.nchunk * p.nb);
+    f.total = c.take<int32_t>(BHk * p.nb);
+    f.start = c.take<int32_t>(BHk * p.nb);
+    f.list = c.take<int32_t>(BHk * p.Nq * p.n_sel);
+    f.counts = c.take<int32_t>(2);
+    f.items = c.take<int4>(static_cast<size_t>(f.max_items));
+  }
+  f.part_o = c.take<float>(parts * d);
+  f.part_ml = c.take<float2>(parts);
   f.bytes = (c.used + 255) / 256 * 256;
   return f;
+}
+
+template <int D>
+svoo_status launch_block_lists(const BlockDims& p, const FwdPlan& f, const uint16_t* q, const uint16_t* k,
+                               const uint16_t* v, const int32_t* idx, const int32_t* lengths, float scale_log2,
+                               uint16_t* o, float* lse, int32_t* dev_err, cudaStream_t st) {
+  const BlockDims lp = list_dims(p);
+  const int BHk = p.B * p.Hkv;
+  const size_t smem = 1024 + list_tile_bytes<D>() + sizeof(ListSmem), cnt = static_cast<size_t>(p.nb) * 4;
+  if (cudaFuncSetAttribute(block_list_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(sel_walk_kernel<kSelCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(sel_walk_kernel<kSelSlots>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+          cudaSuccess)
+    return SVOO_ERR_CUDA;
+  sel_walk_kernel<kSelCount><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
+                                                                   nullptr, nullptr);
+  sel_scan_kernel<<<dim3((p.nb + 31) / 32, BHk), 256, 0, st>>>(lp, f.nchunk, f.hist, f.total);
+  sel_items_kernel<<<1, 1024, 0, st>>>(lp, f.ktiles, f.piece, f.total, f.start, f.items, f.counts);
+  sel_walk_kernel<kSelSlots><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
+                                                                   f.start, f.list);
+  block_list_kernel<D><<<static_cast<unsigned>(f.max_items), kListThreads, smem, st>>>(
+      lp, f.ktiles, f.piece, q, k, v, lengths, f.total, f.start, f.list, f.items, f.counts, scale_log2, f.part_o,
+      f.part_ml, dev_err);
+  const size_t rows = static_cast<size_t>(p.B) * p.H * p.Nq;
+  block_parts_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(lp, idx, lengths, f.part_o, f.part_ml, o,
+                                                                               lse, dev_err);
+  return launch_status();
 }
 
 template <int D>
@@ -429,6 +836,11 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
                               const int32_t* lengths, float scale, void* o, float* lse, void* ws, int32_t* dev_err,
                               cudaStream_t st) {
   const FwdPlan f = fwd_plan(p, D, ws);
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (f.by_blocks)
+    return launch_block_lists<D>(p, f, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                                 static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o),
+                                 lse, dev_err, st);
   CUtensorMap qm, km, vm;
   const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.cap;
   if (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
@@ -439,10 +851,9 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   if (cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
-  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares), kFwdThreads, smem, st>>>(
-      qm, km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml,
-      dev_err);
+      qm, km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx,
+      lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml, dev_err);
   if (f.shares > 1) {
     const size_t qrows = static_cast<size_t>(p.B) * p.H * p.Nq;
     block_join_kernel<D><<<static_cast<unsigned>((qrows + 7) / 8), 256, 0, st>>>(qrows, f.shares, f.part_o, f.part_ml,
