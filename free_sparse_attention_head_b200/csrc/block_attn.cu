@@ -400,24 +400,30 @@ __global__ void __launch_bounds__(256)
 // keeps 128 keys of one block and their values in shared memory and runs through
 // the block's list, 128 gathered rows at a time, so that no row works for
 // nothing. What a row gets from those keys (a part: O at its own maximum m, and
-// m, l) goes to memory in 32 bits; block_parts_kernel adds a row's parts. The
-// parts' bytes bound it (D * 4 per row and 128 keys, written and read), so the
-// way pays only where a block has 128 keys or more.
-// Two CTAs share an SM, each with one row tile in work: one's softmax and
-// stores run beside the other's loads and products.
-// Warps: 0-3 softmax (thread = row), 4-7 row gather, 8 MMA issuer.
+// m, l) goes to memory in 32 bits, in the list's order; block_parts_kernel finds
+// a row's parts by its slots' places in the lists and adds them. The parts' bytes
+// bound it (D * 4 per row and 128 keys, written and read), so the way pays only
+// where a block has 128 keys or more.
+// A row tile's parts lie as [D / 8][rows of the tile][8], so that a warp, whose
+// threads have a row each, stores 1 KB at a time: whole rows would be 32 lines a
+// store, and kept the load/store unit busy for half of the kernel's time.
+// Two CTAs share an SM, each with one row tile in work; stores (32 bytes a clock
+// and SM) take as long as the rest, so warps of their own issue them, beside the
+// products and the softmax of the next tile. The softmax warps gather the next
+// tile's rows (cp.async) as soon as S has been computed.
+// Warps: 0-3 gather and softmax (thread = row), 4-7 stores, 8 keys and values
+// (TMA), MMA issuer.
 // TMEM: S [0,128), P over its first half, O [128,128+D).
 
 constexpr int kListThreads = 288;
 constexpr int kListKeys = 2 * kKeyTile;
 
+constexpr int kPartCols = 8;  // columns that a part's rows have together
+
 struct ListSmem {
-  uint64_t full, q_free, s_full, p_full, o_full, mma_final;
+  uint64_t kv_full[2], full, s_full, p_full, o_full, o_read, mma_final;
   uint32_t tmem_base;
   int abort;
-  int row[kRowTile];      // gather: the rows of the tile being loaded
-  int part[2][kRowTile];  // a row's part, -1: none of these keys are the row's
-  uint8_t nv[2][kRowTile];  // keys that the row sees
 };
 
 template <int D>
@@ -437,14 +443,20 @@ inline BlockDims list_dims(BlockDims p) {
   return p;
 }
 
+// The first part of a block's list for its c-th 128 keys; a list has `rows` rows.
+__device__ __forceinline__ size_t list_part(const BlockDims& p, int bh, int start, int rows, int c) {
+  return (static_cast<size_t>(bh) * p.Nq * p.n_sel + start) * p.G * p.nsub + static_cast<size_t>(c) * rows;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kListThreads, 2)
-    block_list_kernel(BlockDims p, int ktiles, int piece, const uint16_t* __restrict__ q,
-                      const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                      const int32_t* __restrict__ lengths, const int32_t* __restrict__ total,
-                      const int32_t* __restrict__ start, const int32_t* __restrict__ list,
-                      const int4* __restrict__ items, const int32_t* __restrict__ counts, float scale_log2,
-                      float* __restrict__ part_o, float2* __restrict__ part_ml, int* __restrict__ err) {
+    block_list_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
+                      int ktiles, int piece, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                      const uint16_t* __restrict__ v, const int32_t* __restrict__ lengths,
+                      const int32_t* __restrict__ total, const int32_t* __restrict__ start,
+                      const int32_t* __restrict__ list, const int4* __restrict__ items,
+                      const int32_t* __restrict__ counts, float scale_log2, float* __restrict__ part_o,
+                      float2* __restrict__ part_ml, int* __restrict__ err) {
   constexpr int kKvBytes = kListKeys * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -467,26 +479,20 @@ __global__ void __launch_bounds__(kListThreads, 2)
   const int rows = static_cast<int>(min(static_cast<long long>(piece), all_rows - row0));
   const int nj = (max(rows, 0) + kRowTile - 1) / kRowTile;
   if (nj == 0) return;
+  const size_t part0 = list_part(p, bh, start[at], static_cast<int>(all_rows), kt % p.nsub) + row0;
 
   if (tid == 0) {
     S->abort = 0;
-    mbar_init(smem_u32(&S->full), 128);
-    mbar_init(smem_u32(&S->q_free), 1);
+    mbar_init(smem_u32(&S->kv_full[0]), 1);
+    mbar_init(smem_u32(&S->kv_full[1]), 1);
+    mbar_init(smem_u32(&S->full), 4);  // one arrival per warp
     mbar_init(smem_u32(&S->s_full), 1);
     mbar_init(smem_u32(&S->p_full), 4);
     mbar_init(smem_u32(&S->o_full), 1);
+    mbar_init(smem_u32(&S->o_read), 4);
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
-  const size_t krow = static_cast<size_t>(bh) * p.cap + key0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load_key_rows<D, kListKeys>(k_s + h * kKeyTile * 128, k, krow + h * kKeyTile, len - key0 - h * kKeyTile, tid,
-                                kListThreads);
-    load_key_rows<D, kListKeys>(v_s + h * kKeyTile * 128, v, krow + h * kKeyTile, len - key0 - h * kKeyTile, tid,
-                                kListThreads);
-  }
-  fence_proxy_async_smem();
   if (warp == 8) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 256);
@@ -498,58 +504,19 @@ __global__ void __launch_bounds__(kListThreads, 2)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
 
-  if (warp >= 4 && warp < 8) {
-    // ---------------------------------------------------------------- row gather
-    const int t = tid - 128;  // one row's list entry per thread
-    constexpr int kChunks = D / 8;
-    const int ch = t % kChunks, r0 = t / kChunks;
-    const uint32_t q_dst = smem_u32(q_s);
-    const int per_row = p.n_sel * p.nsub;
-    int row = -1, part = -1, nv = 0;
-    auto entry = [&](int j) {  // this thread's row in tile j, -1 behind the last
-      const int f = j * kRowTile + t;
-      return f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
-    };
-    auto scalars = [&](int j, int e) {
-      row = part = -1;
-      nv = 0;
-      if (e >= 0) {
-        const int tok = e & 0xffffff, g = static_cast<int>((row0 + j * kRowTile + t) % p.G);
-        row = (b * p.H + hk * p.G + g) * p.Nq + tok;
-        nv = max(0, min(kListKeys, query_limit(p, len, tok) - key0));
-        if (nv > 0) part = row * per_row + (e >> 24) * p.nsub + kt % p.nsub;
-      }
-    };
-    scalars(0, entry(0));
-    int next = entry(1);
-    for (int j = 0; j < nj; ++j) {
-      // S(j-1) is done with the rows; it came after the softmax of tile j-2,
-      // which was the last to read this tile's place in part[] and nv[]
-      const bool free = j < 1 || mbar_wait(smem_u32(&S->q_free), (j - 1) & 1, abort);
-      S->row[t] = row;
-      if (!loaders_agree(free)) break;  // all four warps go on or leave together
-#pragma unroll 4
-      for (int r = r0; r < kRowTile; r += 128 / kChunks) {
-        const int src = S->row[r];
-        cp_async16_or_zero(q_dst + sw128_offset(r, ch * 8, kRowTile),
-                           q + static_cast<size_t>(src < 0 ? 0 : src) * D + ch * 8, src >= 0);
-      }
-      S->part[j & 1][t] = part;
-      S->nv[j & 1][t] = static_cast<uint8_t>(nv);
-      scalars(j + 1, next);
-      next = entry(j + 2);
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&S->full));  // this thread's part of row tile j is in
-      loaders_agree(true);  // S->row is free again
-    }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- MMA issuer
+  if (warp == 8) {
+    // ---------------------------------------------------------------- keys, values, MMA issuer
+    const size_t krow = static_cast<size_t>(bh) * p.cap;
+    const int key[2] = {key0, key0 + kKeyTile < len ? key0 + kKeyTile : -1};
+    load_key_pair<D>(&kmap, k, k_s, smem_u32(&S->kv_full[0]), krow, len, key);
+    load_key_pair<D>(&vmap, v, v_s, smem_u32(&S->kv_full[1]), krow, len, key);
+    __syncwarp();
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kListKeys, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(kRowTile, D, false, true);
       const uint32_t k_u = smem_u32(k_s), v_u = smem_u32(v_s), q_u = smem_u32(q_s);
-      for (int j = 0; j < nj; ++j) {
+      const bool there = mbar_wait(smem_u32(&S->kv_full[0]), 0, abort) && mbar_wait(smem_u32(&S->kv_full[1]), 0, abort);
+      for (int j = 0; j < nj && there; ++j) {
         if (!mbar_wait(smem_u32(&S->full), j & 1, abort)) break;
         tc_fence_after();
         // over P(j-1), whose product is ahead in the queue
@@ -558,36 +525,103 @@ __global__ void __launch_bounds__(kListThreads, 2)
           umma_f16(tmem, sw128_desc(q_u + (kk >> 2) * kRowTile * 128 + (kk & 3) * 32, 16, 1024),
                    sw128_desc(k_u + (kk >> 2) * kListKeys * 128 + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
         umma_commit(smem_u32(&S->s_full));
-        umma_commit(smem_u32(&S->q_free));
-        if (!mbar_wait(smem_u32(&S->p_full), j & 1, abort)) break;  // and O(j-1) has been read
+        if (!mbar_wait(smem_u32(&S->p_full), j & 1, abort)) break;
+        if (j > 0 && !mbar_wait(smem_u32(&S->o_read), (j - 1) & 1, abort)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kListKeys / 16; ++kk)
-          umma_f16_a_tmem(tmem + 128, tmem + kk * 8, sw128_desc(v_u + kk * 16 * 128, kListKeys * 128, 1024), idesc_o,
-                          kk > 0 ? 1u : 0u);
+          umma_f16_a_tmem(tmem + 128, tmem + kk * 8,
+                          sw128_desc(v_u + kk * 16 * 128, kListKeys * 128, 1024), idesc_o, kk > 0 ? 1u : 0u);
         umma_commit(smem_u32(&S->o_full));
       }
       umma_commit(smem_u32(&S->mma_final));
       mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
+      if (!there) {  // the copies land before the shared memory goes away
+        mbar_wait_cleanup(smem_u32(&S->kv_full[0]), 0);
+        mbar_wait_cleanup(smem_u32(&S->kv_full[1]), 0);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- stores
+    const int r = tid & 127;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128;
+    for (int j = 0; j < nj; ++j) {
+      const int n = min(kRowTile, rows - j * kRowTile);  // rows of the tile
+      float* to = part_o + (part0 + static_cast<size_t>(j) * kRowTile) * D + r * kPartCols;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->o_full), j & 1, abort))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t x[2][32];
+        tmem_ld32(lane_base + c0, x[0]);
+        tmem_ld32(lane_base + c0 + 32, x[1]);
+        tmem_wait_ld_regs(x[0]);
+        tmem_wait_ld_regs(x[1]);
+        if (c0 + 64 == D) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&S->o_read));
+        }
+        if (r < n) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 8)
+            st_global_f32x8(to + (c0 + c) / kPartCols * n * kPartCols + c % kPartCols, x[c >> 5] + (c & 31));
+        }
+      }
     }
   } else {
-    // ---------------------------------------------------------------- softmax
+    // ---------------------------------------------------------------- gather, softmax
     const int r = tid;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const uint64_t sc2 = f2pack(scale_log2, scale_log2);
+    const unsigned first_row = static_cast<unsigned>(row0);
+    auto entry = [&](int j) {  // the query of this thread's row in tile j, -1 behind the last
+      const int f = j * kRowTile + r;
+      return f < rows ? toks[(first_row + f) / p.G] : -1;
+    };
+    auto row_of = [&](int j, int tok) {
+      if (tok < 0) return -1;
+      return (b * p.H + hk * p.G + static_cast<int>((first_row + j * kRowTile + r) % p.G)) * p.Nq + tok;
+    };
+    auto keys_of = [&](int tok) {  // that the row sees
+      return tok < 0 ? 0 : max(0, min(kListKeys, query_limit(p, len, tok) - key0));
+    };
+    auto gather = [&](int row) {  // this warp's rows
+      constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+      const int ch = lane % kChunks, r0 = lane / kChunks;
+#pragma unroll
+      for (int i = 0; i < 32; i += kRows) {
+        const int src = __shfl_sync(0xffffffffu, row, i + r0);
+        cp_async16_or_zero(smem_u32(q_s) + sw128_offset(warp * 32 + i + r0, ch * 8, kRowTile),
+                           q + static_cast<size_t>(src < 0 ? 0 : src) * D + ch * 8, src >= 0);
+      }
+    };
+    auto landed = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&S->full));
+    };
+    int tok = entry(0);
+    gather(row_of(0, tok));
+    int nv = keys_of(tok);
+    tok = entry(1);
+    landed();
     for (int j = 0; j < nj; ++j) {
+      const bool more = j + 1 < nj;
+      const int row = row_of(j + 1, tok), nv_next = keys_of(tok);
+      tok = entry(j + 2);
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->s_full), j & 1, abort))) break;
       tc_fence_after();
-      // they came with the row's tile, which S was computed from
-      const int part = S->part[j & 1][r], nv = S->nv[j & 1][r];
-      const bool whole = __all_sync(0xffffffffu, nv == kListKeys || nv == 0);
+      if (more) gather(row);  // S(j) is done with the rows
+      const bool whole = __all_sync(0xffffffffu, nv == kListKeys);  // no row's own limit falls into these keys
       float m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         float s[32];
         tmem_ld32f(lane_base + h * 32, s);
         tmem_wait_ld_f(s);
-        if (!whole) {  // a row's own limit falls into these keys
+        if (!whole) {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (h * 32 + c >= nv) s[c] = -INFINITY;
@@ -600,8 +634,8 @@ __global__ void __launch_bounds__(kListThreads, 2)
         }
         m = fmaxf(m2[0], m2[1]);
       }
-      m = nv > 0 ? m * scale_log2 : -INFINITY;
-      const float nm = nv > 0 ? -m : -INFINITY;  // a row without keys here: 2^(s - inf) = 0
+      m *= scale_log2;
+      const float nm = m > -INFINITY ? -m : 0.f;  // a row without keys here: P = 2^(-inf - 0) = 0
       const uint64_t nm2 = f2pack(nm, nm);
 #pragma unroll
       for (int h = 0; h < 4; ++h) {  // P(h) goes where S(h / 2) was
@@ -633,22 +667,11 @@ __global__ void __launch_bounds__(kListThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&S->p_full));
-      if (part >= 0) part_ml[part] = make_float2(m, l);
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&S->o_full), j & 1, abort))) break;
-      tc_fence_after();
-      float* to = part_o + static_cast<size_t>(part < 0 ? 0 : part) * D;
-#pragma unroll
-      for (int c0 = 0; c0 < D / 32; ++c0) {
-        uint32_t x[32];
-        tmem_ld32(lane_base + 128 + c0 * 32, x);
-        tmem_wait_ld_regs(x);
-        if (part >= 0) {
-#pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) st_global_f32x8(to + c0 * 32 + c8 * 8, x + c8 * 8);
-        }
-      }
-      tc_fence_before();  // O is free with p_full of the next tile
+      if (j * kRowTile + r < rows) part_ml[part0 + static_cast<size_t>(j) * kRowTile + r] = make_float2(m, l);
+      if (more) landed();
+      nv = nv_next;
     }
+    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -660,51 +683,68 @@ __global__ void __launch_bounds__(kListThreads, 2)
 }
 
 // One warp per row of [B*H*Nq, D], a lane per part: o = sum of the row's parts,
-// each at its own maximum. The parts that exist are those of the list's walk:
-// the counted slots' key tiles below the row's limit.
+// each at its own maximum.
 template <int D>
 __global__ void __launch_bounds__(256)
     block_parts_kernel(BlockDims p, const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths,
-                       const float* __restrict__ part_o, const float2* __restrict__ part_ml, uint16_t* __restrict__ o,
-                       float* __restrict__ lse, int* __restrict__ err) {
+                       const int32_t* __restrict__ total, const int32_t* __restrict__ start,
+                       const int32_t* __restrict__ places, const float* __restrict__ part_o,
+                       const float2* __restrict__ part_ml, uint16_t* __restrict__ o, float* __restrict__ lse,
+                       int* __restrict__ err) {
   const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= static_cast<size_t>(p.B) * p.H * p.Nq) return;
   constexpr int kE = D / 32, kDeep = 8;
   const int t = static_cast<int>(row % p.Nq), head = static_cast<int>(row / p.Nq);
-  const int b = head / p.H, hk = (head - b * p.H) / p.G;
-  const int lim = query_limit(p, seq_len(p, lengths, b), t);
+  const int b = head / p.H, hk = (head - b * p.H) / p.G, g = head % p.G, bh = b * p.Hkv + hk;
+  const size_t mine = (static_cast<size_t>(bh) * p.Nq + t) * p.n_sel;
+  const int parts = p.n_sel * p.nsub, slot = lane / p.nsub, c = lane % p.nsub;
+  // a slot with no place does not count, or lies behind the row's limit
+  const int given = lane < p.n_sel ? idx[mine + lane] : -1;
+  const int place = lane < parts ? places[mine + slot] : -1;
   bool bad = false;
-  const size_t mine = (static_cast<size_t>(b) * p.Hkv + hk) * p.Nq + t;
-  const int held = counted_slot(lane < p.n_sel ? idx[mine * p.n_sel + lane] : -1, p.nb, &bad);
+  counted_slot(given, p.nb, &bad);
   if (bad && lane == 0) report_error(err, kErrBadPlan);
-  const int parts = p.n_sel * p.nsub;
-  const int blk = __shfl_sync(0xffffffffu, held, (lane / p.nsub) & 31);
-  const bool there = lane < parts && blk >= 0 && (blk * p.nsub + lane % p.nsub) * kListKeys < lim;
-  const float2 ml = there ? part_ml[row * parts + lane] : make_float2(-INFINITY, 0.f);
+  const int blk = __shfl_sync(0xffffffffu, given, slot & 31);
+  float2 ml = make_float2(-INFINITY, 0.f);
+  size_t at = 0;   // of the part's first columns
+  int stride = 0;  // from these to the next
+  if (place >= 0) {
+    const size_t cell = static_cast<size_t>(bh) * p.nb + blk;
+    const int first = start[cell], rows = total[cell] * p.G, r = (place - first) * p.G + g;
+    const int tile = r & ~(kRowTile - 1), n = min(kRowTile, rows - tile);
+    const size_t tile0 = list_part(p, bh, first, rows, c) + tile;
+    ml = part_ml[tile0 + (r - tile)];
+    at = tile0 * D + (r - tile) * kPartCols;
+    stride = n * kPartCols;
+  }
+  const bool there = ml.y > 0.f || ml.y != ml.y;  // 128 keys behind the row's limit give nothing
   float top = ml.x;
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
   const float f = there ? ex2_approx(ml.x - top) : 0.f;
-  float l = ml.y * f;
+  float l = there ? ml.y * f : 0.f;
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
   float acc[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
-  const float* src = part_o + row * parts * D + lane * kE;
   const unsigned all = __ballot_sync(0xffffffffu, there);
+  const int c0 = lane * kE / kPartCols, in = lane * kE % kPartCols;  // this lane's columns
   for (int i0 = 0; i0 < parts; i0 += kDeep) {
     float x[kDeep][kE];
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
+      const size_t from = __shfl_sync(0xffffffffu, at, (i0 + i) & 31);
+      const int by = __shfl_sync(0xffffffffu, stride, (i0 + i) & 31);
+      const float* src = part_o + from + static_cast<size_t>(c0 * by + in);
+      const bool on = i0 + i < parts && ((all >> ((i0 + i) & 31)) & 1u);
 #pragma unroll
-      for (int e = 0; e < kE; e += 2) {
-        float2 y = make_float2(0.f, 0.f);
-        if (i0 + i < parts && ((all >> (i0 + i)) & 1u))
-          y = *reinterpret_cast<const float2*>(src + static_cast<size_t>(i0 + i) * D + e);
-        x[i][e] = y.x;
-        x[i][e + 1] = y.y;
+      for (int e = 0; e < kE; ++e) x[i][e] = 0.f;
+      if (kE == 4) {
+        if (on) *reinterpret_cast<float4*>(x[i]) = *reinterpret_cast<const float4*>(src);
+      } else {
+        if (on) *reinterpret_cast<float2*>(x[i]) = *reinterpret_cast<const float2*>(src);
       }
     }
 #pragma unroll
@@ -732,7 +772,7 @@ __global__ void __launch_bounds__(256)
 // and launches cost some 40 us: small calls keep to the union. The parts' place
 // stays below 4 GB.
 inline bool by_blocks(const BlockDims& p) {
-  if (p.block % kListKeys || p.n_sel * (p.block / kListKeys) > 32 || p.Nq >= 1 << 24) return false;
+  if (p.block % kListKeys || p.n_sel * (p.block / kListKeys) > 32) return false;
   const long long parts = static_cast<long long>(p.B) * p.H * p.Nq * p.n_sel * (p.block / kListKeys);
   if (parts < 1 << 18 || parts > 1 << 23) return false;
   long long seen = p.nb;  // blocks before the middle query
@@ -768,7 +808,7 @@ struct FwdPlan {
   int shares;
   int ktiles, chunk, nchunk, piece;
   long long max_items;
-  int32_t *hist, *total, *start, *list, *counts;
+  int32_t *hist, *total, *start, *list, *places, *counts;
   int4* items;
   float* part_o;
   float2* part_ml;
@@ -793,6 +833,7 @@ FwdPlan fwd_plan(const BlockDims& p, int d, void* ws) {
     f.total = c.take<int32_t>(BHk * p.nb);
     f.start = c.take<int32_t>(BHk * p.nb);
     f.list = c.take<int32_t>(BHk * p.Nq * p.n_sel);
+    f.places = c.take<int32_t>(BHk * p.Nq * p.n_sel);
     f.counts = c.take<int32_t>(2);
     f.items = c.take<int4>(static_cast<size_t>(f.max_items));
   }
@@ -808,26 +849,32 @@ svoo_status launch_block_lists(const BlockDims& p, const FwdPlan& f, const uint1
                                uint16_t* o, float* lse, int32_t* dev_err, cudaStream_t st) {
   const BlockDims lp = list_dims(p);
   const int BHk = p.B * p.Hkv;
+  CUtensorMap km, vm;
+  const uint64_t krows = static_cast<uint64_t>(BHk) * p.cap;
+  if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
+      encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
+    return SVOO_ERR_CUDA;
   const size_t smem = 1024 + list_tile_bytes<D>() + sizeof(ListSmem), cnt = static_cast<size_t>(p.nb) * 4;
   if (cudaFuncSetAttribute(block_list_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess ||
       cudaFuncSetAttribute(sel_walk_kernel<kSelCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
           cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelSlots>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+      cudaFuncSetAttribute(sel_walk_kernel<kSelPlaces>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
           cudaSuccess)
     return SVOO_ERR_CUDA;
   sel_walk_kernel<kSelCount><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
-                                                                   nullptr, nullptr);
+                                                                   nullptr, nullptr, nullptr);
   sel_scan_kernel<<<dim3((p.nb + 31) / 32, BHk), 256, 0, st>>>(lp, f.nchunk, f.hist, f.total);
   sel_items_kernel<<<1, 1024, 0, st>>>(lp, f.ktiles, f.piece, f.total, f.start, f.items, f.counts);
-  sel_walk_kernel<kSelSlots><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
-                                                                   f.start, f.list);
+  sel_walk_kernel<kSelPlaces><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
+                                                                    f.start, f.list, f.places);
   block_list_kernel<D><<<static_cast<unsigned>(f.max_items), kListThreads, smem, st>>>(
-      lp, f.ktiles, f.piece, q, k, v, lengths, f.total, f.start, f.list, f.items, f.counts, scale_log2, f.part_o,
+      km, vm, lp, f.ktiles, f.piece, q, k, v, lengths, f.total, f.start, f.list, f.items, f.counts, scale_log2, f.part_o,
       f.part_ml, dev_err);
   const size_t rows = static_cast<size_t>(p.B) * p.H * p.Nq;
-  block_parts_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(lp, idx, lengths, f.part_o, f.part_ml, o,
-                                                                               lse, dev_err);
+  block_parts_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(lp, idx, lengths, f.total, f.start,
+                                                                               f.places, f.part_o, f.part_ml, o, lse,
+                                                                               dev_err);
   return launch_status();
 }
 

@@ -785,19 +785,19 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
                            static_cast<int>(dkv_smem)) != cudaSuccess ||
       cudaFuncSetAttribute(sel_walk_kernel<kSelCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
           cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelQueries>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
+      cudaFuncSetAttribute(sel_walk_kernel<kSelList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
           cudaSuccess)
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (p.Nq > 0) {
     sel_walk_kernel<kSelCount><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
-                                                                      nullptr, nullptr);
+                                                                      nullptr, nullptr, nullptr);
   }
   sel_scan_kernel<<<dim3((p.nb + 31) / 32, BHk), 256, 0, st>>>(p, g.nchunk, g.hist, g.total);
   sel_items_kernel<<<1, 1024, 0, st>>>(p, g.ktiles, g.piece, g.total, g.start, g.items, g.counts);
   if (p.Nq > 0) {
-    sel_walk_kernel<kSelQueries><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
-                                                                     g.start, g.list);
+    sel_walk_kernel<kSelList><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
+                                                                     g.start, g.list, nullptr);
     block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
         qm, gm, om, km, vm, p, static_cast<int>(union_cap(p)), kp, vp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
   }

@@ -14,16 +14,15 @@ namespace {
 // A warp takes `chunk` queries of one (sequence, key head) in order, 32 at a
 // time and slot by slot; lanes with the same block are ranked by lane. Both
 // passes walk the same way, so a place depends on the selection alone.
-// kSelCount: the chunk's count per block; kSelQueries, kSelSlots: the lists,
-// an entry the query, or the query and in the upper 8 bits the slot it names the
-// block in.
-enum SelPass { kSelCount, kSelQueries, kSelSlots };
+// kSelCount: the chunk's count per block; kSelList: the lists; kSelPlaces: and
+// for every slot its place in them (-1: in none).
+enum SelPass { kSelCount, kSelList, kSelPlaces };
 
 template <SelPass kPass>
 __global__ void __launch_bounds__(32)
     sel_walk_kernel(BlockDims p, const int32_t* __restrict__ idx, const int32_t* __restrict__ lengths, int chunk,
                     int nchunk, int32_t* __restrict__ hist, const int32_t* __restrict__ start,
-                    int32_t* __restrict__ list) {
+                    int32_t* __restrict__ list, int32_t* __restrict__ places) {
   extern __shared__ int cnt[];
   const int lane = threadIdx.x, c = blockIdx.x, bh = blockIdx.y;
   const int len = seq_len(p, lengths, bh / p.Hkv);
@@ -41,14 +40,15 @@ __global__ void __launch_bounds__(32)
       const int blk = go ? mine[s] : -1;
       go = go && blk > prev && blk < p.nb;
       prev = blk;
-      if (!__any_sync(0xffffffffu, go)) break;
+      if (kPass != kSelPlaces && !__any_sync(0xffffffffu, go)) break;
       const bool take = go && blk * p.block < lim;
       const unsigned same = __match_any_sync(0xffffffffu, take ? blk : -1 - lane);
-      if (take) {
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        if (kPass != kSelCount)
-          list[static_cast<size_t>(bh) * p.Nq * p.n_sel + cnt[blk] + rank] = kPass == kSelSlots ? t | s << 24 : t;
+      int place = -1;
+      if (kPass != kSelCount && take) {
+        place = cnt[blk] + __popc(same & ((1u << lane) - 1u));
+        list[static_cast<size_t>(bh) * p.Nq * p.n_sel + place] = t;
       }
+      if (kPass == kSelPlaces && t < t1) places[(static_cast<size_t>(bh) * p.Nq + t) * p.n_sel + s] = place;
       __syncwarp();
       if (take && (same & ((1u << lane) - 1u)) == 0) cnt[blk] += __popc(same);
       __syncwarp();
