@@ -765,12 +765,18 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ host side
 
 // Whether a call goes by key blocks. The union of a row tile's selections costs
-// about 0.9 ns per row and block of 128 keys (d = 128) in it, the other way
-// about 3 ns per row and *selected* block, so the union has to be five times a
-// selection and more; and it is near that only where the tile holds queries
-// enough to name each block four times over (neighbouring queries agree). Lists
-// and launches cost some 40 us: small calls keep to the union. The parts' place
-// stays below 4 GB.
+// time by its size, this way by the selections': it pays from unions of about
+// four selections on. A union is as large as that where the queries see more
+// than four times the blocks that they select, and the tile's queries are enough
+// to name each of them eight times over (neighbouring queries agree). Measured
+// (us, union / this, d = 128; neighbours that agree, then independent queries):
+//   12 heads, 16380 queries, 16 of 128 blocks   1384 / 840, 1553 / 851
+//    8 of 128   846 / 489, 1511 / 480      24 of 128   1495 / 1209, 1554 / 1224
+//   causal      892 / 800,  939 / 806      32760 queries, 16 of 256   3058 / 1621
+//   16 of 64 blocks, 8192 queries  430 / 452 (not taken: four selections)
+//   two heads a group  1005 / 1031, 1574 / 1046   four (not taken)  681 / 1555
+// d = 64 (half the parts' bytes): 1430 / 562. Lists and launches cost some 40 us:
+// small calls keep to the union. The parts' place stays below 4.3 GB.
 inline bool by_blocks(const BlockDims& p) {
   if (p.block % kListKeys || p.n_sel * (p.block / kListKeys) > 32) return false;
   const long long parts = static_cast<long long>(p.B) * p.H * p.Nq * p.n_sel * (p.block / kListKeys);
@@ -780,7 +786,7 @@ inline bool by_blocks(const BlockDims& p) {
     const long long middle = (p.q_start >= 0 ? p.q_start : p.Nk - p.Nq) + p.Nq / 2;
     if (middle / p.block + 1 < seen) seen = middle / p.block + 1;
   }
-  return seen >= 5LL * p.n_sel && static_cast<long long>(p.tpt) * p.n_sel >= 4 * seen;
+  return seen > 4LL * p.n_sel && static_cast<long long>(p.tpt) * p.n_sel >= 8 * seen;
 }
 
 // Shares of a row tile's list: as many as bring two CTAs to every SM, while a

@@ -36,7 +36,7 @@ CASES = [
     # B, H, Hkv, Nq, Nk, d, block, n_sel, sink, local, causal, lengths, q_start
     (1, 64, 64, 2048, 2048, 64, 128, 3, 1, 0, False, None, None),
     (2, 32, 32, 2001, 2001, 128, 128, 3, 1, 0, False, [2001, 1930], None),
-    (1, 64, 32, 1900, 4111, 64, 128, 3, 0, 1, True, None, None),
+    (1, 64, 32, 1900, 3911, 64, 128, 3, 0, 1, True, None, None),
     (2, 48, 48, 1000, 4999, 128, 256, 2, 1, 1, True, [4999, 700], -1),
     (3, 40, 40, 1100, 1300, 64, 128, 2, 0, 0, False, [0, 1, 1299], 0),
 ]
