@@ -699,7 +699,9 @@ __global__ void __launch_bounds__(256)
   const int b = head / p.H, hk = (head - b * p.H) / p.G, g = head % p.G, bh = b * p.Hkv + hk;
   const size_t mine = (static_cast<size_t>(bh) * p.Nq + t) * p.n_sel;
   const int parts = p.n_sel * p.nsub, slot = lane / p.nsub, c = lane % p.nsub;
-  // a slot with no place does not count, or lies behind the row's limit
+  // a slot with no place does not count, or lies behind the row's limit, as its
+  // later keys may: nobody wrote a part for keys behind the last
+  const int lim = query_limit(p, seq_len(p, lengths, b), t);
   const int given = lane < p.n_sel ? idx[mine + lane] : -1;
   const int place = lane < parts ? places[mine + slot] : -1;
   bool bad = false;
@@ -709,7 +711,8 @@ __global__ void __launch_bounds__(256)
   float2 ml = make_float2(-INFINITY, 0.f);
   size_t at = 0;   // of the part's first columns
   int stride = 0;  // from these to the next
-  if (place >= 0) {
+  const bool there = place >= 0 && (blk * p.nsub + c) * kListKeys < lim;
+  if (there) {
     const size_t cell = static_cast<size_t>(bh) * p.nb + blk;
     const int first = start[cell], rows = total[cell] * p.G, r = (place - first) * p.G + g;
     const int tile = r & ~(kRowTile - 1), n = min(kRowTile, rows - tile);
@@ -718,12 +721,11 @@ __global__ void __launch_bounds__(256)
     at = tile0 * D + (r - tile) * kPartCols;
     stride = n * kPartCols;
   }
-  const bool there = ml.y > 0.f || ml.y != ml.y;  // 128 keys behind the row's limit give nothing
   float top = ml.x;
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
   const float f = there ? ex2_approx(ml.x - top) : 0.f;
-  float l = there ? ml.y * f : 0.f;
+  float l = ml.y * f;
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
   float acc[kE];

@@ -38,6 +38,8 @@ CASES = [
     (2, 32, 32, 2001, 2001, 128, 128, 3, 1, 0, False, [2001, 1930], None),
     (1, 64, 32, 1900, 3911, 64, 128, 3, 0, 1, True, None, None),
     (2, 48, 48, 1000, 4999, 128, 256, 2, 1, 1, True, [4999, 700], -1),
+    (1, 48, 48, 2048, 2600, 128, 256, 2, 1, 0, False, None, None),   # the last block's second half holds no key
+    (1, 24, 24, 2048, 5700, 64, 512, 2, 0, 1, True, None, None),
     (3, 40, 40, 1100, 1300, 64, 128, 2, 0, 0, False, [0, 1, 1299], 0),
 ]
 
@@ -55,7 +57,12 @@ def test_lists_against_fp64(case):
     pool = svoo.block_pool(k, cfg, ln)
     idx = svoo.block_select(q, pool, cfg, Nk, ln, q_start)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    o, lse = svoo.block_attn(q, k, v, idx, cfg, ln, q_start, dev_err=err)
+    # a workspace that held something else: no part is read that was not written
+    size = svoo._ws_bytes("svoo_block_attn_workspace_size", B, H, Hkv, Nq, Nk, Nk, d, block, n_sel, sink, local,
+                          int(causal), Nk - Nq if q_start is None else q_start)
+    assert size >= B * H * Nq * n_sel * block // 128 * d * 4   # the parts' place: the call goes by lists
+    ws = torch.full((size,), 0x41, dtype=torch.uint8, device="cuda")
+    o, lse = svoo.block_attn(q, k, v, idx, cfg, ln, q_start, workspace=ws, dev_err=err)
     again, lse2 = svoo.block_attn(q, k, v, idx, cfg, ln, q_start)
     assert torch.equal(o, again) and torch.equal(lse, lse2) and int(err) == 0
     for b in range(B):
