@@ -13,7 +13,9 @@
 //                     heads are far from filling a tcgen05 tile, and the kernel
 //                     is bound by the cache's bytes), each with its own running
 //                     maximum, sum and output, joined once at the end.
-// cache_join_kernel   joins the runs, and turns the kept scores into weights.
+//                     Up to eight runs are a cluster and join through each
+//                     other's shared memory.
+// cache_join_kernel   joins more runs, and turns the kept scores into weights.
 // evict_select_kernel the slots that stay, one CTA per (sequence, key head).
 // evict_move_kernel   moves kept rows from behind `keep` into the holes.
 #include "blocks.cuh"
@@ -26,11 +28,13 @@ constexpr int kCacheWarps = 4;                        // 16 slots of a tile each
 constexpr int kCacheThreads = 32 * (kCacheWarps + 1);  // and the producer
 constexpr int kCacheStages = 3;
 constexpr int kHeadRows = 16;  // heads of one CTA
+constexpr int kMaxJoined = 8;  // CTAs of a cluster
 
 struct CacheSmem {
   uint64_t full[kCacheStages], empty[kCacheStages];
   int abort;
   float m[kCacheWarps][kHeadRows], l[kCacheWarps][kHeadRows];
+  float2 ml[kHeadRows];  // of the CTA, for its cluster
 };
 
 template <int D>
@@ -59,14 +63,30 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// what `at` (shared memory) holds in CTA `rank` of the cluster
+__device__ __forceinline__ float2 cluster_read2(uint32_t at, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // Grid (runs, B * Hkv, ceil(G / 16)). Partial results of run x: o (fp32
-// [runs][B*H][D]) and (m in log2 units, l) per head; with one run the output
-// itself. scores (may be NULL): fp32 [B*H][cap], scale * q.k * log2 e.
+// [runs][B*H][D]) and (m in log2 units, l) per head; with one run, or where the
+// runs are a cluster (joined), the output itself. scores (may be NULL): fp32 [B*H][cap], scale * q.k * log2 e.
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads)
     cache_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, BlockDims p,
                       const uint16_t* __restrict__ q, const int32_t* __restrict__ idx,
-                      const int32_t* __restrict__ lengths, float scale_log2, float* __restrict__ scores,
+                      const int32_t* __restrict__ lengths, float scale_log2, int joined, float* __restrict__ scores,
                       float* __restrict__ part_o, float2* __restrict__ part_ml, uint16_t* __restrict__ o,
                       float* __restrict__ lse, int* __restrict__ err) {
   constexpr int kSub = D / 64;
@@ -79,7 +99,9 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int h0 = blockIdx.z * kHeadRows, heads = min(kHeadRows, p.G - h0);
   const int len = seq_len(p, lengths, b);
   const int32_t* slots = idx ? idx + static_cast<size_t>(bh) * p.n_sel : nullptr;
-  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  // a CTA of a cluster stays to its end: the others read its shared memory
+  const bool skip = __syncthreads_or(timed_out_before(err) ? 1 : 0) != 0;
+  if (skip && !joined) return;
   if (tid == 0) {
     S->abort = 0;
     for (int s = 0; s < kCacheStages; ++s) {
@@ -95,6 +117,7 @@ __global__ void __launch_bounds__(kCacheThreads)
     tiles = walk_slots(slots, p.n_sel, p.nb, &bad, [](int) {}) * p.nsub;
     if (bad && tid == 0 && blockIdx.x == 0) report_error(err, kErrBadPlan);
   }
+  if (skip) tiles = 0;
   const int per = (tiles + gridDim.x - 1) / gridDim.x;
   const int i0 = min(tiles, static_cast<int>(blockIdx.x) * per), i1 = min(tiles, i0 + per);
   auto tile_key = [&](int i) { return (slots ? slots[i / p.nsub] * p.nsub + i % p.nsub : i) * kKeyTile; };
@@ -271,8 +294,11 @@ __global__ void __launch_bounds__(kCacheThreads)
     }
   }
   __syncthreads();
-  if (failed) return;
-  for (int i = tid; i < heads * (D / 2); i += kCacheThreads) {
+  if (failed && !joined) return;
+  if (failed)
+    for (int h = tid; h < heads; h += kCacheThreads) S->ml[h] = make_float2(-INFINITY, 0.f);
+  for (int i = tid; i < heads * (D / 2) && !failed; i += kCacheThreads) {
+    // (one thread has all of a column's four values)
     const int h = i / (D / 2), c = (i - h * (D / 2)) * 2;
     float mm = -INFINITY;
 #pragma unroll
@@ -291,12 +317,45 @@ __global__ void __launch_bounds__(kCacheThreads)
       const float inv = ll > 0.f ? 1.f / ll : 0.f;
       *reinterpret_cast<uint32_t*>(o + row * D + c) = pack_bf16x2(x * inv, y * inv);
       if (c == 0) lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    } else if (joined) {
+      *reinterpret_cast<float2*>(os + h * D + c) = make_float2(x, y);
+      if (c == 0) S->ml[h] = make_float2(mm, ll);
     } else {
       const size_t at = static_cast<size_t>(blockIdx.x) * p.B * p.H + row;
       *reinterpret_cast<float2*>(part_o + at * D + c) = make_float2(x, y);
       if (c == 0) part_ml[at] = make_float2(mm, ll);
     }
   }
+  if (!joined) return;
+  // a share of the columns each, over all CTAs of the cluster
+  cluster_sync();
+  const int runs = gridDim.x;
+  for (int i = blockIdx.x * kCacheThreads + tid; i < heads * (D / 2); i += runs * kCacheThreads) {
+    const int h = i / (D / 2), c = (i - h * (D / 2)) * 2;
+    float2 ml[kMaxJoined], v[kMaxJoined];
+    float mm = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kMaxJoined; ++x) {
+      ml[x] = x < runs ? cluster_read2(smem_u32(&S->ml[h]), x) : make_float2(-INFINITY, 0.f);
+      v[x] = x < runs ? cluster_read2(smem_u32(os + h * D + c), x) : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int x = 0; x < kMaxJoined; ++x) mm = fmaxf(mm, ml[x].x);
+    float ll = 0.f, a = 0.f, e = 0.f;
+#pragma unroll
+    for (int x = 0; x < kMaxJoined; ++x) {
+      if (ml[x].x == -INFINITY) continue;  // an empty run's columns may be anything
+      const float f = ex2_approx(ml[x].x - mm);
+      ll = fmaf(ml[x].y, f, ll);
+      a = fmaf(v[x].x, f, a);
+      e = fmaf(v[x].y, f, e);
+    }
+    const size_t row = static_cast<size_t>(b) * p.H + hk * p.G + h0 + h;
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    *reinterpret_cast<uint32_t*>(o + row * D + c) = pack_bf16x2(a * inv, e * inv);
+    if (c == 0) lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  }
+  cluster_sync();  // nobody leaves while its shared memory is read
 }
 
 // Grid (1 + chunks of 1024 slots where weights are kept, B * Hkv). Block 0
@@ -392,19 +451,35 @@ inline int cache_runs(const BlockDims& p, bool selected) {
   return runs < 1 ? 1 : static_cast<int>(runs);
 }
 
+// Up to eight runs are a cluster where all CTAs run at once, and need no kernel
+// (5 us and its launch) to join them. (In several waves a cluster waits for its
+// slowest run with all its places: 48 sequences, 40/8 heads, 32 blocks of 64:
+// 88 us against 75 + 8.) More runs become eight where that leaves at most four
+// tiles to a run: a tile takes a run about 1 us.
+inline int cache_runs(const BlockDims& p, bool selected, bool* joined) {
+  const int tiles = selected ? p.n_sel * p.nsub : (p.Nk + kKeyTile - 1) / kKeyTile;
+  int runs = cache_runs(p, selected);
+  if (runs > kMaxJoined && tiles <= 4 * kMaxJoined) runs = kMaxJoined;
+  const long long ctas = static_cast<long long>(runs) * p.B * p.Hkv * ((p.G + kHeadRows - 1) / kHeadRows);
+  *joined = runs > 1 && runs <= kMaxJoined && ctas <= 2 * 148;
+  return runs;
+}
+
 struct CachePlan {
   int runs;
+  bool joined;
   float *part_o, *scores;
   float2* part_ml;
   size_t bytes;
 };
 CachePlan cache_plan(const BlockDims& p, int d, bool selected, bool weights, void* ws) {
   CachePlan c;
-  c.runs = cache_runs(p, selected);
+  c.runs = cache_runs(p, selected, &c.joined);
   Carver w(ws);
   const size_t rows = static_cast<size_t>(p.B) * p.H;
-  c.part_o = w.take<float>(c.runs > 1 ? c.runs * rows * d : 0);
-  c.part_ml = w.take<float2>(c.runs > 1 ? c.runs * rows : 0);
+  const size_t parts = c.runs > 1 && !c.joined ? c.runs * rows : 0;
+  c.part_o = w.take<float>(parts * d);
+  c.part_ml = w.take<float2>(parts);
   c.scores = w.take<float>(weights ? rows * p.cap : 0);
   c.bytes = (w.used + 255) / 256 * 256;
   return c;
@@ -425,16 +500,29 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  cache_attn_kernel<D><<<dim3(c.runs, p.B * p.Hkv, (p.G + kHeadRows - 1) / kHeadRows), kCacheThreads, smem, st>>>(
-      km, vm, p, static_cast<const uint16_t*>(q), idx, lengths, scale_log2, weight ? c.scores : nullptr, c.part_o,
-      c.part_ml, static_cast<uint16_t*>(o), lse, dev_err);
-  const size_t factors = c.runs > 1 ? static_cast<size_t>(p.G) * c.runs * 4 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.runs, p.B * p.Hkv, (p.G + kHeadRows - 1) / kHeadRows);
+  cfg.blockDim = dim3(kCacheThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = c.runs;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = c.joined ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, cache_attn_kernel<D>, km, vm, p, static_cast<const uint16_t*>(q), idx, lengths,
+                         scale_log2, c.joined ? 1 : 0, weight ? c.scores : nullptr, c.part_o, c.part_ml,
+                         static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err)) != cudaSuccess)
+    return SVOO_ERR_CUDA;
+  const int runs = c.joined ? 1 : c.runs;  // still to join
+  const size_t factors = runs > 1 ? static_cast<size_t>(p.G) * runs * 4 : 0;
   if (factors > 48 * 1024 && cudaFuncSetAttribute(cache_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   static_cast<int>(factors)) != cudaSuccess)
     return SVOO_ERR_CUDA;
-  if (c.runs > 1 || weight)
+  if (runs > 1 || weight)
     cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, factors, st>>>(
-        p, c.runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight);
+        p, runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight);
   return launch_status();
 }
 
