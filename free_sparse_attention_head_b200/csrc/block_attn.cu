@@ -13,7 +13,7 @@
 // worst case the union is what dense attention would read.
 //
 // Where there are few row tiles, a tile's list is shared out to several CTAs
-// (grid.z), whose parts block_join_kernel puts together.
+// (grid.z), a cluster that puts its parts together from its shared memories.
 //
 // Two CTAs share an SM (256 tensor-memory columns and half of the shared
 // memory each), so one's softmax runs beside the other's products.
@@ -29,7 +29,7 @@ namespace svoo {
 namespace {
 
 constexpr int kFwdThreads = 192;
-constexpr int kMaxShares = 16;  // CTAs that share a row tile's list
+constexpr int kMaxShares = 8;  // CTAs that share a row tile's list: a cluster
 // The running maximum stays until it is outgrown by 2^32: P (bf16, fp32's range)
 // and its sums lose nothing by being large, at most 2^52 here, and the rescaling
 // that a smaller bound (2^8) asked for stalled most steps on the last product.
@@ -43,11 +43,18 @@ struct FwdSmem {
   int max_limit;
   int tiles;                 // of the list
   int limit[kRowTile];  // per query of the tile
+  float2 ml[kRowTile];  // of this share's rows
 };
 
 template <int D>
 constexpr size_t fwd_tile_bytes() {
   return static_cast<size_t>(kRowTile) * D * 2 + 4 * static_cast<size_t>(kKeyTile) * D * 2;
+}
+
+// byte of the c4-th 16 bytes of row r of a share's part
+template <int D>
+__device__ __forceinline__ uint32_t part_at(int r, int c4) {
+  return r * (D * 4) + ((c4 ^ (r & 7)) << 4);
 }
 
 template <int D>
@@ -56,8 +63,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                       const __grid_constant__ CUtensorMap vmap, BlockDims p, int cap,
                       const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const int32_t* __restrict__ idx,
                       const int32_t* __restrict__ lengths, float scale_log2, uint16_t* __restrict__ o,
-                      float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
-                      int* __restrict__ err) {
+                      float* __restrict__ lse, int* __restrict__ err) {
   constexpr int kSub = D / 64;
   constexpr int kKvBytes = kKeyTile * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -69,7 +75,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   TileList tl = tile_list(p, cap, S + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
+  const int shares = gridDim.z;
+  // a CTA of a cluster stays to its end: the others read its shared memory
+  const bool skip = __syncthreads_or(timed_out_before(err) ? 1 : 0) != 0;
+  if (skip && shares == 1) return;
   const int b = blockIdx.y / p.Hkv, hk = blockIdx.y - b * p.Hkv;
   const int t0 = blockIdx.x * p.tpt;
   const int nt = min(p.tpt, p.Nq - t0);
@@ -98,8 +107,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tmem_relinquish();
   }
   int tiles = make_tile_list<kFwdThreads>(p, tl, slots, t0, nt, len, S->limit, &S->max_limit, &S->tiles, err);
-  if (gridDim.z > 1) {  // this CTA's share of the list
-    const int per = (tiles + gridDim.z - 1) / gridDim.z, first = min(tiles, static_cast<int>(blockIdx.z) * per);
+  if (skip) tiles = 0;
+  if (shares > 1) {  // this CTA's share of the list
+    const int per = (tiles + shares - 1) / shares, first = min(tiles, static_cast<int>(blockIdx.z) * per);
     tl.list += first;
     tiles = min(per, tiles - first);
   }
@@ -297,12 +307,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     // ---------------------------------------------------------------- epilogue
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S->mma_final), 0, abort));
+    if (!ok) l = 0.f;
+    if (shares > 1) S->ml[r] = make_float2(l > 0.f ? m : -INFINITY, l);
     if (ok) {
       tc_fence_after();
       const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const bool part = gridDim.z > 1;
-      const size_t at = blockIdx.z * (static_cast<size_t>(p.B) * p.H * p.Nq) + row;  // of a part
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t x[32];
@@ -311,11 +321,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_wait_ld_regs(x);
         }
         if (!live) continue;
-        if (part) {
+        if (shares > 1) {  // where keys and values were; 16-byte pieces of a row in an order that spreads the banks
           if (l > 0.f) {
 #pragma unroll
             for (int c4 = 0; c4 < 8; ++c4)
-              *reinterpret_cast<uint4*>(part_o + at * D + c0 * 32 + c4 * 4) =
+              *reinterpret_cast<uint4*>(k_s + part_at<D>(r, c0 * 8 + c4)) =
                   make_uint4(x[c4 * 4], x[c4 * 4 + 1], x[c4 * 4 + 2], x[c4 * 4 + 3]);
           }
           continue;
@@ -332,8 +342,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           reinterpret_cast<uint4*>(o + row * D + c0 * 32)[c8] = pk;
         }
       }
-      if (live && part) part_ml[at] = make_float2(m, l);
-      if (live && !part) lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (live && shares == 1) lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
   tc_fence_before();
@@ -349,49 +358,44 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     __syncthreads();
   }
+  if (shares > 1) {
+    // o = sum of the shares' parts, each at its own maximum; a share of the pieces each
+    cluster_sync();
+    for (int i = blockIdx.z * kFwdThreads + tid; i < nt * p.G * (D / 4); i += shares * kFwdThreads) {
+      const int r = i / (D / 4), c4 = i - r * (D / 4), ti = (r * p.inv_g) >> 16, g = r - ti * p.G;
+      float2 ml[kMaxShares];
+      float4 x[kMaxShares];
+      float top = -INFINITY;
+#pragma unroll
+      for (int z = 0; z < kMaxShares; ++z) {
+        ml[z] = z < shares ? cluster_read2(smem_u32(&S->ml[r]), z) : make_float2(-INFINITY, 0.f);
+        if (z < shares) x[z] = cluster_read4(smem_u32(k_s + part_at<D>(r, c4)), z);
+      }
+#pragma unroll
+      for (int z = 0; z < kMaxShares; ++z) top = fmaxf(top, ml[z].x);
+      float l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int z = 0; z < kMaxShares; ++z) {
+        if (!(ml[z].y > 0.f)) continue;  // the row had nothing there: its part was not written
+        const float f = ex2_approx(ml[z].x - top);
+        l = fmaf(ml[z].y, f, l);
+        a[0] = fmaf(x[z].x, f, a[0]);
+        a[1] = fmaf(x[z].y, f, a[1]);
+        a[2] = fmaf(x[z].z, f, a[2]);
+        a[3] = fmaf(x[z].w, f, a[3]);
+      }
+      const size_t row = (static_cast<size_t>(b) * p.H + hk * p.G + g) * p.Nq + t0 + ti;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(o + row * D + c4 * 4) =
+          make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
+      if (c4 == 0) lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+    cluster_sync();  // nobody leaves while its shared memory is read
+  }
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
-}
-
-// One warp per row of [B*H*Nq, D]: o = sum of the shares' parts, each at its own
-// maximum. A share that the row had nothing in (l = 0) wrote no part.
-template <int D>
-__global__ void __launch_bounds__(256)
-    block_join_kernel(size_t rows, int shares, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                      uint16_t* __restrict__ o, float* __restrict__ lse) {
-  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  constexpr int kE = D / 32;
-  float2 ml[kMaxShares];
-  float top = -INFINITY, l = 0.f, acc[kE];
-#pragma unroll
-  for (int z = 0; z < kMaxShares; ++z) {
-    ml[z] = z < shares ? part_ml[z * rows + row] : make_float2(-INFINITY, 0.f);
-    if (ml[z].y > 0.f) top = fmaxf(top, ml[z].x);
-  }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int z = 0; z < kMaxShares; ++z) {
-    if (!(ml[z].y > 0.f)) continue;
-    const float f = ex2_approx(ml[z].x - top);
-    l = fmaf(ml[z].y, f, l);
-    const float2* src = reinterpret_cast<const float2*>(part_o + (z * rows + row) * D + lane * kE);
-#pragma unroll
-    for (int e = 0; e < kE / 2; ++e) {
-      const float2 x = src[e];
-      acc[2 * e] = fmaf(x.x, f, acc[2 * e]);
-      acc[2 * e + 1] = fmaf(x.y, f, acc[2 * e + 1]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kE);
-#pragma unroll
-  for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ by key blocks
@@ -827,7 +831,7 @@ FwdPlan fwd_plan(const BlockDims& p, int d, void* ws) {
   f.by_blocks = by_blocks(p);
   f.shares = f.by_blocks ? 1 : block_shares(p);
   Carver c(ws);
-  size_t parts = f.shares > 1 ? static_cast<size_t>(f.shares) * p.B * p.H * p.Nq : 0;
+  size_t parts = 0;
   if (f.by_blocks) {
     const BlockDims lp = list_dims(p);
     const size_t BHk = static_cast<size_t>(p.B) * p.Hkv;
@@ -906,14 +910,21 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   if (cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SVOO_ERR_CUDA;
-  block_attn_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares), kFwdThreads, smem, st>>>(
-      qm, km, vm, p, static_cast<int>(union_cap(p)), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx,
-      lengths, scale_log2, static_cast<uint16_t*>(o), lse, f.part_o, f.part_ml, dev_err);
-  if (f.shares > 1) {
-    const size_t qrows = static_cast<size_t>(p.B) * p.H * p.Nq;
-    block_join_kernel<D><<<static_cast<unsigned>((qrows + 7) / 8), 256, 0, st>>>(qrows, f.shares, f.part_o, f.part_ml,
-                                                                                static_cast<uint16_t*>(o), lse);
-  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares);
+  cfg.blockDim = dim3(kFwdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = cluster.val.clusterDim.y = 1;
+  cluster.val.clusterDim.z = f.shares;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = f.shares > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, block_attn_kernel<D>, qm, km, vm, p, static_cast<int>(union_cap(p)),
+                         static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2,
+                         static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err)) != cudaSuccess)
+    return SVOO_ERR_CUDA;
   return launch_status();
 }
 

@@ -344,6 +344,33 @@ __device__ __forceinline__ void load_query_rows(const CUtensorMap* map, uint8_t*
         : "memory");
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// what `at` (shared memory) holds in CTA `rank` of the cluster
+__device__ __forceinline__ float2 cluster_read2(uint32_t at, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_read4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, A read from tensor memory.
 __device__ __forceinline__ void umma_f16_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t accumulate) {

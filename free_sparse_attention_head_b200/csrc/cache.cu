@@ -63,22 +63,6 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// what `at` (shared memory) holds in CTA `rank` of the cluster
-__device__ __forceinline__ float2 cluster_read2(uint32_t at, int rank) {
-  float2 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %2, %3;\n\t"
-      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y)
-      : "r"(at), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // Grid (runs, B * Hkv, ceil(G / 16)). Partial results of run x: o (fp32
 // [runs][B*H][D]) and (m in log2 units, l) per head; with one run, or where the
 // runs are a cluster (joined), the output itself. scores (may be NULL): fp32 [B*H][cap], scale * q.k * log2 e.

@@ -88,12 +88,13 @@ def test_workspaces(lib):
     assert need > 0
     assert lib.svoo_block_select(s, x, x, None, x, x, need - 1, None, None) == WORKSPACE
     assert lib.svoo_block_select(s, x, x, None, x, None, 0, None, None) == WORKSPACE
-    # lists of five tiles are not shared out, longer ones over few queries are
+    # row tiles need none; by key blocks (here: 16 heads of their own, 3 of 32 blocks of 128 keys) the parts do
     assert lib.svoo_block_attn_workspace_size(s) == 0
-    few = shape(Nk=3000, cap=3000)
-    need = lib.svoo_block_attn_workspace_size(few)
-    assert need > 0
-    assert lib.svoo_block_attn(few, x, x, x, x, None, 0.1, x, x, x, need - 1, None, None) == WORKSPACE
+    lists = shape(B=1, H=16, Hkv=16, Nq=8192, Nk=4096, cap=4096, block=128, n_sel=3, sink=1, local=0, causal=0, q_start=0)
+    need = lib.svoo_block_attn_workspace_size(lists)
+    assert need > 16 * 8192 * 3 * 64 * 4
+    assert lib.svoo_block_attn(lists, x, x, x, x, None, 0.1, x, x, x, need - 1, None, None) == WORKSPACE
+    assert lib.svoo_block_attn(lists, x, x, x, x, None, 0.1, x, x, None, 0, None, None) == WORKSPACE
     need = lib.svoo_block_attn_backward_workspace_size(s)
     assert lib.svoo_block_attn_backward(s, x, x, x, x, x, x, x, None, 0.1, x, x, x, x, need - 1, None, None) == WORKSPACE
     one = shape(Nq=1, cap=4096, Nk=4096)
