@@ -690,11 +690,14 @@ class _BlockAttn(torch.autograd.Function):
         ctx.save_for_backward(q, k, v, idx, lengths, o, lse)
         ctx.args = (args, scale, dev_err)    # an error word may be cleared between the two passes
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)    # no zeros for lse
         return o, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_o, _):
+        if grad_o is None:
+            return (None,) * 8
         q, k, v, idx, lengths, o, lse = ctx.saved_tensors
         args, scale, dev_err = ctx.args
         _need("the incoming gradient", torch.bfloat16, q.device, q.shape, grad_o := grad_o.contiguous())

@@ -21,30 +21,40 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   return fn;
 }
 
-CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
-                         uint32_t box_rows, uint32_t box_cols) {
+// A bf16 map. The encoder is a driver call and wants a current context, which a
+// host thread without any runtime call before this one does not have yet
+// (setting the thread's device makes it current, in a stream capture too).
+static CUresult encode_bf16(CUtensorMap* map, uint32_t rank, const void* base, const cuuint64_t* dims,
+                            const cuuint64_t* strides, const cuuint32_t* box) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const auto encode = [&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  const CUresult r = encode();
+  int device;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess)
+    return encode();
+  return r;
+}
+
+CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                         uint32_t box_rows, uint32_t box_cols) {
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
   const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return encode_bf16(map, 2, base, dims, strides, box);
 }
 
 CUresult encode_token_major(CUtensorMap* map, const void* base, uint64_t B, uint64_t H, uint64_t N, uint64_t cols,
                             uint32_t heads, uint32_t tokens) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[4] = {cols, H, N, B};
   const cuuint64_t strides[3] = {N * cols * 2, cols * 2, H * N * cols * 2};
   const cuuint32_t box[4] = {64, heads, tokens, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return encode_bf16(map, 4, base, dims, strides, box);
 }
 
 }  // namespace svoo

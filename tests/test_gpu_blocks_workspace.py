@@ -1,6 +1,7 @@
 """What workspaces and outputs hold before a call reaches no result: every operator of the block-selected attention
 and of the cache, with its workspace and outputs filled beforehand, against a call of its own, bit for bit."""
 import math
+import threading
 
 import pytest
 import torch
@@ -77,3 +78,29 @@ def test_cache(B, H, Hkv, cap, d, byte):
         svoo.cache_evict(*state, 400, sink=2, recent=30, workspace=ws)
         got.append(state)
     assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+def test_first_call_of_a_host_thread():
+    """A thread that has made no CUDA call before: forward, gradient, selection, cache, and the gradient by autograd,
+    whose own thread may be such a one."""
+    q, k, v, g = rand(1, 1, 4, 300, 64), rand(2, 1, 2, 300, 64), rand(3, 1, 2, 300, 64), rand(4, 1, 4, 300, 64)
+    one = q[:, :, :1].contiguous()
+    cfg = svoo.BlockConfig(n_sel=3)
+    pool = svoo.block_pool(k, cfg)
+    idx = svoo.block_select(q, pool, cfg, 300)
+    o, lse = svoo.block_attn(q, k, v, idx, cfg)
+    calls = dict(select=lambda: (svoo.block_select(q, pool, cfg, 300),), attn=lambda: svoo.block_attn(q, k, v, idx, cfg),
+                 grad=lambda: svoo.block_attn_backward(q, k, v, o, lse, g, idx, cfg), cache=lambda: svoo.cache_attn(one, k, v))
+
+    def leaves():
+        x = [t.detach().clone().requires_grad_(True) for t in (q, k, v)]
+        return torch.autograd.grad(svoo.block_attention(*x, cfg)[0], x, g)
+
+    calls["autograd"] = leaves
+    for name, call in calls.items():
+        want, got = call(), []
+        torch.cuda.synchronize()
+        t = threading.Thread(target=lambda: got.append(call()))
+        t.start()
+        t.join()
+        assert got and all(torch.equal(x, y) for x, y in zip(want, got[0])), name
