@@ -10,7 +10,10 @@
 // and a warp none of whose queries did skips the exponentials. The union keeps
 // the tensor cores on full 128-row products whatever G is, at the price of
 // rows that compute for nothing: neighbouring queries mostly agree, and in the
-// worst case the union is what dense attention would read.
+// worst case the union is what dense attention would read. 534 us at 32760
+// tokens, 16/2 heads, d = 128, 16 blocks of 64 keys, whose unions are 1.9
+// selections: 0.5 PFLOP/s of the selected keys, 0.97 of what it computes. Where
+// unions would be near everything, a call goes by key blocks instead (below).
 //
 // Where there are few row tiles, a tile's list is shared out to several CTAs
 // (grid.z), a cluster that puts its parts together from its shared memories.

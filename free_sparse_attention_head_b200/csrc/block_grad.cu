@@ -9,7 +9,7 @@
 //
 //   block_dq_kernel      delta, and dq: row tiles against the union of their
 //                        blocks, as the forward kernel walks it
-//   sel_hist / sel_scan / sel_items / sel_fill
+//   sel_walk / sel_scan / sel_items (block_lists.cuh)
 //                        for every block the list of the queries that selected
 //                        it, in a fixed order (no atomics decide a place)
 //   block_dkv_kernel     dk, dv: one key tile against its list's rows, gathered
@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
 // ------------------------------------------------------------------ dk, dv
 
-constexpr int kDkvThreads = 416;  // warps 0-3, 4-7: dS of even / odd row tiles; 8-11: loads; 12: MMA issuer
+constexpr int kDkvLoaders = 256;  // threads; 128 of them took longer to issue a tile's 64 KB (585 us against 551, as below)
+constexpr int kDkvThreads = 256 + kDkvLoaders + 32;  // warps 0-3, 4-7: dS of even / odd row tiles; 8-15: loads; 16: MMA issuer
+constexpr int kDkvIssuer = kDkvThreads / 32 - 1;
 
 struct DkvSmem {
   uint64_t full[2], free_[2], s_full[2], ds_full[2], mma_final;
@@ -398,6 +400,10 @@ constexpr size_t dkv_tile_bytes() {
 // with the model dimension as the product's 128 rows (d = 64: dO and Q side by
 // side, each product uses its own half of the lanes), so that a tile of 64
 // keys runs at M = 128.
+// Bound by the chain of a stage (rows in, two products, dS, two products, with 64 KB
+// of rows to each of two stages): 551 us at 16384 tokens, 16/4 heads, d = 128, 16
+// blocks of 64 keys, of which the products alone would be 180 and the rows' bytes
+// out of L2 about 210.
 // TMEM: S, dP of stage s at s * 128 + {0, 64}; dV^T at 256, dK^T at 320.
 template <int D>
 __global__ void __launch_bounds__(kDkvThreads, 1)
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (tid == 0) {
     S->abort = 0;
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&S->full[s]), 128);
+      mbar_init(smem_u32(&S->full[s]), kDkvLoaders);
       mbar_init(smem_u32(&S->free_[s]), 1);
       mbar_init(smem_u32(&S->s_full[s]), 1);
       mbar_init(smem_u32(&S->ds_full[s]), 4);
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     load_key_rows<D>(v_s, v, krow, len - key0, tid, kDkvThreads);
     fence_proxy_async_smem();
   }
-  if (warp == 12) {
+  if (warp == kDkvIssuer) {
     __syncwarp();
     tmem_alloc(smem_u32(&S->tmem_base), 512);
     tmem_relinquish();
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   volatile int* abort = &S->abort;
   const uint32_t row_u = smem_u32(row_s), p_u = smem_u32(p_s), k_u = smem_u32(k_s), v_u = smem_u32(v_s);
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8 && warp < kDkvIssuer) {
     // ---------------------------------------------------------------- row gather
     const int t = tid - 256;  // one row's list entry and scalars per thread
     constexpr int kChunks = D / 8;
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     // entry of tile j + 2, and the scalars of tile j + 1.
     auto entry = [&](int j) {  // the query of this thread's row in tile j, -1 behind the last
       const int f = j * kRowTile + t;
-      return f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
+      return t < kRowTile && f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
     };
     int row = -1, nv = 0;
     float l2 = INFINITY, dl = 0.f;
@@ -503,28 +509,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     for (int j = 0; j < nj; ++j) {
       const int st = j & 1;
       const bool free = j < 2 || mbar_wait(smem_u32(&S->free_[st]), ((j - 2) >> 1) & 1, abort);
-      S->row[t] = row;
-      if (!loaders_agree(free)) break;  // all four warps go on or leave together
+      if (t < kRowTile) S->row[t] = row;
+      if (!loaders_agree<kDkvLoaders>(free)) break;  // all warps go on or leave together
       const uint32_t g_dst = row_u + st * 2 * kRowBytes, q_dst = g_dst + kRowBytes;
 #pragma unroll 8
-      for (int r = r0; r < kRowTile; r += 128 / kChunks) {
+      for (int r = r0; r < kRowTile; r += kDkvLoaders / kChunks) {
         const int src = S->row[r];
         const uint32_t off = sw128_offset(r, ch * 8, kRowTile);
         const size_t at = static_cast<size_t>(src < 0 ? 0 : src) * D + ch * 8;
         cp_async16_or_zero(g_dst + off, go + at, src >= 0);
         cp_async16_or_zero(q_dst + off, q + at, src >= 0);
       }
-      S->nv[st][t] = static_cast<uint8_t>(nv);
-      S->lse2[st][t] = l2 * 1.4426950408889634f;
-      S->delta[st][t] = dl;
+      if (t < kRowTile) {
+        S->nv[st][t] = static_cast<uint8_t>(nv);
+        S->lse2[st][t] = l2 * 1.4426950408889634f;
+        S->delta[st][t] = dl;
+      }
       scalars(j + 1, tok);
       tok = entry(j + 2);
       cp_async_wait_all();
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&S->full[st]));  // this thread's part of row tile j is in
-      loaders_agree(true);  // S->row is free again
+      loaders_agree<kDkvLoaders>(true);  // S->row is free again
     }
-  } else if (warp == 12) {
+  } else if (warp == kDkvIssuer) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort) report_error(err, kErrTimeoutAttn);
-  if (warp == 12) {
+  if (warp == kDkvIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -155,17 +155,18 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// barrier of the four loader warps, with a vote
+// barrier of the loader warps, with a vote
+template <int kThreads>
 __device__ __forceinline__ bool loaders_agree(bool ok) {
   uint32_t r;
   __syncwarp();  // bar takes a warp's threads together
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok ? 1u : 0u)
+      : "r"(ok ? 1u : 0u), "n"(kThreads)
       : "memory");
   return r != 0;
 }

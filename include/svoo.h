@@ -351,8 +351,11 @@ svoo_status svoo_block_select(const svoo_block_shape *shape, const void *q, cons
  * first entry that is out of range or not above the one before it, and an entry
  * other than -1 there sets bit 4 in dev_err. A query without keys gets o = 0,
  * lse = -inf. sink and local are not used. fp32 softmax and sums; P is rounded
- * to bf16 for the second product. The workspace (256-byte aligned; 0 bytes where
- * there are many queries) must not be shared by calls that overlap on the GPU. */
+ * to bf16 for the second product. The workspace (256-byte aligned) must not be
+ * shared by calls that overlap on the GPU. Most calls need none (0 bytes); where
+ * neighbouring queries' selections, blocks of a multiple of 128 keys, would
+ * together be nearly all blocks, a call keeps every query's part of each 128
+ * selected keys there: 4 * (d + 2) bytes each, up to 4.5 GB. */
 size_t svoo_block_attn_workspace_size(const svoo_block_shape *shape);
 svoo_status svoo_block_attn(const svoo_block_shape *shape, const void *q, const void *k,
                             const void *v, const int32_t *idx, const int32_t *lengths, float scale,
