@@ -401,7 +401,7 @@ constexpr size_t dkv_tile_bytes() {
 // side, each product uses its own half of the lanes), so that a tile of 64
 // keys runs at M = 128.
 // Bound by the chain of a stage (rows in, two products, dS, two products, with 64 KB
-// of rows to each of two stages): 551 us at 16384 tokens, 16/4 heads, d = 128, 16
+// of rows to each of two stages): 526 us at 16384 tokens, 16/4 heads, d = 128, 16
 // blocks of 64 keys, of which the products alone would be 180 and the rows' bytes
 // out of L2 about 210.
 // TMEM: S, dP of stage s at s * 128 + {0, 64}; dV^T at 256, dK^T at 320.
@@ -480,9 +480,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const int ch = t % kChunks, r0 = t / kChunks;
     // Read ahead, so that no load is waited for where it is issued: the list
     // entry of tile j + 2, and the scalars of tile j + 1.
+    const unsigned first_row = static_cast<unsigned>(row0), G = p.G;  // 32 bits: 64-bit divisions took 500 cycles a tile
     auto entry = [&](int j) {  // the query of this thread's row in tile j, -1 behind the last
       const int f = j * kRowTile + t;
-      return t < kRowTile && f < rows ? toks[static_cast<int>((row0 + f) / p.G)] : -1;
+      return t < kRowTile && f < rows ? toks[(first_row + f) / G] : -1;
     };
     int row = -1, nv = 0;
     float l2 = INFINITY, dl = 0.f;
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       l2 = INFINITY;  // a row that does not take part: P = 2^(s - inf) = 0
       dl = 0.f;
       if (tok >= 0) {
-        const int g = static_cast<int>((row0 + j * kRowTile + t) % p.G);
+        const int g = (first_row + j * kRowTile + t) % G;
         row = (b * p.H + hk * p.G + g) * p.Nq + tok;
         nv = max(0, min(kKeyTile, query_limit(p, len, tok) - key0));
         if (nv > 0) {
