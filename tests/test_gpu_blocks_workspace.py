@@ -104,3 +104,38 @@ def test_first_call_of_a_host_thread():
         t.start()
         t.join()
         assert got and all(torch.equal(x, y) for x, y in zip(want, got[0])), name
+
+
+@pytest.mark.parametrize("shape", [SHAPES[1], SHAPES[4]], ids=["shares", "by key blocks"])
+def test_captured_and_replayed(shape):
+    """A graph with the forward call and its gradient, replayed over other inputs, and one token's calls."""
+    B, H, Hkv, Nq, Nk, d, block, n_sel, sink, local, causal, _ = shape
+    cfg = svoo.BlockConfig(block=block, n_sel=n_sel, sink=sink, local=local, causal=causal)
+    q, k, v, g = rand(1, B, H, Nq, d), rand(2, B, Hkv, Nk, d), rand(3, B, Hkv, Nk, d), rand(4, B, H, Nq, d)
+    one = rand(5, B, H, 1, d)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def calls():
+        pool = svoo.block_pool(k, cfg)
+        idx = svoo.block_select(q, pool, cfg, Nk, dev_err=err)
+        o, lse = svoo.block_attn(q, k, v, idx, cfg, dev_err=err)
+        tok = svoo.block_select(one, pool, cfg, Nk, dev_err=err)
+        return (o, lse, *svoo.block_attn_backward(q, k, v, o, lse, g, idx, cfg, dev_err=err),
+                *svoo.cache_attn(one, k, v, idx=tok, cfg=cfg, dev_err=err), *svoo.cache_attn(one, k, v, dev_err=err))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls()
+    for seed in (11, 12):
+        for i, t in enumerate((q, k, v, g, one)):
+            t.copy_(rand(seed * 10 + i, *t.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(x, y) for x, y in zip(got, calls()))
+    assert int(err) == 0
