@@ -492,9 +492,12 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
     mbar_init(smem_u32(&S->mma_final), 1);
     fence_mbar_init();
   }
+  // one step of at most 64 blocks: the means' parts are made here, without a
+  // kernel of their own before this one (2.3 us and its launch)
+  const bool own = norms == nullptr;
   if (warp == 4) {
     float big = 0.f;
-    for (int i = lane; i < nbp / 64; i += 32)
+    for (int i = lane; !own && i < nbp / 64; i += 32)
       big = fmaxf(big, norms[static_cast<size_t>(blockIdx.y) * (nbp / 64) + i]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -559,6 +562,19 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   const uint32_t tmem = S->tmem_base;
   volatile int* abort = &S->abort;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  constexpr int kMean = D / 4, kMeans = (64 * kMean + kMmaSelThreads - 1) / kMmaSelThreads;  // 16-byte pieces
+  auto mean_at = [&](int i) {
+    const int at = i * kMmaSelThreads + tid;
+    return at / kMean < min(p.nb, 64)
+               ? *reinterpret_cast<const float4*>(pool + static_cast<size_t>(blockIdx.y) * p.nb * D + at * 4)
+               : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  constexpr bool kAhead = D == 64;  // at d = 128 there are no registers for it
+  float4 mean[kAhead ? kMeans : 1];
+  if (kAhead && own && steps > 0) {
+#pragma unroll
+    for (int i = 0; i < kMeans; ++i) mean[kAhead ? i : 0] = mean_at(i);
+  }
   float q2 = 0.f;
   if (steps > 0 && warp < 4) {
     // this query's parts into tensor memory, and its norm
@@ -588,6 +604,30 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (own && steps > 0) {
+    float big = 0.f;
+#pragma unroll(kAhead ? kMeans : 4)
+    for (int i = 0; i < kMeans; ++i) {
+      const int at = i * kMmaSelThreads + tid, c = at / kMean, d = at % kMean * 4;
+      if (c >= 64) break;  // a warp's pieces end together
+      const float4 x = kAhead ? mean[kAhead ? i : 0] : mean_at(i);
+      const uint32_t h0 = pack_bf16x2(x.x, x.y), h1 = pack_bf16x2(x.z, x.w);
+      const uint32_t l0 = pack_bf16x2(x.x - __uint_as_float(h0 << 16), x.y - __uint_as_float(h0 & 0xffff0000u));
+      const uint32_t l1 = pack_bf16x2(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xffff0000u));
+      uint8_t* dst = stage + sw128_offset(c, d & ~7, kKeyTile) + (d & 4) * 2;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(dst + kTile) = make_uint2(l0, l1);
+      float n2 = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w;
+#pragma unroll
+      for (int o = kMean / 2; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      big = fmaxf(big, n2);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    if (lane == 0) atomicMax(reinterpret_cast<int*>(&S->pool_norm2), __float_as_int(big));  // 0 and above
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   int armed = -1;
 
   const Candidates cd = warp < 4 && tid < nt ? candidates(p, len, t0 + tid) : Candidates{0, 0, 0};
@@ -601,7 +641,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   uint16_t* mi = li + (tid & 127);
 
   if (warp == 4) {
-    if (lane == 0 && steps > 0) {
+    if (own) {
+      if (lane == 0 && steps > 0) mbar_arrive(smem_u32(&S->full[0]));
+    } else if (lane == 0 && steps > 0) {
       tma_prefetch_desc(&pmap);
       const int row0 = blockIdx.y * nbp, lo_row = p.B * p.Hkv * nbp;
       for (int j = 0; j < steps; ++j) {
@@ -1003,6 +1045,7 @@ inline bool mma_select(const BlockDims& p) {
 
 struct SelectPlan {
   int nbp;
+  bool split;  // the means' parts by a kernel of their own
   uint16_t* parts;
   float* norms;
   size_t bytes;
@@ -1013,8 +1056,9 @@ SelectPlan select_plan(const BlockDims& p, int d, void* ws) {
   const size_t rows = static_cast<size_t>(p.B) * p.Hkv * s.nbp;
   Carver c(ws);
   const bool mma = mma_select(p);
-  s.parts = c.take<uint16_t>(mma ? 2 * rows * d : 0);
-  s.norms = c.take<float>(mma ? rows / 64 : 0);
+  s.split = mma && p.nb > 64;
+  s.parts = c.take<uint16_t>(s.split ? 2 * rows * d : 0);
+  s.norms = c.take<float>(s.split ? rows / 64 : 0);
   s.bytes = (c.used + 255) / 256 * 256;
   return s;
 }
@@ -1025,14 +1069,15 @@ svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* po
   const SelectPlan s = select_plan(p, D, ws);
   const int BHk = p.B * p.Hkv;
   const uint64_t rows = static_cast<uint64_t>(BHk) * s.nbp;
-  CUtensorMap pm;
-  if (encode_tiled_2d(&pm, s.parts, 2 * rows, D, kKeyTile, 64) != CUDA_SUCCESS) return SVOO_ERR_CUDA;
+  CUtensorMap pm = {};
+  if (s.split && encode_tiled_2d(&pm, s.parts, 2 * rows, D, kKeyTile, 64) != CUDA_SUCCESS) return SVOO_ERR_CUDA;
   if (cudaFuncSetAttribute(mma_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(mma_sel_smem<D>())) != cudaSuccess)
     return SVOO_ERR_CUDA;
-  pool_split_kernel<D><<<dim3(s.nbp / 64, BHk), 256, 0, st>>>(p.nb, s.nbp, rows * D, pool, s.parts, s.norms);
+  if (s.split)
+    pool_split_kernel<D><<<dim3(s.nbp / 64, BHk), 256, 0, st>>>(p.nb, s.nbp, rows * D, pool, s.parts, s.norms);
   mma_select_kernel<D><<<dim3((p.Nq + kRowTile - 1) / kRowTile, BHk), kMmaSelThreads, mma_sel_smem<D>(), st>>>(
-      pm, p, s.nbp, static_cast<const uint16_t*>(q), pool, s.norms, lengths, idx, dev_err);
+      pm, p, s.nbp, static_cast<const uint16_t*>(q), pool, s.split ? s.norms : nullptr, lengths, idx, dev_err);
   return launch_status();
 }
 

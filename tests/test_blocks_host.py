@@ -84,10 +84,12 @@ def test_null_and_misaligned_pointers_are_refused(lib):
 def test_workspaces(lib):
     x = 0x1000
     s = shape()
-    need = lib.svoo_block_select_workspace_size(s)
+    assert lib.svoo_block_select_workspace_size(s) == 0     # up to 64 blocks need none
+    longer = shape(Nk=5000, cap=5000)
+    need = lib.svoo_block_select_workspace_size(longer)
     assert need > 0
-    assert lib.svoo_block_select(s, x, x, None, x, x, need - 1, None, None) == WORKSPACE
-    assert lib.svoo_block_select(s, x, x, None, x, None, 0, None, None) == WORKSPACE
+    assert lib.svoo_block_select(longer, x, x, None, x, x, need - 1, None, None) == WORKSPACE
+    assert lib.svoo_block_select(longer, x, x, None, x, None, 0, None, None) == WORKSPACE
     # row tiles need none; by key blocks (here: 16 heads of their own, 3 of 32 blocks of 128 keys) the parts do
     assert lib.svoo_block_attn_workspace_size(s) == 0
     lists = shape(B=1, H=16, Hkv=16, Nq=8192, Nk=4096, cap=4096, block=128, n_sel=3, sink=1, local=0, causal=0, q_start=0)
