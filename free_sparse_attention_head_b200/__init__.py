@@ -532,7 +532,7 @@ def _queries(q: torch.Tensor):
 
 
 def _key_rows(what: str, t: torch.Tensor, device) -> int:
-    """Rows from one head to the next of a bf16 [B, Hkv, Nk, d] tensor: contiguous, or the first Nk
+    """Rows from one head to the next of a bf16 [B, Hkv, Nk, d] tensor: contiguous, or the same Nk
     rows of every head of a longer contiguous buffer."""
     if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.device != device or not t.is_cuda:
         raise SvooError(f"{what} must be a bf16 [B, Hkv, N, d] tensor on {device}")
@@ -543,7 +543,7 @@ def _key_rows(what: str, t: torch.Tensor, device) -> int:
     cap = s1 // d if Hkv > 1 else s0 // (Hkv * d)
     if s3 != 1 or (s2 != d and Nk > 1) or cap < Nk or (Hkv > 1 and s1 != cap * d) or \
             (B > 1 and s0 != Hkv * cap * d):
-        raise SvooError(f"{what} must be contiguous or the first rows of every head of a contiguous buffer")
+        raise SvooError(f"{what} must be contiguous or the same rows of every head of a contiguous buffer")
     return cap
 
 

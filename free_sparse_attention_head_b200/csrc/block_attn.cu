@@ -865,7 +865,7 @@ svoo_status launch_block_lists(const BlockDims& p, const FwdPlan& f, const uint1
   const BlockDims lp = list_dims(p);
   const int BHk = p.B * p.Hkv;
   CUtensorMap km, vm;
-  const uint64_t krows = static_cast<uint64_t>(BHk) * p.cap;
+  const uint64_t krows = mapped_key_rows(p);
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
@@ -904,7 +904,7 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
                                  static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o),
                                  lse, dev_err, st);
   CUtensorMap qm, km, vm;
-  const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.cap;
+  const uint64_t rows = mapped_key_rows(p);
   if (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
       encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)

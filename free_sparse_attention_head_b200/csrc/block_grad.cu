@@ -777,7 +777,7 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
                  *vp = static_cast<const uint16_t*>(v), *gp = static_cast<const uint16_t*>(go);
   CUtensorMap qm, gm, om, km, vm;
-  const uint64_t krows = static_cast<uint64_t>(BHk) * p.cap;
+  const uint64_t krows = mapped_key_rows(p);
   if (p.Nq > 0 && (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
                    encode_token_major(&gm, go, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
                    encode_token_major(&om, o, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS))

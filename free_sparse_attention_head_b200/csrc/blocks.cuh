@@ -74,6 +74,14 @@ inline BlockDims block_dims(const svoo_block_shape* s) {
   return p;
 }
 
+// Rows of a tensor map over keys or values: up to the last key of the last head.
+// A view may begin inside its buffer, whose end is then less than cap rows from
+// there, and a whole tile is loaded where the sequence ends inside one: what the
+// map does not cover arrives as zeros and is not read.
+inline uint64_t mapped_key_rows(const BlockDims& p) {
+  return (static_cast<uint64_t>(p.B) * p.Hkv - 1) * p.cap + p.Nk;
+}
+
 inline bool scale_ok(float scale) { return scale > 0.f && scale < INFINITY; }
 
 #ifdef __CUDACC__

@@ -478,7 +478,7 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
                               int32_t* dev_err, cudaStream_t st) {
   const CachePlan c = cache_plan(p, D, idx != nullptr, weight != nullptr, ws);
   CUtensorMap km, vm;
-  const uint64_t rows = static_cast<uint64_t>(p.B) * p.Hkv * p.cap;
+  const uint64_t rows = mapped_key_rows(p);
   if (encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;

@@ -300,7 +300,8 @@ svoo_status svoo_snr_top_p(int steps, int warmup, double p_min, double tau, doub
 
 /* Shape of one call.
  *  q, o : bf16 [B][H][Nq][d];  k, v : bf16 [B][Hkv][cap][d], of which the first
- *  Nk rows of every head are keys (cap > Nk: a view into a longer buffer).
+ *  Nk rows of every head are keys (cap > Nk: a view into a longer buffer, which
+ *  may begin anywhere in it: nothing behind the last head's last key is read).
  *  lengths (int32 [B], DEVICE, may be NULL = Nk): the valid keys of every
  *  sequence, 0 <= lengths[b] <= Nk (clamped). What lies behind them is never
  *  used and may hold anything, NaN included.
