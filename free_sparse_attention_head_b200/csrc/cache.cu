@@ -16,7 +16,8 @@
 //                     Up to eight runs are a cluster and join through each
 //                     other's shared memory. 75 us at 48 sequences, 40/8 heads,
 //                     d = 128, 32 blocks of 64 slots each (403 MB: 5.4 TB/s).
-// cache_join_kernel   joins more runs, and turns the kept scores into weights.
+// cache_join_kernel   joins more runs, and turns the kept scores into weights
+//                     (not while a timeout bit is set).
 // evict_select_kernel the slots that stay, one CTA per (sequence, key head): 21 us
 //                     for 128 of them with 8192 slots (barriers of its passes).
 // evict_move_kernel   moves kept rows from behind `keep` into the holes: 49 us
@@ -35,6 +36,9 @@ constexpr int kMaxJoined = 8;  // CTAs of a cluster
 
 struct CacheSmem {
   uint64_t full[kCacheStages], empty[kCacheStages];
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   int abort;
   float m[kCacheWarps][kHeadRows], l[kCacheWarps][kHeadRows];
   float2 ml[kHeadRows];  // of the CTA, for its cluster
@@ -95,6 +99,9 @@ __global__ void __launch_bounds__(kCacheThreads)
       mbar_init(smem_u32(&S->full[s]), 1);
       mbar_init(smem_u32(&S->empty[s]), kCacheWarps);
     }
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
   }
   // tiles of this run: [i0, i1) of the sequence's, or of its selected blocks'
@@ -127,7 +134,11 @@ __global__ void __launch_bounds__(kCacheThreads)
       tma_prefetch_desc(&vmap);
       const int row0 = bh * p.cap;
       int j = 0;
-      for (int i = i0; i < i1; ++i) {
+      bool go = true;
+#ifdef SVOO_TEST_STALL
+      go = mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
+      for (int i = i0; i < i1 && go; ++i) {
         const int key0 = tile_key(i);
         if (key0 >= len) continue;
         const int st = j % kCacheStages;
@@ -347,14 +358,17 @@ __global__ void __launch_bounds__(kCacheThreads)
 
 // Grid (1 + chunks of 1024 slots where weights are kept, B * Hkv). Block 0
 // joins the runs of the group's heads (when there are several), the others add
-// the slots' weights. Dynamic shared memory: a factor per (head, run).
+// the slots' weights, unless a wait has run out: a run that gave up left its
+// scores unwritten, and the weights are the caller's for good. Dynamic shared
+// memory: a factor per (head, run).
 template <int D>
 __global__ void __launch_bounds__(256)
     cache_join_kernel(BlockDims p, int runs, const int32_t* __restrict__ lengths, const float* __restrict__ part_o,
                       const float2* __restrict__ part_ml, const float* __restrict__ scores, uint16_t* __restrict__ o,
-                      float* __restrict__ lse, float* __restrict__ weight) {
+                      float* __restrict__ lse, float* __restrict__ weight, const int* __restrict__ err) {
   extern __shared__ float factor[];
   __shared__ float lse2[kRowTile];
+  if (__syncthreads_or(timed_out_before(err) ? 1 : 0)) return;
   const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh - b * p.Hkv;
   const size_t row0 = static_cast<size_t>(b) * p.H + hk * p.G, rows = static_cast<size_t>(p.B) * p.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -509,7 +523,7 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
     return SVOO_ERR_CUDA;
   if (runs > 1 || weight)
     cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, factors, st>>>(
-        p, runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight);
+        p, runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight, dev_err);
   return launch_status();
 }
 

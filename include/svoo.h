@@ -381,8 +381,10 @@ svoo_status svoo_block_attn_backward(const svoo_block_shape *shape, const void *
  * used): o bf16 [B][H][1][d], lse fp32 [B][H][1].
  *  idx (int32 [B][Hkv][1][n_sel], may be NULL): only the slots of those blocks.
  *  weight (fp32 [B][Hkv][cap], may be NULL): weight[slot] += sum over the
- *  group's heads of the slot's softmax weight, for every valid slot. idx and
- *  weight together are SVOO_ERR_UNSUPPORTED.
+ *  group's heads of the slot's softmax weight, for every valid slot. A call that
+ *  times out, or finds a timeout bit in dev_err, leaves them as they were
+ *  (without dev_err there is no word to tell it by). idx and weight together are
+ *  SVOO_ERR_UNSUPPORTED.
  * Workspace: svoo_cache_attn_workspace_size(shape, idx != NULL, weight != NULL)
  * bytes (may be 0), 256-byte aligned, not shared by calls that overlap on the
  * GPU. */
