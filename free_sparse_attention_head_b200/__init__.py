@@ -482,6 +482,9 @@ class BlockConfig:
     scale: Optional[float] = None  # default 1/sqrt(d)
 
 
+# stream= runs a call as if that stream were current: what the call reads must be ready there, and stay allocated
+# until the stream has used it; the calls' own workspaces and results are the stream's.
+#
 # The calls below serve single tokens, where the host's own work counts: shapes and
 # workspace sizes are looked up by their numbers, pointers go to ctypes as integers.
 
@@ -496,11 +499,26 @@ def _dp(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _call(what: str, t: torch.Tensor, stream, *args):
-    """Calls a C entry point with t's device current, on `stream` or t's device's current one."""
+def _under(stream, fn, t, *args):
+    """A call with stream=: fn(t, *args) with that stream current, so that the workspaces and results made
+    inside are the stream's own memory. The current stream's would be given to later work there while
+    the kernels still use it. Results may be freed once the current stream has used them."""
+    if not isinstance(t, torch.Tensor) or t.device != stream.device:
+        raise SvooError(f"stream is one of {stream.device}: the tensors must live there")
+    mine = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = fn(t, *args)
+    for x in out if isinstance(out, tuple) else (out,):
+        if x is not None and not any(x is a for a in args):
+            x.record_stream(mine)
+    return out
+
+
+def _call(what: str, t: torch.Tensor, *args):
+    """Calls a C entry point with t's device current, on that device's current stream."""
     fn = getattr(_lib if _lib is not None else load(), what)
     dev = t.device.index
-    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    st = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch.cuda.current_device():
         status = fn(*args, st)
     else:
@@ -593,6 +611,8 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
 
     `pool` is written in place instead of a new tensor; with last > 0 only the last `last` blocks that
     hold keys of each sequence are renewed (after a token was appended, last=1)."""
+    if stream is not None:
+        return _under(stream, block_pool, k, cfg, lengths, pool, last)
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, N, d] tensor on a CUDA device")
     dev = k.device
@@ -606,7 +626,7 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
         pool = torch.empty(B, Hkv, nb, d, dtype=torch.float32, device=dev)
     else:
         _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
-    _call("svoo_block_pool", k, stream, _bshape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0),
+    _call("svoo_block_pool", k, _bshape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0),
           k.data_ptr(), _dp(lengths), last, pool.data_ptr())
     return pool
 
@@ -617,6 +637,8 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
 
     n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
     queries are the last Nq of n_keys; -1: the last Nq of each sequence's lengths."""
+    if stream is not None:
+        return _under(stream, block_select, q, pool, cfg, n_keys, lengths, q_start, idx, workspace, dev_err)
     B, H, Nq, d = _queries(q)
     dev = q.device
     nb = -(-n_keys // cfg.block) if cfg.block > 0 else 0
@@ -630,7 +652,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     args = (B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
             n_keys - Nq if q_start is None else q_start)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
-    _call("svoo_block_select", q, stream, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
+    _call("svoo_block_select", q, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
           idx.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return idx
 
@@ -639,20 +661,22 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
                workspace=None, dev_err=None, stream=None):
     """Attention of every query over the blocks in idx; returns (o, lse). No gradient is recorded
     (block_attention records one)."""
+    if stream is not None:
+        return _under(stream, block_attn, q, k, v, idx, cfg, lengths, q_start, out, workspace, dev_err)
     args = _block_args(q, k, v, cfg, lengths, q_start)
     B, H, Hkv, Nq, _, _, d = args[:7]
     dev = q.device
     _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
     _need("out", torch.bfloat16, dev, q.shape, out)
-    return _run_attn(args, _block_scale(cfg, d), q, k, v, idx, lengths, out, workspace, dev_err, stream)
+    return _run_attn(args, _block_scale(cfg, d), q, k, v, idx, lengths, out, workspace, dev_err)
 
 
-def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err, stream=None):
+def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err):
     dev = q.device
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(args[0], args[1], args[3], dtype=torch.float32, device=dev)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
-    _call("svoo_block_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
+    _call("svoo_block_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
           _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return out, lse
 
@@ -660,6 +684,9 @@ def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err, strea
 def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=None,
                         q_start: Optional[int] = None, workspace=None, dev_err=None, stream=None):
     """Gradient of block_attn: (dq, dk, dv), with idx, o and lse as block_attn had or gave them."""
+    if stream is not None:
+        return _under(stream, block_attn_backward, q, k, v, o, lse, grad_o, idx, cfg, lengths, q_start, workspace,
+                      dev_err)
     args = _block_args(q, k, v, cfg, lengths, q_start)
     B, H, Hkv, Nq, _, _, d = args[:7]
     dev = q.device
@@ -667,17 +694,16 @@ def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=
     _need("o", torch.bfloat16, dev, q.shape, o)
     _need("grad_o", torch.bfloat16, dev, q.shape, grad_o)
     _need("lse", torch.float32, dev, (B, H, Nq), lse)
-    return _run_attn_backward(args, _block_scale(cfg, d), q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err,
-                              stream)
+    return _run_attn_backward(args, _block_scale(cfg, d), q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err)
 
 
-def _run_attn_backward(args, scale, q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err, stream=None):
+def _run_attn_backward(args, scale, q, k, v, o, lse, grad_o, idx, lengths, workspace, dev_err):
     dev = q.device
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_backward_workspace_size", *args)
     dq = torch.empty_like(q)
     dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
     dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _call("svoo_block_attn_backward", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call("svoo_block_attn_backward", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), scale,
           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws_at, ws_n, _dp(dev_err))
     return dq, dk, dv
@@ -732,6 +758,8 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
 
     idx (from block_select, with its cfg): only the slots of the selected blocks. weight (fp32
     [B, Hkv, cap]): every valid slot's softmax weight, summed over the group's heads, is added to it."""
+    if stream is not None:
+        return _under(stream, cache_attn, q, k, v, lengths, idx, cfg, weight, out, workspace, dev_err)
     if q.dim() != 4 or q.shape[2] != 1:
         raise SvooError("q must be [B, H, 1, d]: one token per sequence")
     if idx is not None and cfg is None:
@@ -751,7 +779,7 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_attn_workspace_size", *args, idx is not None, weight is not None)
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(B, H, 1, dtype=torch.float32, device=dev)
-    _call("svoo_cache_attn", q, stream, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
+    _call("svoo_cache_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
           _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws_at, ws_n,
           _dp(dev_err))
     return out, lse
@@ -765,6 +793,8 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
     """Brings every sequence of a cache with more than `keep` slots down to `keep`, in place (k, v, weight,
     pos and lengths; see svoo_cache_evict): the first `sink` and last `recent` positions stay, then the
     heaviest slots of each key head. Block means of the cache are to be made anew afterwards."""
+    if stream is not None:
+        return _under(stream, cache_evict, k, v, weight, pos, lengths, keep, sink, recent, workspace)
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, cap, d] tensor on a CUDA device")
     B, Hkv, cap, d = k.shape
@@ -775,5 +805,5 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
         _need(what, dtype, dev, (B, Hkv, cap), t)
     _need("lengths", torch.int32, dev, (B,), lengths)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_evict_workspace_size", B, Hkv, cap, keep)
-    _call("svoo_cache_evict", k, stream, B, Hkv, cap, d, keep, sink, recent, k.data_ptr(), v.data_ptr(),
+    _call("svoo_cache_evict", k, B, Hkv, cap, d, keep, sink, recent, k.data_ptr(), v.data_ptr(),
           weight.data_ptr(), pos.data_ptr(), lengths.data_ptr(), ws_at, ws_n)

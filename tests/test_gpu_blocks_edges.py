@@ -36,3 +36,115 @@ def test_keys_as_a_view_that_begins_inside_its_buffer(first, Nk):
             want = got
     for x, y in zip(got, want):
         assert torch.equal(x, y) and torch.isfinite(x[x > -math.inf].float()).all()
+
+
+def test_another_stream_owns_the_workspace(monkeypatch):
+    """stream=: while that stream still has work before the call, nothing that the current stream allocates lies in
+    the call's workspace or results, and filling it changes no result."""
+    B, H, Hkv, N, d = 1, 16, 16, 5504, 64
+    gen = torch.Generator(device="cuda").manual_seed(53)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, g, one = r(B, H, N, d), r(B, Hkv, N, d), r(B, Hkv, N, d), r(B, H, N, d), r(B, H, 1, d)
+    fine = svoo.BlockConfig(block=64, n_sel=4)                                        # selection of 86 blocks
+    cfg = svoo.BlockConfig(block=128, n_sel=4, sink=1, local=0, causal=False)        # attention by key blocks
+    w0 = torch.rand(B, Hkv, N, generator=gen, device="cuda")
+    fine_pool, pool = svoo.block_pool(k, fine), svoo.block_pool(k, cfg)
+    idx = svoo.block_select(q, pool, cfg, N)
+    o, lse = svoo.block_attn(q, k, v, idx, cfg)
+    pos = torch.arange(N, device="cuda").int().repeat(B, Hkv, 1)
+    wide = svoo.BlockConfig(block=64, n_sel=64)
+    idx1 = svoo.block_select(one, fine_pool, wide, N)
+    calls = dict(
+        pool=lambda **kw: [svoo.block_pool(k, cfg, **kw)],
+        select=lambda **kw: [svoo.block_select(q, fine_pool, fine, N, **kw)],
+        attn=lambda **kw: list(svoo.block_attn(q, k, v, idx, cfg, **kw)),
+        backward=lambda **kw: list(svoo.block_attn_backward(q, k, v, o, lse, g, idx, cfg, **kw)),
+        whole=lambda **kw: list(svoo.cache_attn(one, k, v, **kw)),
+        selected=lambda **kw: list(svoo.cache_attn(one, k, v, idx=idx1, cfg=wide, **kw)),
+    )
+
+    def weigh(**kw):
+        w = kw.pop("w")
+        return [*svoo.cache_attn(one, k, v, weight=w, **kw), w]
+
+    def evict(**kw):
+        state = kw.pop("state")
+        svoo.cache_evict(*state, 3000, sink=4, recent=100, **kw)
+        return list(state)
+
+    torch.full((1,), 0xFF, dtype=torch.uint8, device="cuda")   # a kernel's first launch may wait for the device
+    side = torch.cuda.Stream()
+    for name in (*calls, "weigh", "evict"):
+        if name == "weigh":
+            run = lambda kw, w: weigh(w=w, **kw)  # noqa: E731
+            mine = [(w0.clone(),) for _ in range(2)]
+        elif name == "evict":
+            run = lambda kw, *st: evict(state=st, **kw)  # noqa: E731
+            mine = [(k.clone(), v.clone(), w0.clone(), pos.clone(), lens([N])) for _ in range(2)]
+        else:
+            run = lambda kw: calls[name](**kw)  # noqa: E731
+            mine = [(), ()]
+        want = [t.clone() for t in run({}, *mine[0])]
+        torch.cuda.synchronize()
+        sizes = []
+        empty = torch.empty
+
+        def noting(*a, **kw):
+            t = empty(*a, **kw)
+            if t.is_cuda:
+                sizes.append((t.data_ptr(), t.numel() * t.element_size()))
+            return t
+
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(800_000_000)     # some tenths of a second: the call's kernels have not begun
+        monkeypatch.setattr(svoo.torch, "empty", noting)
+        got = run({"stream": side}, *mine[1])
+        monkeypatch.setattr(svoo.torch, "empty", empty)
+        assert not side.query(), "the stream was to be busy"
+        made = list(sizes)
+        if name in ("select", "attn", "backward", "whole", "weigh", "evict"):
+            assert made, name
+        later = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _, n in made for _ in range(3)]
+        assert not side.query(), "the stream was to be busy"
+        for at, n in made:
+            for t in later:
+                assert t.data_ptr() + t.numel() <= at or at + n <= t.data_ptr(), (name, n)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), name
+        del later, got
+
+
+def test_a_stream_of_no_device_of_the_tensors():
+    k = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16)
+    with pytest.raises(svoo.SvooError):
+        svoo.block_pool(k, svoo.BlockConfig(), stream=torch.cuda.Stream())
+
+
+def test_another_stream_in_a_graph():
+    q, k, v = (t.cuda() for t in make(1, 4, 2, 200, 5000, 64, seed=54))
+    cfg = svoo.BlockConfig(block=64, n_sel=4)
+
+    def calls(side):
+        side.wait_stream(torch.cuda.current_stream())
+        pool = svoo.block_pool(k, cfg, stream=side)
+        idx = svoo.block_select(q, pool, cfg, 5000, stream=side)
+        o, lse = svoo.block_attn(q, k, v, idx, cfg, stream=side)
+        out = (o, lse, *svoo.block_attn_backward(q, k, v, o, lse, q, idx, cfg, stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+        return out
+
+    warm = torch.cuda.Stream()
+    calls(warm)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        out = calls(side)
+    for seed in (55, 56):
+        for t, new in zip((q, k, v), make(1, 4, 2, 200, 5000, 64, seed=seed)):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = calls(warm)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
