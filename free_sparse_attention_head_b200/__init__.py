@@ -3,7 +3,9 @@
 Argument marshalling only: every step runs in the library's CUDA kernels
 (`csrc/`, C ABI in `include/svoo.h`). PyTorch provides device memory and the
 current CUDA stream. If the compiled library is missing or no CUDA device is
-present, calls raise; there is no CPU fallback.
+present, calls raise; there is no CPU fallback. stream= runs a call as if that
+stream were current: what the call reads must be ready there, and stay allocated
+until the stream has used it; workspaces and results made inside are the stream's.
 
 Typical use (all tensors on one CUDA device, bf16 [B, H, N, d]):
 
@@ -128,9 +130,34 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _under(stream, device, fn, *args):
+    """A call with stream=: fn(*args) with that stream current, so that the workspaces and results made inside
+    are the stream's own memory. The current stream's would be given to later work there while the
+    kernels still use it. Results may be freed once the current stream has used them."""
+    mine = torch.cuda.current_stream(device) if device.type == "cuda" else None
+    if mine is None or stream.device != mine.device:
+        raise SvooError(f"stream is one of {stream.device}: the tensors must live there")
+    if stream == mine:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    given = {id(t) for t in _tensors(args)}
+    for t in _tensors(out):
+        if id(t) not in given:
+            t.record_stream(mine)
+    return out
+
+
+def _tensors(x):
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, (tuple, list, dict, Plan)):
+        for y in x.values() if isinstance(x, dict) else vars(x).values() if isinstance(x, Plan) else x:
+            yield from _tensors(y)
 
 
 def _need_cuda(*ts):
@@ -281,6 +308,8 @@ def cluster(q, k, cfg: Config, n_text=0, warm=None, workspace=None, dev_err=None
     outputs. warm = (q_cent, k_cent, k_sizes) starts from those centroids
     (SVOO_CLUSTER_WARM); they may be out's own tensors (the previous call's
     result), in which case nothing is copied."""
+    if stream is not None:
+        return _under(stream, q.device, cluster, q, k, cfg, n_text, warm, workspace, dev_err, None, out)
     _need_cuda(q, k)
     sh = make_shape(q, n_text)
     dev = q.device
@@ -302,7 +331,7 @@ def cluster(q, k, cfg: Config, n_text=0, warm=None, workspace=None, dev_err=None
                                _cluster_flags(cfg, warm), _ptr(out["q_assign"]), _ptr(out["k_assign"]),
                                _ptr(out["q_cent"]), _ptr(out["k_cent"]), _ptr(out["q_sizes"]),
                                _ptr(out["k_sizes"]), _ptr(workspace), workspace.numel(), _ptr(err),
-                               _stream(stream)), "svoo_cluster")
+                               _stream()), "svoo_cluster")
     out["dev_err"] = err
     return out
 
@@ -310,6 +339,9 @@ def cluster(q, k, cfg: Config, n_text=0, warm=None, workspace=None, dev_err=None
 def cluster_step(x, cent, sizes, assign, metric_cent=None, metric_sizes=None, n_text=0,
                  workspace=None, dev_err=None, stream=None):
     """One assignment + update half-step (cent, sizes, assign are updated in place)."""
+    if stream is not None:
+        return _under(stream, x.device, cluster_step, x, cent, sizes, assign, metric_cent, metric_sizes, n_text,
+                      workspace, dev_err)
     _need_cuda(x, cent, sizes, assign, metric_cent, metric_sizes)
     sh = make_shape(x, n_text)
     C = cent.shape[-2]
@@ -320,7 +352,7 @@ def cluster_step(x, cent, sizes, assign, metric_cent=None, metric_sizes=None, n_
     err = _err_buf(dev_err, x.device)
     _check(load().svoo_cluster_step(ctypes.byref(sh), _ptr(x), C, _ptr(cent), _ptr(sizes),
                                     _ptr(assign), _ptr(metric_cent), _ptr(metric_sizes), mC,
-                                    _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
+                                    _ptr(workspace), workspace.numel(), _ptr(err), _stream()),
            "svoo_cluster_step")
     return err
 
@@ -329,6 +361,9 @@ def cluster_step_static(x, cent, sizes, assign, metric_cent=None, metric_sizes=N
                         dev_err=None, stream=None):
     """cluster_step with the library's fixed device scratch instead of a
     workspace (for callers that may not allocate device memory)."""
+    if stream is not None:
+        return _under(stream, x.device, cluster_step_static, x, cent, sizes, assign, metric_cent, metric_sizes,
+                      n_text, dev_err)
     _need_cuda(x, cent, sizes, assign, metric_cent, metric_sizes)
     sh = make_shape(x, n_text)
     C = cent.shape[-2]
@@ -336,13 +371,15 @@ def cluster_step_static(x, cent, sizes, assign, metric_cent=None, metric_sizes=N
     err = _err_buf(dev_err, x.device)
     _check(load().svoo_cluster_step_static(ctypes.byref(sh), _ptr(x), C, _ptr(cent), _ptr(sizes),
                                            _ptr(assign), _ptr(metric_cent), _ptr(metric_sizes), mC,
-                                           _ptr(err), _stream(stream)), "svoo_cluster_step_static")
+                                           _ptr(err), _stream()), "svoo_cluster_step_static")
     return err
 
 
 def build_mask(shape: Shape, cl: dict, keep: torch.Tensor, cfg: Config, plan: Optional[Plan] = None,
                workspace=None, dev_err=None, stream=None) -> Plan:
     """Pair masses, keep-ratio / top-p selection and tail merging into `plan`."""
+    if stream is not None:
+        return _under(stream, cl["q_cent"].device, build_mask, shape, cl, keep, cfg, plan, workspace, dev_err)
     dev = cl["q_cent"].device
     keep = keep.to(device=dev, dtype=torch.float32).contiguous()
     _need_cuda(keep, cl["q_cent"], cl["k_cent"], cl["q_sizes"], cl["k_sizes"], cl["q_assign"])
@@ -356,12 +393,14 @@ def build_mask(shape: Shape, cl: dict, keep: torch.Tensor, cfg: Config, plan: Op
                                   _ptr(cl["q_sizes"]), _ptr(cl["k_sizes"]), _ptr(cl["q_assign"]),
                                   _ptr(keep), cfg.n_qc, cfg.n_kc, cfg.select_mode, cfg.block_q,
                                   cfg.merge_rounds, scale, plan.c, _ptr(workspace),
-                                  workspace.numel(), _ptr(err), _stream(stream)), "svoo_build_mask")
+                                  workspace.numel(), _ptr(err), _stream()), "svoo_build_mask")
     return plan
 
 
 def permute(q, k, v, k_assign, plan: Plan, qp=None, kp=None, vp=None, dev_err=None, stream=None):
     """Cluster-order permutation, query tiles and gathered copies (qp, kp, vp)."""
+    if stream is not None:
+        return _under(stream, q.device, permute, q, k, v, k_assign, plan, qp, kp, vp, dev_err)
     _need_cuda(q, k, v, k_assign)
     qp = torch.empty_like(q) if qp is None else qp
     kp = torch.empty_like(k) if kp is None else kp
@@ -370,12 +409,14 @@ def permute(q, k, v, k_assign, plan: Plan, qp=None, kp=None, vp=None, dev_err=No
     cfg = plan.cfg
     _check(load().svoo_permute(ctypes.byref(plan.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(k_assign),
                                cfg.n_qc, cfg.n_kc, cfg.block_q, plan.c, _ptr(qp), _ptr(kp), _ptr(vp),
-                               _ptr(err), _stream(stream)), "svoo_permute")
+                               _ptr(err), _stream()), "svoo_permute")
     return qp, kp, vp
 
 
 def sparse_attn(qp, kp, vp, plan: Plan, out=None, dev_err=None, stream=None):
     """Block-sparse attention over the plan's kept tiles; returns O in token order."""
+    if stream is not None:
+        return _under(stream, qp.device, sparse_attn, qp, kp, vp, plan, out, dev_err)
     _need_cuda(qp, kp, vp)
     out = torch.empty_like(qp) if out is None else out
     cfg = plan.cfg
@@ -383,18 +424,20 @@ def sparse_attn(qp, kp, vp, plan: Plan, out=None, dev_err=None, stream=None):
     err = _err_buf(dev_err, qp.device)
     _check(load().svoo_sparse_attn(ctypes.byref(plan.shape), _ptr(qp), _ptr(kp), _ptr(vp), plan.c,
                                    cfg.n_qc, cfg.n_kc, cfg.block_q, scale, _ptr(out), _ptr(err),
-                                   _stream(stream)), "svoo_sparse_attn")
+                                   _stream()), "svoo_sparse_attn")
     return out
 
 
 def sparse_attention(q, k, v, keep, cfg: Config, n_text=0, dev_err=None, stream=None):
     """The whole path: cluster -> mask + tail merge -> permute -> sparse attention."""
+    if stream is not None:
+        return _under(stream, q.device, sparse_attention, q, k, v, keep, cfg, n_text, dev_err)
     sh = make_shape(q, n_text)
     err = _err_buf(dev_err, q.device)
-    cl = cluster(q, k, cfg, n_text=n_text, dev_err=err, stream=stream)
-    plan = build_mask(sh, cl, keep, cfg, dev_err=err, stream=stream)
-    qp, kp, vp = permute(q, k, v, cl["k_assign"], plan, dev_err=err, stream=stream)
-    out = sparse_attn(qp, kp, vp, plan, dev_err=err, stream=stream)
+    cl = cluster(q, k, cfg, n_text=n_text, dev_err=err)
+    plan = build_mask(sh, cl, keep, cfg, dev_err=err)
+    qp, kp, vp = permute(q, k, v, cl["k_assign"], plan, dev_err=err)
+    out = sparse_attn(qp, kp, vp, plan, dev_err=err)
     return out, dict(cl=cl, plan=plan, dev_err=err)
 
 
@@ -427,6 +470,8 @@ def psa_mask(shape: Shape, grid, block, params: torch.Tensor, cfg: Config,
              plan: Optional[Plan] = None, k_assign: Optional[torch.Tensor] = None, dev_err=None,
              stream=None):
     """Plan of the PSA stripe mask (svoo_psa_mask): returns (plan, k_assign)."""
+    if stream is not None:
+        return _under(stream, params.device, psa_mask, shape, grid, block, params, cfg, plan, k_assign, dev_err)
     _need_cuda(params)
     dev = params.device
     BH, nv = shape.B * shape.H, shape.N - shape.n_text
@@ -438,19 +483,22 @@ def psa_mask(shape: Shape, grid, block, params: torch.Tensor, cfg: Config,
         k_assign = torch.empty(BH, nv, dtype=torch.int32, device=dev)
     err = _err_buf(dev_err, dev)
     _check(load().svoo_psa_mask(ctypes.byref(shape), *grid, *block, _ptr(params), cfg.block_q, plan.c,
-                                _ptr(k_assign), _ptr(err), _stream(stream)), "svoo_psa_mask")
+                                _ptr(k_assign), _ptr(err), _stream()), "svoo_psa_mask")
     return plan, k_assign
 
 
 def psa_attention(q, k, v, grid, block, params: torch.Tensor, n_text=0, block_q: int = 128,
                   scale: Optional[float] = None, dev_err=None, stream=None):
     """The stripe-mask path: PSA plan -> permute -> sparse attention."""
+    if stream is not None:
+        return _under(stream, q.device, psa_attention, q, k, v, grid, block, params, n_text, block_q, scale,
+                      dev_err)
     sh = make_shape(q, n_text)
     cfg = psa_config(grid, block, block_q, scale)
     err = _err_buf(dev_err, q.device)
-    plan, k_assign = psa_mask(sh, grid, block, params, cfg, dev_err=err, stream=stream)
-    qp, kp, vp = permute(q, k, v, k_assign, plan, dev_err=err, stream=stream)
-    out = sparse_attn(qp, kp, vp, plan, dev_err=err, stream=stream)
+    plan, k_assign = psa_mask(sh, grid, block, params, cfg, dev_err=err)
+    qp, kp, vp = permute(q, k, v, k_assign, plan, dev_err=err)
+    out = sparse_attn(qp, kp, vp, plan, dev_err=err)
     return out, dict(plan=plan, k_assign=k_assign, dev_err=err, cfg=cfg)
 
 
@@ -482,9 +530,6 @@ class BlockConfig:
     scale: Optional[float] = None  # default 1/sqrt(d)
 
 
-# stream= runs a call as if that stream were current: what the call reads must be ready there, and stay allocated
-# until the stream has used it; the calls' own workspaces and results are the stream's.
-#
 # The calls below serve single tokens, where the host's own work counts: shapes and
 # workspace sizes are looked up by their numbers, pointers go to ctypes as integers.
 
@@ -497,21 +542,6 @@ def _bshape(*fields) -> "ctypes.Array":
 
 def _dp(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
-
-
-def _under(stream, fn, t, *args):
-    """A call with stream=: fn(t, *args) with that stream current, so that the workspaces and results made
-    inside are the stream's own memory. The current stream's would be given to later work there while
-    the kernels still use it. Results may be freed once the current stream has used them."""
-    if not isinstance(t, torch.Tensor) or t.device != stream.device:
-        raise SvooError(f"stream is one of {stream.device}: the tensors must live there")
-    mine = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        out = fn(t, *args)
-    for x in out if isinstance(out, tuple) else (out,):
-        if x is not None and not any(x is a for a in args):
-            x.record_stream(mine)
-    return out
 
 
 def _call(what: str, t: torch.Tensor, *args):
@@ -612,7 +642,7 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
     `pool` is written in place instead of a new tensor; with last > 0 only the last `last` blocks that
     hold keys of each sequence are renewed (after a token was appended, last=1)."""
     if stream is not None:
-        return _under(stream, block_pool, k, cfg, lengths, pool, last)
+        return _under(stream, k.device, block_pool, k, cfg, lengths, pool, last)
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, N, d] tensor on a CUDA device")
     dev = k.device
@@ -638,7 +668,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
     queries are the last Nq of n_keys; -1: the last Nq of each sequence's lengths."""
     if stream is not None:
-        return _under(stream, block_select, q, pool, cfg, n_keys, lengths, q_start, idx, workspace, dev_err)
+        return _under(stream, q.device, block_select, q, pool, cfg, n_keys, lengths, q_start, idx, workspace, dev_err)
     B, H, Nq, d = _queries(q)
     dev = q.device
     nb = -(-n_keys // cfg.block) if cfg.block > 0 else 0
@@ -662,7 +692,7 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
     """Attention of every query over the blocks in idx; returns (o, lse). No gradient is recorded
     (block_attention records one)."""
     if stream is not None:
-        return _under(stream, block_attn, q, k, v, idx, cfg, lengths, q_start, out, workspace, dev_err)
+        return _under(stream, q.device, block_attn, q, k, v, idx, cfg, lengths, q_start, out, workspace, dev_err)
     args = _block_args(q, k, v, cfg, lengths, q_start)
     B, H, Hkv, Nq, _, _, d = args[:7]
     dev = q.device
@@ -685,8 +715,8 @@ def block_attn_backward(q, k, v, o, lse, grad_o, idx, cfg: BlockConfig, lengths=
                         q_start: Optional[int] = None, workspace=None, dev_err=None, stream=None):
     """Gradient of block_attn: (dq, dk, dv), with idx, o and lse as block_attn had or gave them."""
     if stream is not None:
-        return _under(stream, block_attn_backward, q, k, v, o, lse, grad_o, idx, cfg, lengths, q_start, workspace,
-                      dev_err)
+        return _under(stream, q.device, block_attn_backward, q, k, v, o, lse, grad_o, idx, cfg, lengths, q_start,
+                      workspace, dev_err)
     args = _block_args(q, k, v, cfg, lengths, q_start)
     B, H, Hkv, Nq, _, _, d = args[:7]
     dev = q.device
@@ -759,7 +789,7 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
     idx (from block_select, with its cfg): only the slots of the selected blocks. weight (fp32
     [B, Hkv, cap]): every valid slot's softmax weight, summed over the group's heads, is added to it."""
     if stream is not None:
-        return _under(stream, cache_attn, q, k, v, lengths, idx, cfg, weight, out, workspace, dev_err)
+        return _under(stream, q.device, cache_attn, q, k, v, lengths, idx, cfg, weight, out, workspace, dev_err)
     if q.dim() != 4 or q.shape[2] != 1:
         raise SvooError("q must be [B, H, 1, d]: one token per sequence")
     if idx is not None and cfg is None:
@@ -794,7 +824,7 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
     pos and lengths; see svoo_cache_evict): the first `sink` and last `recent` positions stay, then the
     heaviest slots of each key head. Block means of the cache are to be made anew afterwards."""
     if stream is not None:
-        return _under(stream, cache_evict, k, v, weight, pos, lengths, keep, sink, recent, workspace)
+        return _under(stream, k.device, cache_evict, k, v, weight, pos, lengths, keep, sink, recent, workspace)
     if k.dim() != 4 or not k.is_cuda:
         raise SvooError("k must be a bf16 [B, Hkv, cap, d] tensor on a CUDA device")
     B, Hkv, cap, d = k.shape
