@@ -870,12 +870,8 @@ svoo_status launch_block_lists(const BlockDims& p, const FwdPlan& f, const uint1
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
   const size_t smem = 1024 + list_tile_bytes<D>() + sizeof(ListSmem), cnt = static_cast<size_t>(p.nb) * 4;
-  if (cudaFuncSetAttribute(block_list_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelPlaces>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
-          cudaSuccess)
+  if (!allow_smem(block_list_kernel<D>, smem) || !allow_smem(sel_walk_kernel<kSelCount>, kMaxBlocks * 4) ||
+      !allow_smem(sel_walk_kernel<kSelPlaces>, kMaxBlocks * 4))
     return SVOO_ERR_CUDA;
   sel_walk_kernel<kSelCount><<<dim3(f.nchunk, BHk), 32, cnt, st>>>(lp, idx, lengths, f.chunk, f.nchunk, f.hist,
                                                                    nullptr, nullptr, nullptr);
@@ -910,9 +906,7 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
   const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + tile_list_bytes(p);
-  if (cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+  if (!allow_smem(block_attn_kernel<D>, kMaxSmem)) return SVOO_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares);
   cfg.blockDim = dim3(kFwdThreads);
@@ -924,10 +918,9 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   cluster.val.clusterDim.z = f.shares;
   cfg.attrs = &cluster;
   cfg.numAttrs = f.shares > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, block_attn_kernel<D>, qm, km, vm, p, static_cast<int>(union_cap(p)),
-                         static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2,
-                         static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+  cudaLaunchKernelEx(&cfg, block_attn_kernel<D>, qm, km, vm, p, static_cast<int>(union_cap(p)),
+                     static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2,
+                     static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err));
   return launch_status();
 }
 

@@ -788,14 +788,8 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   const size_t dq_smem = static_cast<size_t>(kDqK + kDqV) * kDqPair * D * 2 + sizeof(DqSmem) + tile_list_bytes(p);
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
   const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
-  if (cudaFuncSetAttribute(block_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(dq_smem)) != cudaSuccess ||
-      cudaFuncSetAttribute(block_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(dkv_smem)) != cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(sel_walk_kernel<kSelList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlocks * 4) !=
-          cudaSuccess)
+  if (!allow_smem(block_dq_kernel<D>, kMaxSmem) || !allow_smem(block_dkv_kernel<D>, dkv_smem) ||
+      !allow_smem(sel_walk_kernel<kSelCount>, kMaxBlocks * 4) || !allow_smem(sel_walk_kernel<kSelList>, kMaxBlocks * 4))
     return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (p.Nq > 0) {

@@ -1071,9 +1071,7 @@ svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* po
   const uint64_t rows = static_cast<uint64_t>(BHk) * s.nbp;
   CUtensorMap pm = {};
   if (s.split && encode_tiled_2d(&pm, s.parts, 2 * rows, D, kKeyTile, 64) != CUDA_SUCCESS) return SVOO_ERR_CUDA;
-  if (cudaFuncSetAttribute(mma_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(mma_sel_smem<D>())) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+  if (!allow_smem(mma_select_kernel<D>, mma_sel_smem<D>())) return SVOO_ERR_CUDA;
   if (s.split)
     pool_split_kernel<D><<<dim3(s.nbp / 64, BHk), 256, 0, st>>>(p.nb, s.nbp, rows * D, pool, s.parts, s.norms);
   mma_select_kernel<D><<<dim3((p.Nq + kRowTile - 1) / kRowTile, BHk), kMmaSelThreads, mma_sel_smem<D>(), st>>>(
@@ -1081,15 +1079,19 @@ svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* po
   return launch_status();
 }
 
+// Queries of a CTA by the blocks: as many as the scores' shared memory allows (32 x
+// 1024 blocks are 128 KB).
+constexpr int sel_most_blocks(int tq) { return tq == 32 ? 1024 : tq == 8 ? 4096 : kMaxBlocks; }
+constexpr size_t sel_scores_smem(int d, int tq, int pitch) {
+  return sizeof(SelWarp) * (kSelThreads / 32) + static_cast<size_t>(tq) * (d + pitch) * 4;
+}
+
 template <int D, int TQ>
 svoo_status launch_select(const BlockDims& p, const void* q, const float* pool, const int32_t* lengths, int32_t* idx,
                           cudaStream_t st) {
   const int pitch = (p.nb + 31) / 32 * 32;
-  const size_t smem = sizeof(SelWarp) * (kSelThreads / 32) + static_cast<size_t>(TQ) * (D + pitch) * 4;
-  if (cudaFuncSetAttribute(block_select_kernel<D, TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
-  block_select_kernel<D, TQ><<<dim3((p.Nq + TQ - 1) / TQ, p.B * p.Hkv), kSelThreads, smem, st>>>(
+  if (!allow_smem(block_select_kernel<D, TQ>, sel_scores_smem(D, TQ, sel_most_blocks(TQ)))) return SVOO_ERR_CUDA;
+  block_select_kernel<D, TQ><<<dim3((p.Nq + TQ - 1) / TQ, p.B * p.Hkv), kSelThreads, sel_scores_smem(D, TQ, pitch), st>>>(
       p, pitch, static_cast<const uint16_t*>(q), pool, lengths, idx);
   return launch_status();
 }
@@ -1097,10 +1099,9 @@ svoo_status launch_select(const BlockDims& p, const void* q, const float* pool, 
 template <int D>
 svoo_status launch_select_d(const BlockDims& p, const void* q, const float* pool, const int32_t* lengths, int32_t* idx,
                             cudaStream_t st) {
-  // as many queries per CTA as the scores' shared memory allows (32 x 1024
-  // blocks are 128 KB), one where there are few
-  if (p.Nq < 8 || p.nb > 4096) return launch_select<D, 1>(p, q, pool, lengths, idx, st);
-  if (p.nb > 1024) return launch_select<D, 8>(p, q, pool, lengths, idx, st);
+  // one query a CTA where there are few
+  if (p.Nq < 8 || p.nb > sel_most_blocks(8)) return launch_select<D, 1>(p, q, pool, lengths, idx, st);
+  if (p.nb > sel_most_blocks(32)) return launch_select<D, 8>(p, q, pool, lengths, idx, st);
   return launch_select<D, 32>(p, q, pool, lengths, idx, st);
 }
 

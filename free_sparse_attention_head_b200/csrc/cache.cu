@@ -33,6 +33,7 @@ constexpr int kCacheThreads = 32 * (kCacheWarps + 1);  // and the producer
 constexpr int kCacheStages = 3;
 constexpr int kHeadRows = 16;  // heads of one CTA
 constexpr int kMaxJoined = 8;  // CTAs of a cluster
+constexpr int kMaxRuns = 256;
 
 struct CacheSmem {
   uint64_t full[kCacheStages], empty[kCacheStages];
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(256)
   for (int g = warp; g < p.G; g += 8) {
     float l2;
     if (runs > 1) {
-      // lanes over the runs (at most 256: eight a lane)
+      // lanes over the runs (at most kMaxRuns: eight a lane)
       float2 v[8];
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
@@ -448,7 +449,7 @@ inline int cache_runs(const BlockDims& p, bool selected) {
   long long runs = tiles / 8 < most ? tiles / 8 : most;
   const long long few = (148 + ctas - 1) / ctas;
   if (runs < few) runs = few < tiles ? few : tiles;
-  if (runs > 256) runs = 256;
+  if (runs > kMaxRuns) runs = kMaxRuns;
   return runs < 1 ? 1 : static_cast<int>(runs);
 }
 
@@ -497,9 +498,7 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
   const size_t smem = cache_smem_bytes<D>();
-  if (cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+  if (!allow_smem(cache_attn_kernel<D>, smem)) return SVOO_ERR_CUDA;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.runs, p.B * p.Hkv, (p.G + kHeadRows - 1) / kHeadRows);
@@ -515,12 +514,10 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
   if (cudaLaunchKernelEx(&cfg, cache_attn_kernel<D>, km, vm, p, static_cast<const uint16_t*>(q), idx, lengths,
                          scale_log2, c.joined ? 1 : 0, weight ? c.scores : nullptr, c.part_o, c.part_ml,
                          static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+    return launch_status();
   const int runs = c.joined ? 1 : c.runs;  // still to join
   const size_t factors = runs > 1 ? static_cast<size_t>(p.G) * runs * 4 : 0;
-  if (factors > 48 * 1024 && cudaFuncSetAttribute(cache_join_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(factors)) != cudaSuccess)
-    return SVOO_ERR_CUDA;
+  if (factors > 48 * 1024 && !allow_smem(cache_join_kernel<D>, kRowTile * kMaxRuns * 4)) return SVOO_ERR_CUDA;
   if (runs > 1 || weight)
     cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, factors, st>>>(
         p, runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight, dev_err);

@@ -65,6 +65,21 @@ CUresult encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t rows, uint
 CUresult encode_token_major(CUtensorMap* map, const void* base, uint64_t B, uint64_t H, uint64_t N, uint64_t cols,
                             uint32_t heads, uint32_t tokens);
 
+// Leave for a kernel to use up to `bytes` of dynamic shared memory. It is a state
+// of the function, not of a launch: every call gives the same number, or a call
+// of another host thread could take it back before this one's launch. A refusal
+// is this call's to report, and is not left for the next launch check.
+inline bool allow_smem(const void* kernel, size_t bytes) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess)
+    return true;
+  cudaGetLastError();
+  return false;
+}
+template <class... Args>
+inline bool allow_smem(void (*kernel)(Args...), size_t bytes) {
+  return allow_smem(reinterpret_cast<const void*>(kernel), bytes);
+}
+
 inline svoo_status launch_status() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SVOO_OK : SVOO_ERR_CUDA;

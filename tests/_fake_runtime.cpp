@@ -19,6 +19,7 @@ struct Config {
   size_t smem;
   cudaStream_t stream;
 } pushed;
+int refuse;  // 1: attributes, 2: launches
 
 cudaError_t note(cudaError_t e) {
   if (e != cudaSuccess) last_error = e;
@@ -30,7 +31,7 @@ constexpr long long kFree = 48 * 1024, kMost = 232448;
 
 cudaError_t launch(const void* f, dim3 g, dim3 b, size_t smem) {
   const long long most = allowed.count(f) ? allowed[f] : kFree;
-  const bool bad = static_cast<long long>(smem) > most || g.x == 0 || g.y == 0 || g.z == 0 || g.y > 65535 || g.z > 65535;
+  const bool bad = refuse == 2 || static_cast<long long>(smem) > most || g.x == 0 || g.y == 0 || g.z == 0 || g.y > 65535 || g.z > 65535;
   char line[512];
   snprintf(line, sizeof line, "launch %s %u %u %u %u %zu %d\n", names[f].c_str(), g.x, g.y, g.z, b.x, smem, bad ? 1 : 0);
   log_text += line;
@@ -43,6 +44,7 @@ extern "C" {
 
 const char* fake_log() { return log_text.c_str(); }
 void fake_clear() { log_text.clear(); }
+void fake_refuse(int what) { refuse = what; }
 int fake_last_error() { return last_error; }
 
 void** __cudaRegisterFatBinary(void*) {
@@ -70,7 +72,7 @@ cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute a, int value) 
     char line[512];
     snprintf(line, sizeof line, "allow %s %d\n", names[f].c_str(), value);
     log_text += line;
-    if (value > kMost) return note(cudaErrorInvalidValue);
+    if (refuse == 1 || value > kMost) return note(cudaErrorInvalidValue);
     allowed[f] = value;
   }
   return cudaSuccess;

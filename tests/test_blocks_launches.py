@@ -31,3 +31,49 @@ def test_maps_of_keys_end_with_their_last_row(host, B, Hkv, first, Nk):
     assert host.attn(shape(**lists)) == 0
     assert any("block_list_kernel" in x.kernel for x in host.launches)
     assert [m[1] for m in host.maps] == [15 * 4096 + 4000] * 2
+
+
+SHAPES = [   # small to large lists and rows of scores, many and few queries, both head dimensions
+    dict(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, cap=Nk, d=d, block=block, n_sel=n_sel, sink=0, local=1, causal=1, q_start=0)
+    for B, H, Hkv, Nq, Nk, block, n_sel in [(1, 1, 1, 1, 64, 64, 2), (2, 8, 2, 40, 5000, 64, 4), (1, 2, 2, 300, 60000, 64, 16),
+                                             (1, 64, 1, 20, 250000, 64, 70), (1, 4, 2, 3000, 90000, 128, 30),
+                                             (3, 6, 6, 7, 1 << 19, 64, 100)] for d in (64, 128)]
+
+
+def calls_of(host, s):
+    f = dict(s)
+    one = shape(**{**f, "Nq": 1})
+    return [lambda: host.select(shape(**f)), lambda: host.attn(shape(**f)), lambda: host.backward(shape(**f)),
+            lambda: host.select(one), lambda: host.cache(one), lambda: host.cache(one, idx=0x40000),
+            lambda: host.cache(one, weight=0x40000)]
+
+
+def test_leave_for_shared_memory_is_the_same_in_every_call(host):
+    """It is a state of the function: a call that gave less could take it from another thread's, before its launch."""
+    given = {}
+    for s in SHAPES:
+        for call in calls_of(host, s):
+            call()
+            for kernel, most in host.allowed:
+                given.setdefault(kernel, set()).add(most)
+    assert len(given) > 10
+    assert {k: v for k, v in given.items() if len(v) > 1} == {}
+
+
+def test_a_refused_call_leaves_no_error_behind(host):
+    """The runtime's last error is the next launch check's to find, whoever makes it."""
+    for s in SHAPES[:4]:
+        for call in calls_of(host, s):
+            host.lib.fake_refuse(1)
+            try:
+                assert call() != 0
+                assert host.lib.fake_last_error() == 0
+            finally:
+                host.lib.fake_refuse(0)
+            host.lib.fake_refuse(2)
+            try:
+                assert call() != 0
+                assert host.lib.fake_last_error() == 0
+            finally:
+                host.lib.fake_refuse(0)
+            call()

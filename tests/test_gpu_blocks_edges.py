@@ -1,6 +1,7 @@
 """Calls at the edges of what the block-selected attention and the cache calls document. Tolerances as in
 test_gpu_blocks.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -148,3 +149,42 @@ def test_another_stream_in_a_graph():
         want = calls(warm)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_two_host_threads_with_different_shapes():
+    """Kernels of different shared-memory needs, called at the same time from two threads with their own streams."""
+    def work(Nk, n_sel, block, seed):
+        q, k, v, g = (t.cuda() for t in (*make(1, 2, 2, 200, Nk, 64, seed=seed), make(1, 2, 2, 200, Nk, 64, seed=seed + 1)[0]))
+        cfg = svoo.BlockConfig(block=block, n_sel=n_sel)
+        one = q[:, :, :1].contiguous()
+
+        def call():
+            pool = svoo.block_pool(k, cfg)
+            idx = svoo.block_select(q, pool, cfg, Nk)
+            o, lse = svoo.block_attn(q, k, v, idx, cfg)
+            tok = svoo.block_select(one, pool, cfg, Nk)
+            return (idx, o, lse, tok, *svoo.block_attn_backward(q, k, v, o, lse, g, idx, cfg),
+                    *svoo.cache_attn(one, k, v, idx=tok, cfg=cfg))
+        return call, call()
+
+    jobs = [work(300, 2, 64, 57), work(60000, 30, 64, 58)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def loop(call, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    got = call()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                        wrong.append("results differ")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=loop, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
