@@ -54,6 +54,11 @@ constexpr size_t fwd_tile_bytes() {
   return static_cast<size_t>(kRowTile) * D * 2 + 4 * static_cast<size_t>(kKeyTile) * D * 2;
 }
 
+// shared memory before a tile's list
+constexpr size_t fwd_smem(int d) {
+  return 1024 + (d == 128 ? fwd_tile_bytes<128>() : fwd_tile_bytes<64>()) + sizeof(FwdSmem);
+}
+
 // byte of the c4-th 16 bytes of row r of a share's part
 template <int D>
 __device__ __forceinline__ uint32_t part_at(int r, int c4) {
@@ -820,6 +825,7 @@ inline int list_piece(const BlockDims& p) {
 
 struct FwdPlan {
   bool by_blocks;
+  BlockDims tile;  // as row tiles take them
   int shares;
   int ktiles, chunk, nchunk, piece;
   long long max_items;
@@ -832,7 +838,8 @@ struct FwdPlan {
 FwdPlan fwd_plan(const BlockDims& p, int d, void* ws) {
   FwdPlan f = {};
   f.by_blocks = by_blocks(p);
-  f.shares = f.by_blocks ? 1 : block_shares(p);
+  f.tile = fit_tile(p, kMaxSmem - fwd_smem(d));
+  f.shares = f.by_blocks ? 1 : block_shares(f.tile);
   Carver c(ws);
   size_t parts = 0;
   if (f.by_blocks) {
@@ -899,18 +906,18 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
     return launch_block_lists<D>(p, f, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                                  static_cast<const uint16_t*>(v), idx, lengths, scale_log2, static_cast<uint16_t*>(o),
                                  lse, dev_err, st);
+  const BlockDims& t = f.tile;
   CUtensorMap qm, km, vm;
-  const uint64_t rows = mapped_key_rows(p);
-  if (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
+  const uint64_t rows = mapped_key_rows(t);
+  if (encode_token_major(&qm, q, t.B, t.H, t.Nq, D, t.G, t.tpt) != CUDA_SUCCESS ||
       encode_tiled_2d(&km, k, rows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, rows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t smem = 1024 + fwd_tile_bytes<D>() + sizeof(FwdSmem) + tile_list_bytes(p);
   if (!allow_smem(block_attn_kernel<D>, kMaxSmem)) return SVOO_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.Nq + p.tpt - 1) / p.tpt, p.B * p.Hkv, f.shares);
+  cfg.gridDim = dim3((t.Nq + t.tpt - 1) / t.tpt, t.B * t.Hkv, f.shares);
   cfg.blockDim = dim3(kFwdThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = fwd_smem(D) + tile_list_bytes(t);
   cfg.stream = st;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -918,7 +925,7 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   cluster.val.clusterDim.z = f.shares;
   cfg.attrs = &cluster;
   cfg.numAttrs = f.shares > 1 ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, block_attn_kernel<D>, qm, km, vm, p, static_cast<int>(union_cap(p)),
+  cudaLaunchKernelEx(&cfg, block_attn_kernel<D>, qm, km, vm, t, static_cast<int>(union_cap(t)),
                      static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), idx, lengths, scale_log2,
                      static_cast<uint16_t*>(o), lse, static_cast<int*>(dev_err));
   return launch_status();

@@ -58,6 +58,12 @@ struct DqSmem {
   float delta[kRowTile];
 };
 
+// shared memory before a tile's list
+template <int D>
+constexpr size_t dq_smem() {
+  return static_cast<size_t>(kDqK + kDqV) * kDqPair * D * 2 + sizeof(DqSmem);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
     block_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
@@ -776,16 +782,16 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   const int BHk = p.B * p.Hkv;
   const uint16_t *qp = static_cast<const uint16_t*>(q), *kp = static_cast<const uint16_t*>(k),
                  *vp = static_cast<const uint16_t*>(v), *gp = static_cast<const uint16_t*>(go);
+  const BlockDims t = fit_tile(p, kMaxSmem - dq_smem<D>());  // as row tiles take them
   CUtensorMap qm, gm, om, km, vm;
   const uint64_t krows = mapped_key_rows(p);
-  if (p.Nq > 0 && (encode_token_major(&qm, q, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
-                   encode_token_major(&gm, go, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS ||
-                   encode_token_major(&om, o, p.B, p.H, p.Nq, D, p.G, p.tpt) != CUDA_SUCCESS))
+  if (p.Nq > 0 && (encode_token_major(&qm, q, t.B, t.H, t.Nq, D, t.G, t.tpt) != CUDA_SUCCESS ||
+                   encode_token_major(&gm, go, t.B, t.H, t.Nq, D, t.G, t.tpt) != CUDA_SUCCESS ||
+                   encode_token_major(&om, o, t.B, t.H, t.Nq, D, t.G, t.tpt) != CUDA_SUCCESS))
     return SVOO_ERR_CUDA;
   if (encode_tiled_2d(&km, k, krows, D, kKeyTile, 64) != CUDA_SUCCESS ||
       encode_tiled_2d(&vm, v, krows, D, kKeyTile, 64) != CUDA_SUCCESS)
     return SVOO_ERR_CUDA;
-  const size_t dq_smem = static_cast<size_t>(kDqK + kDqV) * kDqPair * D * 2 + sizeof(DqSmem) + tile_list_bytes(p);
   const size_t dkv_smem = dkv_tile_bytes<D>() + sizeof(DkvSmem);
   const size_t cnt_smem = static_cast<size_t>(p.nb) * 4;
   if (!allow_smem(block_dq_kernel<D>, kMaxSmem) || !allow_smem(block_dkv_kernel<D>, dkv_smem) ||
@@ -801,8 +807,9 @@ svoo_status launch_block_grad(const BlockDims& p, const void* q, const void* k, 
   if (p.Nq > 0) {
     sel_walk_kernel<kSelList><<<dim3(g.nchunk, BHk), 32, cnt_smem, st>>>(p, idx, lengths, g.chunk, g.nchunk, g.hist,
                                                                      g.start, g.list, nullptr);
-    block_dq_kernel<D><<<dim3((p.Nq + p.tpt - 1) / p.tpt, BHk), kDqThreads, dq_smem, st>>>(
-        qm, gm, om, km, vm, p, static_cast<int>(union_cap(p)), kp, vp, lse, g.delta, idx, lengths, scale, scale_log2, static_cast<uint16_t*>(dq), dev_err);
+    block_dq_kernel<D><<<dim3((t.Nq + t.tpt - 1) / t.tpt, BHk), kDqThreads, dq_smem<D>() + tile_list_bytes(t), st>>>(
+        qm, gm, om, km, vm, t, static_cast<int>(union_cap(t)), kp, vp, lse, g.delta, idx, lengths, scale, scale_log2,
+        static_cast<uint16_t*>(dq), dev_err);
   }
   block_dkv_kernel<D><<<static_cast<unsigned>(g.max_items), kDkvThreads, dkv_smem, st>>>(
       p, g.ktiles, g.piece, qp, kp, vp, gp, lse, g.delta, lengths, g.total, g.start, g.list, g.items, g.counts, scale,

@@ -165,6 +165,15 @@ inline size_t tile_list_bytes(const BlockDims& p) {
   const size_t words = (p.nb + 31) / 32;
   return 4 * (union_cap(p) * (p.nsub + (p.tpt + 31) / 32) + words + (words + 1) / 2);
 }
+// Queries of a row tile, at most: as many as keep its list within `room` bytes of
+// shared memory (long sequences of few heads a group name more blocks than fit
+// beside the tiles; the rows behind the last query then work for nothing). One
+// query's 256 slots of blocks of 1024 keys are 20 KB.
+inline BlockDims fit_tile(BlockDims p, size_t room) {
+  while (p.tpt > 1 && tile_list_bytes(p) > room) --p.tpt;
+  return p;
+}
+
 __device__ __forceinline__ TileList tile_list(const BlockDims& p, int cap, void* at) {
   TileList t;
   const int w = (p.nb + 31) / 32;

@@ -1,4 +1,6 @@
 """What the block-selected attention and the cache calls ask of the CUDA runtime, checked without a GPU."""
+import random
+
 import pytest
 import torch
 
@@ -77,3 +79,27 @@ def test_a_refused_call_leaves_no_error_behind(host):
             finally:
                 host.lib.fake_refuse(0)
             call()
+
+
+def draw(rng):
+    """A shape from all that svoo_block_shape allows, extremes first."""
+    d, block = rng.choice([64, 128]), rng.choice([64, 64, 128, 192, 1024])
+    Hkv = rng.choice([1, 2, 5])
+    G = rng.choice([1, 1, 2, 3, 8, 40, 128])
+    Nk = rng.choice([1 << 20, 1 << 20, 262144, 360000, rng.randint(1, 1 << 20), rng.randint(1, 5000)])
+    n_sel = rng.choice([256, 128, 64, 48, 32, 16, rng.randint(1, 256)])
+    causal = rng.randint(0, 1)
+    sink = rng.randint(0, min(2, n_sel - causal))
+    return dict(B=rng.randint(1, 2), H=Hkv * G, Hkv=Hkv, Nq=rng.choice([1, 7, 63, 200, 5000]), Nk=Nk, cap=Nk, d=d, block=block,
+                n_sel=n_sel, sink=sink, local=causal, causal=causal, q_start=rng.choice([-1, 0, Nk - 1]))
+
+
+def test_every_shape_of_the_documented_range_is_launched(host):
+    rng = random.Random(1)
+    shapes = [dict(B=1, H=1, Hkv=1, Nq=200, Nk=Nk, cap=Nk, d=128, block=block, n_sel=n_sel, sink=1, local=1, causal=1, q_start=-1)
+              for Nk, block, n_sel in [(262144, 64, 32), (360000, 128, 32), (524288, 64, 64), (1 << 20, 64, 256),
+                                       (1 << 20, 1024, 256), (1 << 20, 64, 16)]]
+    for s in shapes + [draw(rng) for _ in range(400)]:
+        for call in calls_of(host, s):
+            assert call() == 0, s
+            assert not any(x.bad for x in host.launches), s

@@ -188,3 +188,31 @@ def test_two_host_threads_with_different_shapes():
     for t in threads:
         t.join()
     assert not wrong, wrong[:3]
+
+
+@pytest.mark.parametrize("case", [
+    # H, Hkv, Nq, Nk, d, block, n_sel: lists of a row tile's blocks that fit beside the tiles, and that do not
+    (1, 1, 150, 200_000, 128, 64, 32),
+    (1, 1, 150, 262_144, 128, 64, 32),        # the gradient's
+    (2, 2, 300, 524_288 - 5, 128, 64, 64),    # the forward call's too
+    (2, 1, 140, 360_000, 128, 128, 128),
+    (1, 1, 200, 600_001, 64, 64, 200),
+    (1, 1, 9, 1 << 20, 128, 1024, 256),
+], ids=str)
+def test_long_sequences_of_few_heads(case):
+    H, Hkv, Nq, Nk, d, block, n_sel = case
+    gen = torch.Generator(device="cuda").manual_seed(59)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, g = r(1, H, Nq, d), r(1, Hkv, Nk, d), r(1, Hkv, Nk, d), r(1, H, Nq, d)
+    cfg = svoo.BlockConfig(block=block, n_sel=n_sel)
+    qc, kc, vc = (t.clone().requires_grad_(True) for t in (q, k, v))
+    o, aux = svoo.block_attention(qc, kc, vc, cfg)
+    got = torch.autograd.grad(o, (qc, kc, vc), g)
+    svoo.check_device_errors(aux["dev_err"])
+    q, k, v, g = (t.cpu() for t in (q, k, v, g))
+    idx = aux["idx"].cpu()
+    assert torch.equal(idx, ref.select(q, aux["pool"].cpu(), cfg, Nk))
+    o64, l64, *want = ref.attn(q, k, v, idx, cfg, grad_o=g)
+    check_out(o.detach(), aux["lse"], o64, l64, float(v.float().abs().max()))
+    for name, x, y in zip(("dq", "dk", "dv"), got, want):
+        close(x, y, name)
