@@ -595,6 +595,18 @@ def _key_rows(what: str, t: torch.Tensor, device) -> int:
     return cap
 
 
+def _first_position(q_start: Optional[int], n_keys: int, Nq: int, causal) -> int:
+    """q_start of a BlockShape: None is the last Nq of n_keys. (-1 means the last Nq of every sequence's own
+    length there, so a position before the first is never passed on.) Without causality positions mean nothing."""
+    if q_start is not None:
+        return q_start
+    if not causal:
+        return 0
+    if Nq > n_keys:
+        raise SvooError(f"{Nq} queries cannot be the last of {n_keys} keys: pass q_start")
+    return n_keys - Nq
+
+
 def _block_args(q, k, v, cfg: BlockConfig, lengths, q_start):
     """The fields of a call's BlockShape, after checking its tensors."""
     B, H, Nq, d = _queries(q)
@@ -607,7 +619,7 @@ def _block_args(q, k, v, cfg: BlockConfig, lengths, q_start):
         raise SvooError("q, k and v must agree in batch and head dimension")
     _need("lengths", torch.int32, dev, (B,), lengths)
     return (B, H, Hkv, Nq, Nk, cap, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
-            Nk - Nq if q_start is None else q_start)
+            _first_position(q_start, Nk, Nq, cfg.causal))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -666,7 +678,9 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     """The blocks that every query selects: int32 [B, Hkv, Nq, n_sel], ascending, -1 behind them.
 
     n_keys: key rows per head (an upper bound of lengths). q_start: position of query 0; None: the
-    queries are the last Nq of n_keys; -1: the last Nq of each sequence's lengths."""
+    queries are the last Nq of n_keys (which cannot be fewer); -1: the last Nq of each sequence's
+    lengths, of which a longer Nq has some before the first token: those select nothing. Not causal:
+    positions mean nothing, and there may be more queries than keys."""
     if stream is not None:
         return _under(stream, q.device, block_select, q, pool, cfg, n_keys, lengths, q_start, idx, workspace, dev_err)
     B, H, Nq, d = _queries(q)
@@ -680,7 +694,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     else:
         _need("idx", torch.int32, dev, (B, Hkv, Nq, cfg.n_sel), idx)
     args = (B, H, Hkv, Nq, n_keys, n_keys, d, cfg.block, cfg.n_sel, cfg.sink, cfg.local, 1 if cfg.causal else 0,
-            n_keys - Nq if q_start is None else q_start)
+            _first_position(q_start, n_keys, Nq, cfg.causal))
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
     _call("svoo_block_select", q, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
           idx.data_ptr(), ws_at, ws_n, _dp(dev_err))
@@ -764,7 +778,7 @@ class _BlockAttn(torch.autograd.Function):
 def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[int] = None, dev_err=None):
     """The whole path on the current stream: block means -> selection -> attention over the selected
     blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
-    right-padded batch. Differentiable in q, k and v (the selection is a constant of the gradient; the
+    right-padded batch; q_start as in block_select. Differentiable in q, k and v (the selection is a constant of the gradient; the
     gradient's gradient is not offered). Returns (o, dict(idx, lse, pool, dev_err))."""
     args = _block_args(q, k, v, cfg, lengths, q_start)
     scale = _block_scale(cfg, args[6])

@@ -1,0 +1,16 @@
+"""Arguments that the Python entry points settle themselves, without a GPU."""
+import pytest
+
+import free_sparse_attention_head_b200 as svoo
+
+
+def test_positions_of_the_queries():
+    """-1 is the C call's word for the end of every sequence: no default may come out as it by arithmetic."""
+    first = svoo._first_position
+    assert first(None, 300, 100, True) == 200 and first(None, 300, 300, True) == 0
+    for Nq in (301, 302, 1000):
+        with pytest.raises(svoo.SvooError):
+            first(None, 300, Nq, True)
+        assert first(None, 300, Nq, False) == 0    # positions mean nothing
+    for given in (-1, 0, 7):
+        assert first(given, 300, 301, True) == first(given, 300, 301, False) == given

@@ -216,3 +216,31 @@ def test_long_sequences_of_few_heads(case):
     check_out(o.detach(), aux["lse"], o64, l64, float(v.float().abs().max()))
     for name, x, y in zip(("dq", "dk", "dv"), got, want):
         close(x, y, name)
+
+
+@pytest.mark.parametrize("Nq", [201, 202, 500])
+def test_more_queries_than_keys(Nq):
+    """Not causal: every query sees all keys; a causal call says where its queries are."""
+    Nk, lengths = 200, [200, 130]
+    q, k, v = make(2, 4, 2, Nq, Nk, 64, seed=60)
+    g = make(2, 4, 2, Nq, Nk, 64, seed=61)[0]
+    cfg = svoo.BlockConfig(block=64, n_sel=2, sink=1, local=0, causal=False)
+    qc, kc, vc = (t.cuda().requires_grad_(True) for t in (q, k, v))
+    o, aux = svoo.block_attention(qc, kc, vc, cfg, lens(lengths))
+    got = torch.autograd.grad(o, (qc, kc, vc), g.cuda())
+    assert torch.equal(aux["idx"].cpu(), ref.select(q, aux["pool"].cpu(), cfg, Nk, lengths, 0))
+    o64, l64, *want = ref.attn(q, k, v, aux["idx"].cpu(), cfg, lengths, 0, grad_o=g)
+    check_out(o.detach(), aux["lse"], o64, l64, float(v.float().abs().max()))
+    for name, x, y in zip(("dq", "dk", "dv"), got, want):
+        close(x, y, name)
+    causal = svoo.BlockConfig(block=64, n_sel=2)
+    args = [t.detach() for t in (qc, kc, vc)]
+    with pytest.raises(svoo.SvooError):
+        svoo.block_attention(*args, causal, lens(lengths))
+    with pytest.raises(svoo.SvooError):
+        svoo.block_select(args[0], aux["pool"], causal, Nk, lens(lengths))
+    for q_start in (-1, 0):   # the queries before the first token, or behind the last, see nothing
+        o, aux = svoo.block_attention(*args, causal, lens(lengths), q_start)
+        assert torch.equal(aux["idx"].cpu(), ref.select(q, aux["pool"].cpu(), causal, Nk, lengths, q_start))
+        o64, l64 = ref.attn(q, k, v, aux["idx"].cpu(), causal, lengths, q_start)
+        check_out(o, aux["lse"], o64, l64, float(v.float().abs().max()))
