@@ -9,7 +9,9 @@
 // scores go to the lower block. The choice is that of an fp64 evaluation:
 // scores are computed in fp32, and where the last block taken and the first
 // one left out lie within twice the error bound of each other, the candidates
-// around that border are scored again in fp64.
+// around that border are scored again in fp64. The bound counts the sum over the
+// heads too, whose fp32 additions err by the heads' sizes, not by the sum's:
+// (G - 1) 2^-24 |A| |pool| with A_d = sum |q_hd|, and |A|^2 <= G sum q_hd^2.
 //
 // When causal, only blocks that end before the query's own block are scored,
 // and the own block is always kept: a mean never shows a query a key behind it.
@@ -113,7 +115,8 @@ __global__ void __launch_bounds__(kSelThreads)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelWarp* amb = reinterpret_cast<SelWarp*>(smem_raw);
   float* qs = reinterpret_cast<float*>(amb + kSelThreads / 32);  // [TQ][D]
-  float* sc = qs + TQ * D;                                       // [TQ][pitch]
+  float* hs = qs + TQ * D;                                       // [TQ][D] sums of the heads' squares
+  float* sc = hs + TQ * D;                                       // [TQ][pitch]
   __shared__ int pool_norm2;                                     // largest |pool[c]|^2 seen, as bits
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y / p.Hkv, hk = blockIdx.y - b * p.Hkv;
@@ -125,11 +128,16 @@ __global__ void __launch_bounds__(kSelThreads)
   if (tid == 0) pool_norm2 = 0;
   for (int i = tid; i < TQ * D; i += kSelThreads) {
     const int t = i / D, d = i - t * D;
-    float a = 0.f;
+    float a = 0.f, sq = 0.f;
     if (t < nt)
 #pragma unroll 8
-      for (int g = 0; g < p.G; ++g) a += bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + t) * D + d]);
+      for (int g = 0; g < p.G; ++g) {
+        const float x = bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + t) * D + d]);
+        a += x;
+        sq = fmaf(x, x, sq);
+      }
     qs[i] = a;
+    hs[i] = sq;
   }
   // the tile's last query inside the sequence has the most candidates
   int most = (len + p.block - 1) / p.block;
@@ -239,13 +247,20 @@ __global__ void __launch_bounds__(kSelThreads)
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       }
-      float q2 = 0.f;
-      for (int d = lane; d < D; d += 32) q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
+      float q2 = 0.f, h2 = 0.f;
+      for (int d = lane; d < D; d += 32) {
+        q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
+        h2 += hs[t * D + d];
+      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-      // |fp32 score - score| <= (D + G + 2) 2^-24 sum |q_d pool_d| <= (D + G + 2) 2^-24 |q||pool|,
-      // and the norms themselves are good to far better than the 1.5 spent on them
-      const float e2 = 3.f * (D + p.G + 2) * 5.9604645e-8f * sqrtf(q2) * sqrtf(__int_as_float(pool_norm2));
+      for (int o = 16; o; o >>= 1) {
+        q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+        h2 += __shfl_xor_sync(0xffffffffu, h2, o);
+      }
+      // |fp32 score - score| <= 2^-24 ((D + 2) |q| + (G - 1) |A|) |pool|, and the norms themselves
+      // are good to far better than the 1.5 spent on them
+      const float e2 = 3.f * 5.9604645e-8f * ((D + 2) * sqrtf(q2) + (p.G - 1) * sqrtf(p.G * h2)) *
+                       sqrtf(__int_as_float(pool_norm2));
       int n = cd.hi - cd.lo, n_hi = 1;
       for (int it = 0; it < 48 && n != m; ++it) {
         const float mid = probe_at(lo, hi, n, n_hi, m, it);
@@ -364,7 +379,8 @@ __global__ void __launch_bounds__(kSelThreads)
 // what is left is below 2^-16 of the value), and hi.hi + hi.lo + lo.hi
 // accumulate in fp32. With u = 2^-16 a part product's neglected rest is at most
 // 3 u sum |q_d pool_d|, the 3 D additions at most 3 D 2^-23 of the same sum, and
-// the sum at most |q||pool|: that is the error bound of the border test.
+// the sum at most |q||pool|: with the sum over the heads (above) that is the error
+// bound of the border test.
 //
 // A thread owns a query (= TMEM lane) and streams its scores, 64 blocks a step,
 // through a list of at most kList candidates: a score enters when it is not
@@ -508,18 +524,21 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
     tmem_alloc(smem_u32(&S->tmem_base), 256);
     tmem_relinquish();
   }
+  // the heads' squares, summed over 8 columns each, where the lists begin later
+  constexpr int kChunks = D / 8;
+  float* squares = lv;  // [128][kChunks]
   if (steps > 0) {
     // group sums: coalesced loads (four rows at a time in flight), fp32 sums,
     // bf16 parts to shared memory
-    constexpr int kChunks = D / 8, kStep = kMmaSelThreads / kChunks;
+    constexpr int kStep = kMmaSelThreads / kChunks;
     static_assert(kMmaSelThreads % kChunks == 0, "a thread keeps its columns");
     const int ch = tid % kChunks;
     for (int r0 = tid / kChunks; r0 < kRowTile; r0 += 4 * kStep) {
-      float a[4][8];
+      uint64_t a[4][4], sq[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of columns: their sums, and their squares'
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) a[k][i] = 0ull;
 #pragma unroll 2
       for (int g = 0; g < p.G; ++g) {
         uint4 x[4];
@@ -534,8 +553,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            a[k][2 * i] += __uint_as_float(w[i] << 16);
-            a[k][2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+            const uint64_t y = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            a[k][i] = f2add(a[k][i], y);
+            sq[k] = f2fma(y, y, sq[k]);
           }
         }
       }
@@ -546,10 +566,14 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
         uint32_t h[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[i] = pack_bf16x2(a[k][2 * i], a[k][2 * i + 1]);
-          l[i] = pack_bf16x2(a[k][2 * i] - __uint_as_float(h[i] << 16),
-                             a[k][2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+          float x, y;
+          f2unpack(a[k][i], x, y);
+          h[i] = pack_bf16x2(x, y);
+          l[i] = pack_bf16x2(x - __uint_as_float(h[i] << 16), y - __uint_as_float(h[i] & 0xffff0000u));
         }
+        float x, y;
+        f2unpack(sq[k], x, y);
+        squares[r * kChunks + ch] = x + y;
         const uint32_t off = r * D * 2 + ((ch ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(stage + off) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(stage + kHalf + off) = make_uint4(l[0], l[1], l[2], l[3]);
@@ -575,9 +599,14 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
 #pragma unroll
     for (int i = 0; i < kMeans; ++i) mean[kAhead ? i : 0] = mean_at(i);
   }
-  float q2 = 0.f;
+  float q2 = 0.f, h2 = 0.f;
   if (steps > 0 && warp < 4) {
-    // this query's parts into tensor memory, and its norm
+    // this query's parts into tensor memory, and its norms
+#pragma unroll
+    for (int i = 0; i < kChunks; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(squares + tid * kChunks + i);
+      h2 += (x.x + x.y) + (x.z + x.w);
+    }
 #pragma unroll
     for (int c4 = 0; c4 < D / 32; ++c4) {
       uint32_t h[16], l[16];
@@ -634,7 +663,8 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   const bool all = cd.nc <= p.n_sel;                  // no choice to make
   const int m = p.n_sel - (cd.nc - (cd.hi - cd.lo));  // to be chosen by score
   // twice the error bound, with a tenth more for the fp32 norms and this product
-  const float e2 = 2.2f * (3.f * 1.52587890625e-5f + 3.f * D * 1.1920929e-7f) * sqrtf(q2) * sqrtf(S->pool_norm2);
+  const float e2 = 2.2f * ((3.f * 1.52587890625e-5f + 3.f * D * 1.1920929e-7f) * sqrtf(q2) +
+                           (p.G - 1) * 5.9604645e-8f * sqrtf(p.G * h2)) * sqrtf(S->pool_norm2);
   int cnt = 0;
   bool hard = false;
   float* mv = lv + (tid & 127);
@@ -1083,7 +1113,7 @@ svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* po
 // 1024 blocks are 128 KB).
 constexpr int sel_most_blocks(int tq) { return tq == 32 ? 1024 : tq == 8 ? 4096 : kMaxBlocks; }
 constexpr size_t sel_scores_smem(int d, int tq, int pitch) {
-  return sizeof(SelWarp) * (kSelThreads / 32) + static_cast<size_t>(tq) * (d + pitch) * 4;
+  return sizeof(SelWarp) * (kSelThreads / 32) + static_cast<size_t>(tq) * (2 * d + pitch) * 4;
 }
 
 template <int D, int TQ>

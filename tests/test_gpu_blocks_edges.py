@@ -244,3 +244,20 @@ def test_more_queries_than_keys(Nq):
         assert torch.equal(aux["idx"].cpu(), ref.select(q, aux["pool"].cpu(), causal, Nk, lengths, q_start))
         o64, l64 = ref.attn(q, k, v, aux["idx"].cpu(), causal, lengths, q_start)
         check_out(o, aux["lse"], o64, l64, float(v.float().abs().max()))
+
+
+@pytest.mark.parametrize("Nq", [1, 7, 40, 64, 200])      # both selection kernels, one to 32 queries a CTA
+@pytest.mark.parametrize("G,d,block,n_sel", [(3, 64, 64, 6), (4, 128, 64, 12), (16, 64, 128, 5)])
+def test_selection_of_heads_that_cancel(Nq, G, d, block, n_sel):
+    """A group's sum is small beside its heads: fp32 additions of them are off by more than the scores' own bound."""
+    Hkv, Nk = 2, 6000
+    q, k, _ = make(1, G * Hkv, Hkv, Nq, Nk, d, seed=62)
+    q = q.view(1, Hkv, G, Nq, d).clone()
+    q[:, :, 0] *= 2.0 ** 17
+    q[:, :, 2] = -q[:, :, 0]
+    q = q.view(1, Hkv * G, Nq, d)
+    for causal in (True, False):
+        cfg = svoo.BlockConfig(block=block, n_sel=n_sel, sink=1, local=int(causal), causal=causal)
+        pool = svoo.block_pool(k.cuda(), cfg)
+        idx = svoo.block_select(q.cuda(), pool, cfg, Nk)
+        assert torch.equal(idx.cpu(), ref.select(q, pool.cpu(), cfg, Nk))
