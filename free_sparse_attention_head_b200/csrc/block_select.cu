@@ -82,6 +82,14 @@ __device__ __forceinline__ float probe_at(float lo, float hi, int n_lo, int n_hi
   return lo + f * (hi - lo);
 }
 
+// A norm for an error bound from its square in fp32, at least 1e-18: squares of
+// less than that lose bits there. It is infinite where the square is: the row is
+// then decided in fp64 throughout.
+__device__ __forceinline__ float bound_norm(float square) { return sqrtf(fmaxf(square, 1e-36f)); }
+// (G - 1) |A| of a sum over G heads, from the sum of their squares
+__device__ __forceinline__ float heads_error(int G, float h2) { return G > 1 ? (G - 1) * bound_norm(G * h2) : 0.f; }
+constexpr float kMostFp32 = 3.402823466e38f;
+
 struct SelWarp {
   double val[kAmb];
   int blk[kAmb];
@@ -213,6 +221,25 @@ __global__ void __launch_bounds__(kSelThreads)
     float cut = INFINITY;   // scores above it are taken
     bool incl = false;      // ... and those equal to it
     if (!all && m > 0) {
+      float q2 = 0.f, h2 = 0.f;
+      for (int d = lane; d < D; d += 32) {
+        q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
+        h2 += hs[t * D + d];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+        h2 += __shfl_xor_sync(0xffffffffu, h2, o);
+      }
+      // |fp32 score - score| <= 2^-24 ((D + 2) |q| + (G - 1) |A|) |pool|, and the norms themselves
+      // are good to far better than the 1.5 spent on them
+      float e2 = 3.f * 5.9604645e-8f * ((D + 2) * bound_norm(q2) + heads_error(p.G, h2)) *
+                 bound_norm(__int_as_float(pool_norm2));
+      if (e2 > kMostFp32) {  // no fp32 score says anything: all of them stand at the border
+        e2 = 0.f;
+        for (int c = cd.lo + lane; c < cd.hi; c += 32) s[c] = 0.f;
+        __syncwarp();
+      }
       // the m-th largest score, between `lo`, which n_lo >= m scores reach, and
       // `hi`, which fewer do; up to 32 a lane in registers
       constexpr int kHeld = 32;
@@ -247,20 +274,6 @@ __global__ void __launch_bounds__(kSelThreads)
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       }
-      float q2 = 0.f, h2 = 0.f;
-      for (int d = lane; d < D; d += 32) {
-        q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
-        h2 += hs[t * D + d];
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-        h2 += __shfl_xor_sync(0xffffffffu, h2, o);
-      }
-      // |fp32 score - score| <= 2^-24 ((D + 2) |q| + (G - 1) |A|) |pool|, and the norms themselves
-      // are good to far better than the 1.5 spent on them
-      const float e2 = 3.f * 5.9604645e-8f * ((D + 2) * sqrtf(q2) + (p.G - 1) * sqrtf(p.G * h2)) *
-                       sqrtf(__int_as_float(pool_norm2));
       int n = cd.hi - cd.lo, n_hi = 1;
       for (int it = 0; it < 48 && n != m; ++it) {
         const float mid = probe_at(lo, hi, n, n_hi, m, it);
@@ -401,7 +414,7 @@ struct MmaSelSmem {
   uint64_t full[2], empty[2], s_full[2], s_empty[2], mma_final;
   uint32_t tmem_base;
   int abort;
-  int hard;             // queries whose ties overran the list
+  int hard;             // queries whose ties overran the list, or whose norms are out of fp32's range
   float pool_norm2;
 };
 
@@ -663,10 +676,10 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   const bool all = cd.nc <= p.n_sel;                  // no choice to make
   const int m = p.n_sel - (cd.nc - (cd.hi - cd.lo));  // to be chosen by score
   // twice the error bound, with a tenth more for the fp32 norms and this product
-  const float e2 = 2.2f * ((3.f * 1.52587890625e-5f + 3.f * D * 1.1920929e-7f) * sqrtf(q2) +
-                           (p.G - 1) * 5.9604645e-8f * sqrtf(p.G * h2)) * sqrtf(S->pool_norm2);
+  const float e2 = 2.2f * ((3.f * 1.52587890625e-5f + 3.f * D * 1.1920929e-7f) * bound_norm(q2) +
+                           5.9604645e-8f * heads_error(p.G, h2)) * bound_norm(S->pool_norm2);
   int cnt = 0;
-  bool hard = false;
+  bool hard = !all && m > 0 && e2 > kMostFp32;  // decided in fp64: no fp32 score says anything
   float* mv = lv + (tid & 127);
   uint16_t* mi = li + (tid & 127);
 
@@ -712,8 +725,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       mbar_wait_cleanup(smem_u32(&S->mma_final), 0);
     }
   } else {
-    const int lo_c = all || m <= 0 ? 0 : cd.lo, hi_c = all || m <= 0 ? 0 : cd.hi;
-    float cut = -3.402823466e38f;  // nothing below it can be among the m best
+    const bool list = !all && m > 0 && !hard;
+    const int lo_c = list ? cd.lo : 0, hi_c = list ? cd.hi : 0;
+    float cut = -kMostFp32;  // nothing below it can be among the m best
     float s[kKeyTile];
     // Raises the cut to just below a value that m to m + 6 of the list's entries
     // and this step's scores reach, and packs the list.
@@ -992,8 +1006,8 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   __syncthreads();
   const bool fine = !*abort;
   if (fine && S->hard && warp < 4) {
-    // Rows whose ties overran the list, one at a time: every free candidate in
-    // fp64 (a lane each) where the lists were, the m-th best by bisection.
+    // Such rows, one at a time: every free candidate in fp64 (a lane each) where
+    // the lists were, the m-th best by bisection.
     double* ex = reinterpret_cast<double*>(lv);
     for (int w = 0; w < 4; ++w) {
       asm volatile("bar.sync 1, 128;" ::: "memory");

@@ -261,3 +261,20 @@ def test_selection_of_heads_that_cancel(Nq, G, d, block, n_sel):
         pool = svoo.block_pool(k.cuda(), cfg)
         idx = svoo.block_select(q.cuda(), pool, cfg, Nk)
         assert torch.equal(idx.cpu(), ref.select(q, pool.cpu(), cfg, Nk))
+
+
+@pytest.mark.parametrize("q_exp,k_exp", [(70, 0), (0, 70), (70, 70), (-80, 0), (0, -80), (-70, -50), (120, -100), (-120, 110)])
+@pytest.mark.parametrize("Nq", [1, 40, 200])
+def test_selection_far_from_one(Nq, q_exp, k_exp):
+    """Norms whose squares, or scores that themselves, are outside fp32: blocks a few keys' last bits apart."""
+    Hkv, G, d, block, Nk = 2, 2, 64, 64, 3000
+    gen = torch.Generator().manual_seed(63)
+    q, _, _ = make(1, G * Hkv, Hkv, Nq, 1, d, seed=64)
+    k = torch.randn(1, Hkv, block, d, generator=gen).bfloat16().repeat(1, 1, 47, 1)[:, :, :Nk].clone()
+    k.view(torch.int16)[:, :, ::block, ::7] ^= torch.randint(2, k[:, :, ::block, ::7].shape, generator=gen, dtype=torch.int16)
+    q, k = q * 2.0 ** q_exp, k * 2.0 ** k_exp   # powers of two: no rounding
+    for causal in (True, False):
+        cfg = svoo.BlockConfig(block=block, n_sel=9, sink=1, local=int(causal), causal=causal)
+        pool = svoo.block_pool(k.cuda(), cfg)
+        idx = svoo.block_select(q.cuda(), pool, cfg, Nk)
+        assert torch.equal(idx.cpu(), ref.select(q, pool.cpu(), cfg, Nk))
