@@ -775,11 +775,20 @@ class _BlockAttn(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None, None
 
 
+def _has_tangent(*ts) -> bool:
+    """Whether forward-mode differentiation is under way and one of the tensors takes part."""
+    ad = torch.autograd.forward_ad
+    return ad._current_level >= 0 and any(ad.unpack_dual(t).tangent is not None for t in ts)
+
+
 def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[int] = None, dev_err=None):
     """The whole path on the current stream: block means -> selection -> attention over the selected
     blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
-    right-padded batch; q_start as in block_select. Differentiable in q, k and v (the selection is a constant of the gradient; the
-    gradient's gradient is not offered). Returns (o, dict(idx, lse, pool, dev_err))."""
+    right-padded batch; q_start as in block_select. Differentiable in q, k and v (the selection is a
+    constant of the gradient; the gradient's gradient and forward-mode gradients are not offered).
+    Returns (o, dict(idx, lse, pool, dev_err))."""
+    if _has_tangent(q, k, v):
+        raise SvooError("block_attention has no forward-mode gradient")
     args = _block_args(q, k, v, cfg, lengths, q_start)
     scale = _block_scale(cfg, args[6])
     err = _err_buf(dev_err, q.device)
@@ -798,7 +807,7 @@ def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[i
 def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = None, weight=None, out=None,
                workspace=None, dev_err=None, stream=None):
     """Attention of one token per sequence, q bf16 [B, H, 1, d], over the first lengths[b] slots of a
-    cache, k and v bf16 [B, Hkv, cap, d]; returns (o, lse).
+    cache, k and v bf16 [B, Hkv, cap, d]; returns (o, lse). No gradient is recorded.
 
     idx (from block_select, with its cfg): only the slots of the selected blocks. weight (fp32
     [B, Hkv, cap]): every valid slot's softmax weight, summed over the group's heads, is added to it."""

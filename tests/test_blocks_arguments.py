@@ -1,5 +1,7 @@
 """Arguments that the Python entry points settle themselves, without a GPU."""
 import pytest
+import torch
+import torch.autograd.forward_ad as fwd
 
 import free_sparse_attention_head_b200 as svoo
 
@@ -14,3 +16,16 @@ def test_positions_of_the_queries():
         assert first(None, 300, Nq, False) == 0    # positions mean nothing
     for given in (-1, 0, 7):
         assert first(given, 300, 301, True) == first(given, 300, 301, False) == given
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_forward_mode_gradients_are_refused(which):
+    """A tangent would be lost without a word: the autograd function is passed by where nothing requires a gradient."""
+    ts = [torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16) for _ in range(3)]
+    with fwd.dual_level():
+        assert not svoo._has_tangent(*ts)
+        ts[which] = fwd.make_dual(ts[which], torch.ones_like(ts[which]))
+        assert svoo._has_tangent(*ts)
+        with pytest.raises(svoo.SvooError, match="forward-mode"):
+            svoo.block_attention(*ts, svoo.BlockConfig())
+    assert not svoo._has_tangent(*ts)

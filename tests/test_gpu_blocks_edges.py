@@ -278,3 +278,15 @@ def test_selection_far_from_one(Nq, q_exp, k_exp):
         pool = svoo.block_pool(k.cuda(), cfg)
         idx = svoo.block_select(q.cuda(), pool, cfg, Nk)
         assert torch.equal(idx.cpu(), ref.select(q, pool.cpu(), cfg, Nk))
+
+
+def test_forward_mode_gradients_are_refused():
+    q, k, v = (t.cuda() for t in make(1, 2, 1, 70, 70, 64, seed=65))
+    cfg = svoo.BlockConfig(n_sel=2)
+    want, _ = svoo.block_attention(q, k, v, cfg)
+    with torch.autograd.forward_ad.dual_level():
+        for grad in (False, True):
+            dual = torch.autograd.forward_ad.make_dual(v.clone().requires_grad_(grad), torch.ones_like(v))
+            with pytest.raises(svoo.SvooError, match="forward-mode"):
+                svoo.block_attention(q, k, dual, cfg)
+        assert torch.equal(svoo.block_attention(q, k, v, cfg)[0], want)
