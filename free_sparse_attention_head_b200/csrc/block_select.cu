@@ -1161,7 +1161,7 @@ extern "C" svoo_status svoo_block_pool(const svoo_block_shape* shape, const void
   if (!aligned(k, 16) || !aligned(pool, 16) || !aligned(lengths, 4)) return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const dim3 grid(last > 0 && last < p.nb ? last : p.nb, p.B * p.Hkv);
-  const int tail = last > 0 && last < p.nb ? 1 : 0;
+  const int tail = last > 0 ? 1 : 0;  // blocks behind a sequence stay, however many are asked for
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (shape->d == 128)
     block_pool_kernel<128><<<grid, 128, 0, st>>>(p, static_cast<const uint16_t*>(k), lengths, tail, pool);

@@ -290,3 +290,21 @@ def test_forward_mode_gradients_are_refused():
             with pytest.raises(svoo.SvooError, match="forward-mode"):
                 svoo.block_attention(q, k, dual, cfg)
         assert torch.equal(svoo.block_attention(q, k, v, cfg)[0], want)
+
+
+@pytest.mark.parametrize("last", [1, 2, 5, 6, 100])
+def test_renewed_means_leave_the_others(last):
+    """The last blocks that hold keys are renewed, all others stay, also where more are asked for than there are."""
+    lengths, block, Nk = [300, 64, 1, 0, 130], 64, 300
+    _, k, _ = make(5, 2, 2, 1, Nk, 64, seed=66)
+    cfg = svoo.BlockConfig(block=block)
+    pool = torch.full((5, 2, 5, 64), 7.0, device="cuda")
+    svoo.block_pool(k.cuda(), cfg, lens(lengths), pool=pool, last=last)
+    want = ref.pool(k, block, lengths).float()
+    for b, L in enumerate(lengths):
+        n = -(-L // block)
+        for c in range(5):
+            if max(0, n - last) <= c < n:
+                assert ((pool[b, :, c].cpu() - want[b, :, c]).abs() <= 2.0 ** -23 * want[b, :, c].abs()).all()
+            else:
+                assert (pool[b, :, c] == 7.0).all(), (b, c)
