@@ -261,8 +261,16 @@ def workspace_sizes(shape: Shape, cfg: Config) -> tuple:
     return int(c), int(m)
 
 
+def _error_word(dev_err, device):
+    """The caller's error word, which kernels write to through its address."""
+    if not isinstance(dev_err, torch.Tensor) or dev_err.dtype is not torch.int32 or dev_err.device != device or \
+            dev_err.numel() < 1:
+        raise SvooError(f"dev_err must be an int32 tensor on {device}")
+    return dev_err
+
+
 def _err_buf(dev_err, device):
-    return dev_err if dev_err is not None else torch.zeros(1, dtype=torch.int32, device=device)
+    return torch.zeros(1, dtype=torch.int32, device=device) if dev_err is None else _error_word(dev_err, device)
 
 
 def check_device_errors(dev_err: torch.Tensor):
@@ -544,6 +552,10 @@ def _dp(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _err_at(dev_err, device):
+    return None if dev_err is None else _error_word(dev_err, device).data_ptr()
+
+
 def _call(what: str, t: torch.Tensor, *args):
     """Calls a C entry point with t's device current, on that device's current stream."""
     fn = getattr(_lib if _lib is not None else load(), what)
@@ -697,7 +709,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
             _first_position(q_start, n_keys, Nq, cfg.causal))
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
     _call("svoo_block_select", q, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
-          idx.data_ptr(), ws_at, ws_n, _dp(dev_err))
+          idx.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
     return idx
 
 
@@ -721,7 +733,7 @@ def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err):
     lse = torch.empty(args[0], args[1], args[3], dtype=torch.float32, device=dev)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
     _call("svoo_block_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-          _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _dp(dev_err))
+          _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
     return out, lse
 
 
@@ -749,7 +761,7 @@ def _run_attn_backward(args, scale, q, k, v, o, lse, grad_o, idx, lengths, works
     dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
     _call("svoo_block_attn_backward", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), lse.data_ptr(), grad_o.data_ptr(), idx.data_ptr(), _dp(lengths), scale,
-          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws_at, ws_n, _dp(dev_err))
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
     return dq, dk, dv
 
 
@@ -834,7 +846,7 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
     lse = torch.empty(B, H, 1, dtype=torch.float32, device=dev)
     _call("svoo_cache_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
           _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws_at, ws_n,
-          _dp(dev_err))
+          _err_at(dev_err, dev))
     return out, lse
 
 

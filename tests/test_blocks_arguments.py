@@ -29,3 +29,19 @@ def test_forward_mode_gradients_are_refused(which):
         with pytest.raises(svoo.SvooError, match="forward-mode"):
             svoo.block_attention(*ts, svoo.BlockConfig())
     assert not svoo._has_tangent(*ts)
+
+
+def test_the_error_word_is_checked():
+    """Kernels write to its address: an address of the host, of another device or of nothing may not reach them."""
+    dev = torch.device("cuda", 0)
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(0, dtype=torch.int32, device="meta"), 4096, [0]):
+        with pytest.raises(svoo.SvooError, match="dev_err"):
+            svoo._err_at(bad, dev)
+        with pytest.raises(svoo.SvooError, match="dev_err"):
+            svoo._err_buf(bad, dev)
+    meta = torch.device("meta")
+    for bad in (torch.zeros(1, dtype=torch.int64, device=meta), torch.zeros(0, dtype=torch.int32, device=meta)):
+        with pytest.raises(svoo.SvooError, match="dev_err"):
+            svoo._err_at(bad, meta)
+    good = torch.zeros(2, dtype=torch.int32, device=meta)
+    assert svoo._err_buf(good, meta) is good and svoo._err_at(None, dev) is None

@@ -308,3 +308,21 @@ def test_renewed_means_leave_the_others(last):
                 assert ((pool[b, :, c].cpu() - want[b, :, c]).abs() <= 2.0 ** -23 * want[b, :, c].abs()).all()
             else:
                 assert (pool[b, :, c] == 7.0).all(), (b, c)
+
+
+@pytest.mark.parametrize("bad", [lambda: torch.zeros(1, dtype=torch.int32), lambda: torch.zeros(1, dtype=torch.int64, device="cuda"),
+                                 lambda: torch.zeros(0, dtype=torch.int32, device="cuda")])
+def test_error_words_that_are_none(bad):
+    q, k, v = (t.cuda() for t in make(1, 2, 1, 70, 70, 64, seed=67))
+    cfg, err = svoo.BlockConfig(n_sel=2), bad()
+    pool = svoo.block_pool(k, cfg)
+    idx = svoo.block_select(q, pool, cfg, 70)
+    o, lse = svoo.block_attn(q, k, v, idx, cfg)
+    one = q[:, :, :1].contiguous()
+    for call in (lambda: svoo.block_select(q, pool, cfg, 70, dev_err=err), lambda: svoo.block_attn(q, k, v, idx, cfg, dev_err=err),
+                 lambda: svoo.block_attn_backward(q, k, v, o, lse, q, idx, cfg, dev_err=err),
+                 lambda: svoo.block_attention(q, k, v, cfg, dev_err=err), lambda: svoo.cache_attn(one, k, v, dev_err=err),
+                 lambda: svoo.cluster(q, k, svoo.Config(n_qc=4, n_kc=4), dev_err=err)):
+        with pytest.raises(svoo.SvooError, match="dev_err"):
+            call()
+    torch.cuda.synchronize()
