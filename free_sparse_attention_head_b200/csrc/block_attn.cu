@@ -33,6 +33,11 @@ namespace {
 
 constexpr int kFwdThreads = 192;
 constexpr int kMaxShares = 8;  // CTAs that share a row tile's list: a cluster
+// Shared memory of which an SM holds no three CTAs (228 KB, 1 KB of each its own).
+// A cluster's CTA keeps its tensor memory, half of the SM's, until the others are
+// through; a third on the SM would wait for some, and clusters could wait for each
+// other in a ring. (As compiled, 113 registers a thread leave room for two as well.)
+constexpr size_t kNoThird = 228 * 1024 / 3 - 1024 + 128;
 // The running maximum stays until it is outgrown by 2^32: P (bf16, fp32's range)
 // and its sums lose nothing by being large, at most 2^52 here, and the rescaling
 // that a smaller bound (2^8) asked for stalled most steps on the last product.
@@ -918,6 +923,7 @@ svoo_status launch_block_attn(const BlockDims& p, const void* q, const void* k, 
   cfg.gridDim = dim3((t.Nq + t.tpt - 1) / t.tpt, t.B * t.Hkv, f.shares);
   cfg.blockDim = dim3(kFwdThreads);
   cfg.dynamicSmemBytes = fwd_smem(D) + tile_list_bytes(t);
+  if (f.shares > 1 && cfg.dynamicSmemBytes < kNoThird) cfg.dynamicSmemBytes = kNoThird;
   cfg.stream = st;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;

@@ -103,3 +103,18 @@ def test_every_shape_of_the_documented_range_is_launched(host):
         for call in calls_of(host, s):
             assert call() == 0, s
             assert not any(x.bad for x in host.launches), s
+
+
+def test_clusters_never_share_an_sm_three_at_a_time(host):
+    """A CTA of the forward call's clusters holds half of an SM's tensor memory until its whole cluster is through: a
+    third on the SM would wait for some there, and clusters that wait for each other that way would never end."""
+    seen = 0
+    for d in (64, 128):
+        for Nq, Nk, n_sel in [(333, 1999, 8), (20, 300, 4), (64, 5000, 30), (700, 700, 16), (1, 9000, 64)]:
+            s = shape(B=1, H=4, Hkv=2, Nq=Nq, Nk=Nk, cap=Nk, d=d, block=64, n_sel=n_sel, sink=0, local=1, causal=1, q_start=-1)
+            assert host.attn(s) == 0
+            for x in host.launches:
+                if "block_attn_kernel" in x.kernel and x.grid[2] > 1:
+                    seen += 1
+                    assert 3 * (x.smem + 1024) > 228 * 1024 and not x.bad
+    assert seen >= 8
