@@ -1,10 +1,10 @@
 """Builds libsvoo.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc.
 
 It also links libsvoo_stall.so, a test-only variant whose pipelined kernels
-(attention, clustering assignment, attention over a cache) are compiled with SVOO_TEST_STALL: one
-pipeline wait on a barrier that nothing completes and a pipeline wait budget
-of about 10 ms, so a test can drive the device timeout path and read the
-error word. No product code loads it.
+(attention, clustering assignment, the block-selected attention's and the
+cache's) are compiled with SVOO_TEST_STALL: one pipeline wait on a barrier that
+nothing completes and a pipeline wait budget of about 10 ms, so a test can drive
+the device timeout path and read the error word. No product code loads it.
 
     python -m free_sparse_attention_head_b200.build [--force]
 """
@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libsvoo.so")
 STALL_LIB = os.path.join(HERE, "libsvoo_stall.so")
 SOURCES = ["api.cu", "cluster.cu", "mask.cu", "permute.cu", "attn.cu", "psa.cu",
            "block_select.cu", "block_attn.cu", "block_grad.cu", "cache.cu"]
-STALL_SOURCES = ["cluster.cu", "attn.cu", "cache.cu"]  # kernels with pipeline waits
+STALL_SOURCES = ["cluster.cu", "attn.cu",  # the kernels with pipeline waits
+                 "block_select.cu", "block_attn.cu", "block_grad.cu", "cache.cu"]
 HEADERS = ["common.cuh", "internal.h", "blocks.cuh", "block_lists.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 

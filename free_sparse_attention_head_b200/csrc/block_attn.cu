@@ -46,6 +46,9 @@ constexpr float kFwdRescaleLog2 = 32.0f;
 struct FwdSmem {
   uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2];
   uint64_t s_full[2], p_full[2], mma_final;
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   uint32_t tmem_base;
   int abort;
   int max_limit;
@@ -110,6 +113,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     mbar_init(smem_u32(&S->q_full), 1);
     mbar_init(smem_u32(&S->mma_final), 1);
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
     mbar_arrive_expect_tx(smem_u32(&S->q_full), p.tpt * p.G * D * 2);
     load_query_rows<D>(&qmap, q_s, smem_u32(&S->q_full), hk * p.G, t0, b);
@@ -190,7 +196,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         umma_commit(smem_u32(&S->k_empty[st]));
         return true;
       };
-      bool ok = mbar_wait(smem_u32(&S->q_full), 0, abort) && tiles > 0 && issue_s(0);
+      bool ok = mbar_wait(smem_u32(&S->q_full), 0, abort) && tiles > 0;
+#ifdef SVOO_TEST_STALL
+      ok = ok && mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
+      ok = ok && issue_s(0);
       for (int j = 0; j < tiles && ok; ++j) {
         const int st = j & 1;
         // S(j+1) goes where P(j-1) was: its product is ahead in the queue
@@ -439,6 +449,9 @@ constexpr int kPartCols = 8;  // columns that a part's rows have together
 
 struct ListSmem {
   uint64_t kv_full[2], full, s_full, p_full, o_full, o_read, mma_final;
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   uint32_t tmem_base;
   int abort;
 };
@@ -508,6 +521,9 @@ __global__ void __launch_bounds__(kListThreads, 2)
     mbar_init(smem_u32(&S->o_full), 1);
     mbar_init(smem_u32(&S->o_read), 4);
     mbar_init(smem_u32(&S->mma_final), 1);
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -532,7 +548,10 @@ __global__ void __launch_bounds__(kListThreads, 2)
       const uint32_t idesc_s = idesc_bf16_f32(kRowTile, kListKeys, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(kRowTile, D, false, true);
       const uint32_t k_u = smem_u32(k_s), v_u = smem_u32(v_s), q_u = smem_u32(q_s);
-      const bool there = mbar_wait(smem_u32(&S->kv_full[0]), 0, abort) && mbar_wait(smem_u32(&S->kv_full[1]), 0, abort);
+      bool there = mbar_wait(smem_u32(&S->kv_full[0]), 0, abort) && mbar_wait(smem_u32(&S->kv_full[1]), 0, abort);
+#ifdef SVOO_TEST_STALL
+      there = there && mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
       for (int j = 0; j < nj && there; ++j) {
         if (!mbar_wait(smem_u32(&S->full), j & 1, abort)) break;
         tc_fence_after();

@@ -50,6 +50,9 @@ constexpr int kDqV = 2;  // stages of V, where Q and dO pass through first
 struct DqSmem {
   uint64_t k_full[kDqK], k_empty[kDqK], v_full[kDqV], v_empty[kDqV];
   uint64_t q_full, s_full, s_read, dp_full, ds_full, mma_final;
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   uint32_t tmem_base;
   int abort;
   int max_limit;
@@ -115,6 +118,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(smem_u32(&S->ds_full), 8);
     mbar_init(smem_u32(&S->q_full), 1);
     mbar_init(smem_u32(&S->mma_final), 1);
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
     const uint32_t bar = smem_u32(&S->q_full);
     mbar_arrive_expect_tx(bar, 3 * p.tpt * p.G * D * 2);
@@ -227,7 +233,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         umma_commit(smem_u32(&S->v_empty[vs]));
         return true;
       };
-      bool ok = steps > 0 && issue_s(0) && issue_dp(0);
+      bool ok = steps > 0;
+#ifdef SVOO_TEST_STALL
+      ok = ok && mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
+      ok = ok && issue_s(0) && issue_dp(0);
       for (int j = 0; j < steps && ok; ++j) {
         const bool more = j + 1 < steps;
         if (more && (!mbar_wait(smem_u32(&S->s_read), j & 1, abort) || !issue_s(j + 1))) break;
@@ -387,6 +397,9 @@ constexpr int kDkvIssuer = kDkvThreads / 32 - 1;
 
 struct DkvSmem {
   uint64_t full[2], free_[2], s_full[2], ds_full[2], mma_final;
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   uint32_t tmem_base;
   int abort;
   float lse2[2][kRowTile];
@@ -459,6 +472,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       mbar_init(smem_u32(&S->ds_full[s]), 4);
     }
     mbar_init(smem_u32(&S->mma_final), 1);
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
   }
   if (nj > 0) {
@@ -547,8 +563,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       // S, dP of tile js and the sums of tile jg, whichever can go first: a tile
       // that has not landed does not hold back the sums that its stage waits for
       int js = 0, jg = 0;
+      bool go = true;
+#ifdef SVOO_TEST_STALL
+      go = nj == 0 || mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
       long long since = clock64();
-      while (jg < nj) {
+      while (jg < nj && go) {
         bool did = false;
         if (js < nj && js < jg + 2 && mbar_try_wait(smem_u32(&S->full[js & 1]), (js >> 1) & 1)) {
           const int st = js & 1;

@@ -412,6 +412,9 @@ constexpr int kMmaMaxBlocks = 6144;  // exact scores of a whole row fit where th
 
 struct MmaSelSmem {
   uint64_t full[2], empty[2], s_full[2], s_empty[2], mma_final;
+#ifdef SVOO_TEST_STALL
+  uint64_t stall;  // test-only: a barrier that nothing completes
+#endif
   uint32_t tmem_base;
   int abort;
   int hard;             // queries whose ties overran the list, or whose norms are out of fp32's range
@@ -519,6 +522,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       mbar_init(smem_u32(&S->s_empty[s]), 4);
     }
     mbar_init(smem_u32(&S->mma_final), 1);
+#ifdef SVOO_TEST_STALL
+    mbar_init(smem_u32(&S->stall), 1);
+#endif
     fence_mbar_init();
   }
   // one step of at most 64 blocks: the means' parts are made here, without a
@@ -704,7 +710,11 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   } else if (warp == 5) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(kRowTile, kKeyTile, false, false);
-      for (int j = 0; j < steps; ++j) {
+      bool go = true;
+#ifdef SVOO_TEST_STALL
+      go = steps == 0 || mbar_wait(smem_u32(&S->stall), 0, abort);  // nothing completes it
+#endif
+      for (int j = 0; j < steps && go; ++j) {
         const int st = j & 1;
         if (!mbar_wait(smem_u32(&S->full[st]), (j >> 1) & 1, abort)) break;
         if (j >= 2 && !mbar_wait(smem_u32(&S->s_empty[st]), ((j - 2) >> 1) & 1, abort)) break;
