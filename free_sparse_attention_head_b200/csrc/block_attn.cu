@@ -974,7 +974,7 @@ extern "C" svoo_status svoo_block_attn(const svoo_block_shape* shape, const void
   if (shape->Nq == 0) return SVOO_OK;  // empty tensors have no address
   if (!q || !k || !v || !idx || !o || !lse) return SVOO_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(idx, 4) ||
-      !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
+      !aligned(lse, 4) || !aligned(lengths, 4) || !aligned(dev_err, 4) || !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const size_t need = fwd_plan(p, shape->d, nullptr).bytes;

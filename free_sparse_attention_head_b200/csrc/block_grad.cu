@@ -862,7 +862,9 @@ extern "C" svoo_status svoo_block_attn_backward(const svoo_block_shape* shape, c
   for (const void* x : {q, k, v, o, grad_o, static_cast<const void*>(dq), static_cast<const void*>(dk),
                         static_cast<const void*>(dv)})
     if (!aligned(x, 16)) return SVOO_ERR_INVALID_ARG;
-  if (!aligned(workspace, 256) || !aligned(idx, 4) || !aligned(lse, 4)) return SVOO_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || !aligned(idx, 4) || !aligned(lse, 4) || !aligned(lengths, 4) ||
+      !aligned(dev_err, 4))
+    return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   if (workspace_bytes < grad_plan(p, shape->d, nullptr).bytes) return SVOO_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

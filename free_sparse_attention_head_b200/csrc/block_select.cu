@@ -1191,7 +1191,8 @@ extern "C" svoo_status svoo_block_select(const svoo_block_shape* shape, const vo
   if (!block_shape_ok(shape)) return SVOO_ERR_INVALID_ARG;
   if (shape->Nq == 0) return SVOO_OK;  // empty tensors have no address
   if (!q || !pool || !idx) return SVOO_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4) || !aligned(workspace, 256))
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(idx, 4) || !aligned(lengths, 4) || !aligned(dev_err, 4) ||
+      !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const size_t need = select_plan(p, shape->d, nullptr).bytes;

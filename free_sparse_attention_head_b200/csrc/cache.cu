@@ -829,7 +829,8 @@ extern "C" svoo_status svoo_cache_attn(const svoo_block_shape* shape, const void
     return SVOO_ERR_INVALID_ARG;
   if (idx && weight) return SVOO_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
-      !aligned(lengths, 4) || !aligned(idx, 4) || !aligned(weight, 4) || !aligned(workspace, 256))
+      !aligned(lengths, 4) || !aligned(idx, 4) || !aligned(weight, 4) || !aligned(dev_err, 4) ||
+      !aligned(workspace, 256))
     return SVOO_ERR_INVALID_ARG;
   const BlockDims p = block_dims(shape);
   const size_t need = cache_plan(p, shape->d, idx != nullptr, weight != nullptr, nullptr).bytes;

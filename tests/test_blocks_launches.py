@@ -118,3 +118,22 @@ def test_clusters_never_share_an_sm_three_at_a_time(host):
                     seen += 1
                     assert 3 * (x.smem + 1024) > 228 * 1024 and not x.bad
     assert seen >= 8
+
+
+def test_misaligned_lengths_and_error_words_are_refused(host):
+    """Optional addresses are checked like the others: kernels read and write 32-bit words there."""
+    x, n, odd = 0x10000, 1 << 60, 0x10002
+    s = dict(B=2, H=4, Hkv=2, Nq=100, Nk=300, cap=300, d=64, block=64, n_sel=4, sink=1, local=1, causal=1, q_start=0)
+    many, one = shape(**s), shape(**{**s, "Nq": 1})
+
+    def calls(lengths, err):
+        yield host("svoo_block_select", many, x, x, lengths, x, x, n, err, None)
+        yield host("svoo_block_attn", many, x, x, x, x, lengths, 0.1, x, x, x, n, err, None)
+        yield host("svoo_block_attn_backward", many, x, x, x, x, x, x, x, lengths, 0.1, x, x, x, x, n, err, None)
+        yield host("svoo_cache_attn", one, x, x, x, lengths, None, 0.1, None, x, x, x, n, err, None)
+        if err is None:
+            yield host("svoo_block_pool", many, x, lengths, 0, x, None)
+
+    assert all(status == 0 for status in calls(None, None)) and all(status == 0 for status in calls(x, x))
+    assert all(status == 1 and not host.launches for status in calls(odd, None))
+    assert all(status == 1 and not host.launches for status in calls(None, odd))
