@@ -570,6 +570,14 @@ def _call(what: str, t: torch.Tensor, *args):
         _check(status, what)
 
 
+def _written(*ts: Optional[torch.Tensor]):
+    """Tells autograd that the caller's tensors were written in place, so that a backward pass that had saved
+    one of them says so instead of using what it holds now."""
+    given = [t for t in ts if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _need(what: str, dtype, device, shape, t: Optional[torch.Tensor]):
     """A dense tensor of that type, device and shape, or None."""
     if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
@@ -674,6 +682,7 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
     B, Hkv, Nk, d = k.shape
     nb = -(-Nk // cfg.block) if cfg.block > 0 else 0
     _need("lengths", torch.int32, dev, (B,), lengths)
+    given = pool
     if pool is None:
         if last:
             raise SvooError("last renews blocks of an existing pool: pass it")
@@ -682,6 +691,7 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
         _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
     _call("svoo_block_pool", k, _bshape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0),
           k.data_ptr(), _dp(lengths), last, pool.data_ptr())
+    _written(given)
     return pool
 
 
@@ -701,6 +711,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     Hkv = pool.shape[1] if pool.dim() == 4 else 0
     _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
     _need("lengths", torch.int32, dev, (B,), lengths)
+    given = idx
     if idx is None:
         idx = torch.empty(B, Hkv, Nq, max(cfg.n_sel, 0), dtype=torch.int32, device=dev)
     else:
@@ -710,6 +721,7 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
     _call("svoo_block_select", q, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
           idx.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
+    _written(given)
     return idx
 
 
@@ -728,12 +740,13 @@ def block_attn(q, k, v, idx, cfg: BlockConfig, lengths=None, q_start: Optional[i
 
 
 def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err):
-    dev = q.device
+    dev, given = q.device, out
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(args[0], args[1], args[3], dtype=torch.float32, device=dev)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
     _call("svoo_block_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
           _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
+    _written(given)
     return out, lse
 
 
@@ -842,11 +855,13 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
         _need("weight", torch.float32, dev, (B, Hkv, Nk), weight)
     _need("out", torch.bfloat16, dev, q.shape, out)
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_attn_workspace_size", *args, idx is not None, weight is not None)
+    given = out
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(B, H, 1, dtype=torch.float32, device=dev)
     _call("svoo_cache_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
           _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws_at, ws_n,
           _err_at(dev_err, dev))
+    _written(given, weight)
     return out, lse
 
 
@@ -872,3 +887,4 @@ def cache_evict(k, v, weight, pos, lengths, keep: int, sink: int = 0, recent: in
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_cache_evict_workspace_size", B, Hkv, cap, keep)
     _call("svoo_cache_evict", k, B, Hkv, cap, d, keep, sink, recent, k.data_ptr(), v.data_ptr(),
           weight.data_ptr(), pos.data_ptr(), lengths.data_ptr(), ws_at, ws_n)
+    _written(k, v, weight, pos, lengths)

@@ -326,3 +326,37 @@ def test_error_words_that_are_none(bad):
         with pytest.raises(svoo.SvooError, match="dev_err"):
             call()
     torch.cuda.synchronize()
+
+
+def test_tensors_written_in_place_are_known_to_autograd():
+    """A backward pass over a cache that was cut since says so, instead of using the moved rows."""
+    B, H, Hkv, N, d = 1, 4, 2, 200, 64
+    q, k, v = (t.cuda() for t in make(B, H, Hkv, N, N, d, seed=68))
+    cfg = svoo.BlockConfig(n_sel=3)
+    w, pos = torch.rand(B, Hkv, N, device="cuda"), torch.arange(N, device="cuda").int().repeat(B, Hkv, 1)
+    ln = lens([N])
+    q.requires_grad_(True)
+    for n in range(3):
+        o, _ = svoo.block_attention(q, k, v, cfg, ln)
+        if n == 0:
+            o.float().sum().backward()   # nothing was written
+            continue
+        if n == 1:
+            svoo.cache_evict(k, v, w, pos, ln, 150)
+        else:
+            svoo.block_attn(q.detach(), k, v, svoo.block_select(q.detach(), svoo.block_pool(k, cfg), cfg, N), cfg, out=o.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            o.float().sum().backward()
+    one = q.detach()[:, :, :1].contiguous()
+    pool = svoo.block_pool(k, cfg)
+    idx = svoo.block_select(one, pool, cfg, N)
+    before = [t._version for t in (w, pool, idx)]
+    svoo.cache_attn(one, k, v, weight=w)
+    svoo.block_pool(k, cfg, pool=pool, last=1)
+    svoo.block_select(one, pool, cfg, N, idx=idx)
+    assert [t._version for t in (w, pool, idx)] == [x + 1 for x in before]
+    with torch.inference_mode():   # tensors without versions
+        caches = [t.clone() for t in (k, v, w, pos, lens([N]))]
+        svoo.cache_attn(one, *caches[:2], weight=caches[2])
+    svoo.cache_evict(*caches, 100)
+    assert caches[4].tolist() == [100]
