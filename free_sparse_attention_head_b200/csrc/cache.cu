@@ -517,7 +517,8 @@ svoo_status launch_cache_attn(const BlockDims& p, const void* q, const void* k, 
     return launch_status();
   const int runs = c.joined ? 1 : c.runs;  // still to join
   const size_t factors = runs > 1 ? static_cast<size_t>(p.G) * runs * 4 : 0;
-  if (factors > 48 * 1024 && !allow_smem(cache_join_kernel<D>, kRowTile * kMaxRuns * 4)) return SVOO_ERR_CUDA;
+  // (48 KB need no leave, the kernel's own half KB among them)
+  if (factors > 32 * 1024 && !allow_smem(cache_join_kernel<D>, kRowTile * kMaxRuns * 4)) return SVOO_ERR_CUDA;
   if (runs > 1 || weight)
     cache_join_kernel<D><<<dim3(1 + (weight ? (p.Nk + 1023) / 1024 : 0), p.B * p.Hkv), 256, factors, st>>>(
         p, runs, lengths, c.part_o, c.part_ml, c.scores, static_cast<uint16_t*>(o), lse, weight, dev_err);

@@ -137,3 +137,15 @@ def test_misaligned_lengths_and_error_words_are_refused(host):
     assert all(status == 0 for status in calls(None, None)) and all(status == 0 for status in calls(x, x))
     assert all(status == 1 and not host.launches for status in calls(odd, None))
     assert all(status == 1 and not host.launches for status in calls(None, odd))
+
+
+@pytest.mark.parametrize("G", [112, 126, 127, 128])
+@pytest.mark.parametrize("selected", [False, True])
+def test_joining_runs_of_large_groups(host, G, selected):
+    """A factor per head and run: about 48 KB, beside what the kernel declares for itself."""
+    for B in (1, 2):
+        for tiles in range(300, 1200, 4):
+            s = dict(B=B, H=G, Hkv=1, Nq=1, Nk=64 * tiles, cap=64 * tiles, d=128, block=64, n_sel=16, sink=0, local=1, causal=1, q_start=0)
+            if selected:
+                s.update(Nk=832, cap=832, block=1024, n_sel=tiles // 16)
+            assert host.cache(shape(**s), idx=0x40000 if selected else None) == 0, (B, tiles)

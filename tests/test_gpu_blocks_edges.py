@@ -360,3 +360,16 @@ def test_tensors_written_in_place_are_known_to_autograd():
         svoo.cache_attn(one, *caches[:2], weight=caches[2])
     svoo.cache_evict(*caches, 100)
     assert caches[4].tolist() == [100]
+
+
+@pytest.mark.parametrize("G,cap,d", [(128, 768 * 64, 64), (128, 767 * 64 + 5, 128), (120, 820 * 64 + 1, 64)])
+def test_joining_runs_of_large_groups(G, cap, d):
+    """The joining kernel's factors, one per head and run, take about the 48 KB that need no leave."""
+    gen = torch.Generator(device="cuda").manual_seed(69)
+    q, k, v = (torch.randn(1, h, n, d, generator=gen, device="cuda").bfloat16() for h, n in ((G, 1), (1, cap), (1, cap)))
+    w = torch.zeros(1, 1, cap, device="cuda")
+    o, lse = svoo.cache_attn(q, k, v, weight=w)
+    s = q[0, :, 0].double() @ k[0, 0].double().T / math.sqrt(d)
+    p = torch.softmax(s, -1)
+    check_out(o, lse, (p @ v[0, 0].double())[None, :, None].cpu(), s.logsumexp(-1)[None, :, None].cpu(), float(v.abs().max()))
+    assert ((w[0, 0].double() - p.sum(0)).abs() <= 2e-5 * p.sum(0)).all()
