@@ -561,7 +561,7 @@ def _call(what: str, t: torch.Tensor, *args):
     fn = getattr(_lib if _lib is not None else load(), what)
     dev = t.device.index
     st = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -570,12 +570,10 @@ def _call(what: str, t: torch.Tensor, *args):
         _check(status, what)
 
 
-def _written(*ts: Optional[torch.Tensor]):
+def _written(*ts: torch.Tensor):
     """Tells autograd that the caller's tensors were written in place, so that a backward pass that had saved
     one of them says so instead of using what it holds now."""
-    given = [t for t in ts if t is not None]
-    if given:
-        torch.autograd.graph.increment_version(given)
+    torch._C._increment_version(ts)    # (of torch.autograd.graph, without its look at the type)
 
 
 def _need(what: str, dtype, device, shape, t: Optional[torch.Tensor]):
@@ -691,7 +689,8 @@ def block_pool(k, cfg: BlockConfig, lengths=None, pool=None, last: int = 0, stre
         _need("pool", torch.float32, dev, (B, Hkv, nb, d), pool)
     _call("svoo_block_pool", k, _bshape(B, Hkv, Hkv, 1, Nk, cap, d, cfg.block, 1, 0, 0, 0, 0),
           k.data_ptr(), _dp(lengths), last, pool.data_ptr())
-    _written(given)
+    if given is not None:
+        _written(given)
     return pool
 
 
@@ -721,7 +720,8 @@ def block_select(q, pool, cfg: BlockConfig, n_keys: int, lengths=None, q_start: 
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_select_workspace_size", *args)
     _call("svoo_block_select", q, _bshape(*args), q.data_ptr(), pool.data_ptr(), _dp(lengths),
           idx.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
-    _written(given)
+    if given is not None:
+        _written(given)
     return idx
 
 
@@ -746,7 +746,8 @@ def _run_attn(args, scale, q, k, v, idx, lengths, out, workspace, dev_err):
     ws, ws_at, ws_n = _workspace(workspace, dev, "svoo_block_attn_workspace_size", *args)
     _call("svoo_block_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
           _dp(lengths), scale, out.data_ptr(), lse.data_ptr(), ws_at, ws_n, _err_at(dev_err, dev))
-    _written(given)
+    if given is not None:
+        _written(given)
     return out, lse
 
 
@@ -861,7 +862,10 @@ def cache_attn(q, k, v, lengths=None, idx=None, cfg: Optional[BlockConfig] = Non
     _call("svoo_cache_attn", q, _bshape(*args), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dp(lengths),
           _dp(idx), _block_scale(cfg, d), _dp(weight), out.data_ptr(), lse.data_ptr(), ws_at, ws_n,
           _err_at(dev_err, dev))
-    _written(given, weight)
+    if given is not None:
+        _written(given)
+    if weight is not None:
+        _written(weight)
     return out, lse
 
 
