@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kSelThreads)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelWarp* amb = reinterpret_cast<SelWarp*>(smem_raw);
   float* qs = reinterpret_cast<float*>(amb + kSelThreads / 32);  // [TQ][D]
-  float* hs = qs + TQ * D;                                       // [TQ][D] sums of the heads' squares
-  float* sc = hs + TQ * D;                                       // [TQ][pitch]
+  float* hs = qs + TQ * D;                                       // [TQ][D] sums of the heads' squares,
+  float* sc = TQ == 1 ? hs + D : hs;                             // [TQ][pitch] which scores overwrite
+  __shared__ float2 norm2[TQ];                                   // squared norms: of the sums, of the heads
   __shared__ int pool_norm2;                                     // largest |pool[c]|^2 seen, as bits
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y / p.Hkv, hk = blockIdx.y - b * p.Hkv;
@@ -154,7 +155,25 @@ __global__ void __launch_bounds__(kSelThreads)
     most = pos >= 0 ? pos / p.block + 1 : 0;
   }
   const int nmax = most - p.local;
+  auto norms = [&](int t) {  // one warp
+    float q2 = 0.f, h2 = 0.f;
+    for (int d = lane; d < D; d += 32) {
+      q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
+      h2 += hs[t * D + d];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+      h2 += __shfl_xor_sync(0xffffffffu, h2, o);
+    }
+    if (lane == 0) norm2[t] = make_float2(q2, h2);
+    __syncwarp();
+  };
   __syncthreads();
+  if (TQ > 1 && most > p.n_sel) {  // before the scores go where the squares are
+    for (int t = warp; t < TQ; t += kSelThreads / 32) norms(t);
+    __syncthreads();
+  }
   if (most > p.n_sel) {
     float big = 0.f;
     if (TQ == 1) {
@@ -221,16 +240,8 @@ __global__ void __launch_bounds__(kSelThreads)
     float cut = INFINITY;   // scores above it are taken
     bool incl = false;      // ... and those equal to it
     if (!all && m > 0) {
-      float q2 = 0.f, h2 = 0.f;
-      for (int d = lane; d < D; d += 32) {
-        q2 = fmaf(qs[t * D + d], qs[t * D + d], q2);
-        h2 += hs[t * D + d];
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-        h2 += __shfl_xor_sync(0xffffffffu, h2, o);
-      }
+      if (TQ == 1) norms(0);
+      const float q2 = norm2[t].x, h2 = norm2[t].y;
       // |fp32 score - score| <= 2^-24 ((D + 2) |q| + (G - 1) |A|) |pool|, and the norms themselves
       // are good to far better than the 1.5 spent on them
       float e2 = 3.f * 5.9604645e-8f * ((D + 2) * bound_norm(q2) + heads_error(p.G, h2)) *
@@ -1137,7 +1148,8 @@ svoo_status launch_mma_select(const BlockDims& p, const void* q, const float* po
 // 1024 blocks are 128 KB).
 constexpr int sel_most_blocks(int tq) { return tq == 32 ? 1024 : tq == 8 ? 4096 : kMaxBlocks; }
 constexpr size_t sel_scores_smem(int d, int tq, int pitch) {
-  return sizeof(SelWarp) * (kSelThreads / 32) + static_cast<size_t>(tq) * (2 * d + pitch) * 4;
+  return sizeof(SelWarp) * (kSelThreads / 32) +
+         static_cast<size_t>(tq) * (tq == 1 ? 2 * d + pitch : d + (pitch > d ? pitch : d)) * 4;
 }
 
 template <int D, int TQ>
