@@ -95,6 +95,58 @@ struct SelWarp {
   int blk[kAmb];
 };
 
+// Scores in fp64, by a warp: eight lanes hold a query's sum over its heads (`q`:
+// its row in the first one, `head` elements from one to the next), D / 8 dimensions
+// each, four times over, and each of the four scores a block.
+template <int D>
+__device__ __forceinline__ void query64(const uint16_t* q, int G, size_t head, double (&qd)[D / 8]) {
+  const int part = threadIdx.x & 7;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) qd[i] = 0.;
+  for (int g = 0; g < G; ++g) {
+    const uint4* src = reinterpret_cast<const uint4*>(q + g * head + part * (D / 8));
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 x = src[c];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        qd[c * 8 + 2 * i] += static_cast<double>(__uint_as_float(w[i] << 16));
+        qd[c * 8 + 2 * i + 1] += static_cast<double>(__uint_as_float(w[i] & 0xffff0000u));
+      }
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ double score64(const double (&qd)[D / 8], const float* pool, int block) {
+  const float4* pc = reinterpret_cast<const float4*>(pool + static_cast<size_t>(block) * D + (threadIdx.x & 7) * (D / 8));
+  double x = 0.;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    const float4 v = pc[c];
+    x = fma(qd[4 * c], static_cast<double>(v.x), x);
+    x = fma(qd[4 * c + 1], static_cast<double>(v.y), x);
+    x = fma(qd[4 * c + 2], static_cast<double>(v.z), x);
+    x = fma(qd[4 * c + 3], static_cast<double>(v.w), x);
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// An unsigned key in the order of the values, -0 as 0.
+__device__ __forceinline__ unsigned long long order64(double x) {
+  const unsigned long long u = x == 0. ? 0ull : __double_as_longlong(x);
+  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ void warp_min_max(unsigned long long& lo, unsigned long long& hi) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+}
+
 // The queries' candidate range: blocks [0, nc), of which [lo, hi) are chosen
 // by score and the others forced; nc = 0 for a query outside its sequence.
 struct Candidates {
@@ -111,6 +163,57 @@ __device__ __forceinline__ Candidates candidates(const BlockDims& p, int len, in
   c.lo = min(p.sink, c.nc);
   c.hi = max(c.lo, c.nc - p.local);
   return c;
+}
+
+// The `need` best of a query's candidates in [lo, hi) whose score lies in [edge, cut],
+// marked by an infinite score: by bisection over fp64 scores that every pass computes
+// anew, in order and four at a time; equal scores to the lower block. One warp.
+template <int D>
+__device__ __noinline__ void best_near(const uint16_t* q, int G, size_t head, const float* pl, float* s, int lo, int hi,
+                                       float edge, float cut, int need) {
+  const int lane = threadIdx.x & 31, part = lane & 7, who = lane >> 3;
+  double qd[D / 8];
+  query64<D>(q, G, head, qd);
+  auto each = [&](auto f) {
+    for (int c0 = lo; c0 < hi; c0 += 4) {
+      const int c = c0 + who;
+      const bool near = c < hi && s[c] <= cut && s[c] >= edge;
+      if (!__any_sync(0xffffffffu, near)) continue;
+      const unsigned long long k = order64(score64<D>(qd, pl, min(c, hi - 1)));
+      f(c, near && part == 0, k);
+    }
+  };
+  unsigned long long kl = ~0ull, kh = 0ull;
+  each([&](int, bool near, unsigned long long k) {
+    if (near) {
+      kl = min(kl, k);
+      kh = max(kh, k);
+    }
+  });
+  warp_min_max(kl, kh);
+  int over = 0;        // candidates above kl, once kl = kh
+  bool all = false;    // exactly `need` of them reach kl
+  while (kl < kh && !all) {
+    const unsigned long long mid = kl + (kh - kl) / 2 + 1;
+    int n = 0;
+    each([&](int, bool near, unsigned long long k) { n += near && k >= mid; });
+    n = __reduce_add_sync(0xffffffffu, n);
+    all = n == need;
+    if (n >= need) {
+      kl = mid;
+    } else {
+      kh = mid - 1;
+      over = n;
+    }
+  }
+  int equal = 0;
+  each([&](int c, bool near, unsigned long long k) {
+    const unsigned eq = __ballot_sync(0xffffffffu, near && k == kl);
+    const int rank = equal + __popc(eq & ((1u << lane) - 1u));
+    if (near && (k > kl || (k == kl && (all || rank < need - over)))) s[c] = INFINITY;
+    equal += __popc(eq);
+  });
+  __syncwarp();
 }
 
 // TQ queries of one key head per CTA: fp32 scores of all their candidate
@@ -362,23 +465,8 @@ __global__ void __launch_bounds__(kSelThreads)
           }
           __syncwarp();
         } else {
-          // more candidates than the list holds (many equal blocks): one at a time
-          for (int pick = 0; pick < need; ++pick) {
-            double best = 0.;
-            int at = -1;
-            for (int c = cd.lo; c < cd.hi; ++c) {
-              const float x = s[c];
-              if (!(x <= cut && x >= edge)) continue;
-              const double y = exact(c);
-              if (at < 0 || y > best) {
-                best = y;
-                at = c;
-              }
-            }
-            __syncwarp();
-            if (lane == 0 && at >= 0) s[at] = INFINITY;
-            __syncwarp();
-          }
+          // more candidates than the list holds (many equal blocks)
+          best_near<D>(qh + static_cast<size_t>(t0 + t) * D, p.G, head, pl, s, cd.lo, cd.hi, edge, cut, need);
         }
       }
     }
@@ -489,6 +577,72 @@ struct Width {
 };
 
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// The rows of the four list warps with `hard` set (thread = row), each by its warp and
+// one at a time: every free candidate in fp64, four at a time, where the lists were
+// (as many warps at once as rows of scores fit there), the m-th best by bisection.
+// Keys or queries of all zeros bring every row here (16384 queries of 256 blocks, 16/4
+// heads, d = 128: 1.55 ms against 0.11; one row of a CTA at a time, its sum over the
+// heads made anew for every block, took 48). A function of its own: inside the kernel
+// its code cost other calls time (13.4 against 13.2 us at 1024 queries of 16 blocks).
+template <int D>
+__device__ __noinline__ void rows_in_fp64(const uint16_t* q, int G, size_t head, const float* pl, int nb, int n_sel,
+                                          bool hard, Candidates cd, int m, float* lists, int32_t* ids) {
+  constexpr int kDims = D / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 7, who = lane >> 3;
+  const int room = (kList + 1) * 128 * 6 / (nb * 8), at_once = room >= 4 ? 4 : room >= 2 ? 2 : 1;
+  for (int w = 0; w < 4; w += at_once) {
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp < w || warp >= w + at_once) continue;
+    double* ex = reinterpret_cast<double*>(lists) + static_cast<size_t>(warp - w) * nb;
+    unsigned todo = __ballot_sync(0xffffffffu, hard);
+    while (todo) {
+      const int src = __ffs(todo) - 1, r = (warp << 5) + src;
+      todo &= todo - 1;
+      const int lo_c = __shfl_sync(0xffffffffu, cd.lo, src), hi_c = __shfl_sync(0xffffffffu, cd.hi, src);
+      const int nc = __shfl_sync(0xffffffffu, cd.nc, src), mr = __shfl_sync(0xffffffffu, m, src);
+      unsigned long long lo = ~0ull, hi = 0ull;
+      double qd[kDims];
+      query64<D>(q + static_cast<size_t>(r) * D, G, head, qd);
+#pragma unroll 2
+      for (int c0 = lo_c; c0 < hi_c; c0 += 4) {
+        const double x = score64<D>(qd, pl, min(c0 + who, hi_c - 1));
+        if (part == 0 && c0 + who < hi_c) ex[c0 + who] = x;
+      }
+      __syncwarp();
+      for (int c = lo_c + lane; c < hi_c; c += 32) {
+        lo = min(lo, order64(ex[c]));
+        hi = max(hi, order64(ex[c]));
+      }
+      warp_min_max(lo, hi);
+      while (lo < hi) {
+        const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+        int k = 0;
+        for (int c = lo_c + lane; c < hi_c; c += 32) k += order64(ex[c]) >= mid;
+        k = __reduce_add_sync(0xffffffffu, k);
+        if (k >= mr) lo = mid;
+        else hi = mid - 1;
+      }
+      int over = 0;
+      for (int c = lo_c + lane; c < hi_c; c += 32) over += order64(ex[c]) > lo;
+      over = __reduce_add_sync(0xffffffffu, over);
+      int equal = 0, at = 0;
+      for (int c0 = 0; c0 < nc; c0 += 32) {
+        const int c = c0 + lane;
+        const bool forced = c < nc && (c < lo_c || c >= hi_c), open = c < nc && !forced;
+        const unsigned eq = __ballot_sync(0xffffffffu, open && order64(ex[c]) == lo);
+        const bool take = forced || (open && (order64(ex[c]) > lo || (((eq >> lane) & 1u) &&
+                                                                  equal + __popc(eq & ((1u << lane) - 1u)) < mr - over)));
+        equal += __popc(eq);
+        const unsigned bal = __ballot_sync(0xffffffffu, take);
+        const int to = at + __popc(bal & ((1u << lane) - 1u));
+        if (take && to < n_sel) ids[r * n_sel + to] = c;
+        at += __popc(bal);
+      }
+      __syncwarp();
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kMmaSelThreads, 2)
@@ -856,6 +1010,9 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
     }
   }
   __syncthreads();
+  constexpr int kDims = D / 8;
+  const int part = lane & 7, who = lane >> 3;
+  const float* pl = pool + static_cast<size_t>(blockIdx.y) * p.nb * D;
   if (*abort) {
     if (tid == 0) report_error(err, kErrTimeoutAttn);
     if (warp == 4 && lane == 0)
@@ -920,26 +1077,8 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
       todo &= todo - 1;
       const float el = __shfl_sync(0xffffffffu, edge_lo, src), eh = __shfl_sync(0xffffffffu, edge_hi, src);
       const int nr = __shfl_sync(0xffffffffu, cnt, src), mr = __shfl_sync(0xffffffffu, m, src);
-      // group sums: eight lanes hold a query, D / 8 dimensions each, four times over
-      constexpr int kDims = D / 8;
-      const int part = lane & 7, who = lane >> 3;
       double qd[kDims];
-#pragma unroll
-      for (int i = 0; i < kDims; ++i) qd[i] = 0.;
-      for (int g = 0; g < p.G; ++g) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(qh + g * head + static_cast<size_t>(t0 + r) * D + part * kDims);
-#pragma unroll
-        for (int c = 0; c < kDims / 8; ++c) {
-          const uint4 x = src[c];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            qd[c * 8 + 2 * i] += static_cast<double>(__uint_as_float(w[i] << 16));
-            qd[c * 8 + 2 * i + 1] += static_cast<double>(__uint_as_float(w[i] & 0xffff0000u));
-          }
-        }
-      }
+      query64<D>(qh + static_cast<size_t>(t0 + r) * D, p.G, head, qd);
       int sure = 0;
       double ex[2] = {0., 0.};
       bool near[2];
@@ -959,19 +1098,7 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
             bal &= bal - 1;
           }
           const int mine = at[who] < 0 ? at[0] : at[who];
-          const float4* pc = reinterpret_cast<const float4*>(
-              pool + (static_cast<size_t>(blockIdx.y) * p.nb + li[(h * 32 + mine) * 128 + r]) * D + part * kDims);
-          double x64 = 0.;
-#pragma unroll
-          for (int c = 0; c < kDims / 4; ++c) {
-            const float4 v = pc[c];
-            x64 = fma(qd[4 * c], static_cast<double>(v.x), x64);
-            x64 = fma(qd[4 * c + 1], static_cast<double>(v.y), x64);
-            x64 = fma(qd[4 * c + 2], static_cast<double>(v.z), x64);
-            x64 = fma(qd[4 * c + 3], static_cast<double>(v.w), x64);
-          }
-#pragma unroll
-          for (int o = 4; o; o >>= 1) x64 += __shfl_xor_sync(0xffffffffu, x64, o);
+          const double x64 = score64<D>(qd, pl, li[(h * 32 + mine) * 128 + r]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const double y = __shfl_sync(0xffffffffu, x64, k * 8);
@@ -1027,68 +1154,7 @@ __global__ void __launch_bounds__(kMmaSelThreads, 2)
   __syncthreads();
   const bool fine = !*abort;
   if (fine && S->hard && warp < 4) {
-    // Such rows, one at a time: every free candidate in fp64 (a lane each) where
-    // the lists were, the m-th best by bisection.
-    double* ex = reinterpret_cast<double*>(lv);
-    for (int w = 0; w < 4; ++w) {
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (warp != w) continue;
-      unsigned todo = __ballot_sync(0xffffffffu, hard);
-      while (todo) {
-        const int src = __ffs(todo) - 1, r = (warp << 5) + src;
-        todo &= todo - 1;
-        const int lo_c = __shfl_sync(0xffffffffu, cd.lo, src), hi_c = __shfl_sync(0xffffffffu, cd.hi, src);
-        const int nc = __shfl_sync(0xffffffffu, cd.nc, src), mr = __shfl_sync(0xffffffffu, m, src);
-        unsigned long long lo = ~0ull, hi = 0ull;
-        auto key = [](double x) {
-          const unsigned long long u = x == 0. ? 0ull : __double_as_longlong(x);
-          return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
-        };
-        for (int c = lo_c + lane; c < hi_c; c += 32) {
-          double x = 0.;
-          for (int d = 0; d < D; ++d) {
-            double a = 0.;
-            for (int g = 0; g < p.G; ++g)
-              a += static_cast<double>(bf16_to_f32(qh[g * head + static_cast<size_t>(t0 + r) * D + d]));
-            x = fma(a, static_cast<double>(pool[(static_cast<size_t>(blockIdx.y) * p.nb + c) * D + d]), x);
-          }
-          ex[c] = x;
-          lo = min(lo, key(x));
-          hi = max(hi, key(x));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        __syncwarp();
-        while (lo < hi) {
-          const unsigned long long mid = lo + (hi - lo) / 2 + 1;
-          int k = 0;
-          for (int c = lo_c + lane; c < hi_c; c += 32) k += key(ex[c]) >= mid;
-          k = __reduce_add_sync(0xffffffffu, k);
-          if (k >= mr) lo = mid;
-          else hi = mid - 1;
-        }
-        int over = 0;
-        for (int c = lo_c + lane; c < hi_c; c += 32) over += key(ex[c]) > lo;
-        over = __reduce_add_sync(0xffffffffu, over);
-        int equal = 0, at = 0;
-        for (int c0 = 0; c0 < nc; c0 += 32) {
-          const int c = c0 + lane;
-          const bool forced = c < nc && (c < lo_c || c >= hi_c), open = c < nc && !forced;
-          const unsigned eq = __ballot_sync(0xffffffffu, open && key(ex[c]) == lo);
-          const bool take = forced || (open && (key(ex[c]) > lo || (((eq >> lane) & 1u) &&
-                                                                    equal + __popc(eq & ((1u << lane) - 1u)) < mr - over)));
-          equal += __popc(eq);
-          const unsigned bal = __ballot_sync(0xffffffffu, take);
-          const int to = at + __popc(bal & ((1u << lane) - 1u));
-          if (take && to < p.n_sel) ids[r * p.n_sel + to] = c;
-          at += __popc(bal);
-        }
-        __syncwarp();
-      }
-    }
+    rows_in_fp64<D>(qh + static_cast<size_t>(t0) * D, p.G, head, pl, p.nb, p.n_sel, hard, cd, m, lv, ids);
   }
   __syncthreads();
   if (fine) {
