@@ -811,7 +811,10 @@ def block_attention(q, k, v, cfg: BlockConfig, lengths=None, q_start: Optional[i
     """The whole path on the current stream: block means -> selection -> attention over the selected
     blocks. q: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lengths: int32 [B], the valid keys of a
     right-padded batch; q_start as in block_select. Differentiable in q, k and v (the selection is a
-    constant of the gradient; the gradient's gradient and forward-mode gradients are not offered).
+    constant of the gradient; the gradient's gradient and forward-mode gradients are not offered). fp32
+    softmax and sums; P and dS in bf16 for the second products (svoo_block_attn_backward says which).
+    Where neighbouring queries select nearly all blocks, blocks of 128 keys and multiples, a call takes
+    a workspace of 4 * (d + 2) bytes for every query's 128 selected keys, up to 4.5 GB.
     Returns (o, dict(idx, lse, pool, dev_err))."""
     if _has_tangent(q, k, v):
         raise SvooError("block_attention has no forward-mode gradient")

@@ -391,7 +391,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
 // ------------------------------------------------------------------ dk, dv
 
-constexpr int kDkvLoaders = 256;  // threads; 128 of them took longer to issue a tile's 64 KB (585 us against 551, as below)
+// threads; 128 of them took longer to issue a tile's 64 KB (585 us against 551 for the case below, which 32-bit row
+// numbers then brought to 526)
+constexpr int kDkvLoaders = 256;
 constexpr int kDkvThreads = 256 + kDkvLoaders + 32;  // warps 0-3, 4-7: dS of even / odd row tiles; 8-15: loads; 16: MMA issuer
 constexpr int kDkvIssuer = kDkvThreads / 32 - 1;
 

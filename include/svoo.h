@@ -309,10 +309,11 @@ svoo_status svoo_snr_top_p(int steps, int warmup, double p_min, double tau, doub
  *  (the queries are the last Nq tokens of their sequence). Causal: a query sees
  *  the keys up to its own position, and nothing when its position is outside
  *  [0, lengths[b]). Not causal: every query sees all keys of its sequence.
- *  Limits: 1 <= H / Hkv <= 128, B*H <= 65535, 0 <= Nq, 1 <= Nk <= cap <= 2^20,
- *  B*H*Nq and B*Hkv*cap < 2^31 - 256, d in {64, 128}, block a multiple of 64
- *  up to 1024, 1 <= n_sel <= 256, sink + local <= n_sel, local >= 1 when causal
- *  and 0 when not. Valid rows of q, k, v must be finite. */
+ *  Limits: 1 <= H / Hkv <= 128, B*H <= 65535, 0 <= Nq <= 2^20,
+ *  1 <= Nk <= cap <= 2^20, B*H*Nq and B*Hkv*cap < 2^31 - 256, d in {64, 128},
+ *  block a multiple of 64 up to 1024, 1 <= n_sel <= 256, sink + local <= n_sel,
+ *  local >= 1 when causal and 0 when not, -1 <= q_start <= 2^20. Valid rows of
+ *  q, k, v must be finite. */
 typedef struct {
     int B, H, Hkv;
     int Nq, Nk, cap;
@@ -336,7 +337,7 @@ svoo_status svoo_block_pool(const svoo_block_shape *shape, const void *k, const 
 /* idx: int32 [B][Hkv][Nq][n_sel], ascending block ids, then -1. The forced
  * blocks and the best of the others by
  *   score(t, c) = (sum over the group's heads of q[t]) . pool[c],
- * equal scores to the lower block; decided as in fp64. Causal: the blocks up to
+ * equal scores to the lower block; decided as in fp64 for all finite q and pool. Causal: the blocks up to
  * the query's own, which is always kept and never scored. A query outside its
  * sequence selects nothing. The workspace (256-byte aligned; a call of few
  * queries needs none, 0 bytes) must not be shared by calls that overlap on the
@@ -366,8 +367,12 @@ svoo_status svoo_block_attn(const svoo_block_shape *shape, const void *q, const 
 /* Gradient of svoo_block_attn with respect to q, k and v (the selection is a
  * constant): dq bf16 [B][H][Nq][d]; dk, dv bf16 [B][Hkv][Nk][d], contiguous
  * whatever cap is, zero for keys that no query attends to. o, lse: what the
- * forward call wrote. grad_o: bf16 [B][H][Nq][d]. Every sum runs in a fixed
- * order, so equal calls give equal bits. The workspace (256-byte aligned) must
+ * forward call wrote. grad_o: bf16 [B][H][Nq][d]. fp32 sums; P and dS are
+ * rounded to bf16 for the products of dv and dk, dS enters dq's as two bf16
+ * parts, rowsum(grad_o * o) is taken from the rounded o: with the outputs' own
+ * rounding some 2.5e-3 of the formula in the 2-norm, and where terms cancel (a
+ * query of one key) the error goes by the terms, not by their sum. Every sum
+ * runs in a fixed order, so equal calls give equal bits. The workspace (256-byte aligned) must
  * not be shared by calls that overlap on the GPU. */
 size_t svoo_block_attn_backward_workspace_size(const svoo_block_shape *shape);
 svoo_status svoo_block_attn_backward(const svoo_block_shape *shape, const void *q, const void *k,
@@ -379,6 +384,8 @@ svoo_status svoo_block_attn_backward(const svoo_block_shape *shape, const void *
 /* One token per sequence (Nq = 1) over a cache of cap slots, all valid ones
  * visible (the order of the slots does not matter; causal and q_start are not
  * used): o bf16 [B][H][1][d], lse fp32 [B][H][1].
+ * fp32 softmax and sums; P is rounded to bf16 for the second product, weights
+ * are not.
  *  idx (int32 [B][Hkv][1][n_sel], may be NULL): only the slots of those blocks.
  *  weight (fp32 [B][Hkv][cap], may be NULL): weight[slot] += sum over the
  *  group's heads of the slot's softmax weight, for every valid slot. A call that
